@@ -369,6 +369,156 @@ MOE_API int moe_forward_noalloc(const moe_shape* shape,
                 const uint8_t* w2, const uint8_t* w2_sf,
                 uint16_t* y, void* stream);
 
+/* ---- in front of the experts: norm, router product, gate ----------------------
+ * What an MoE layer computes between the previous layer's output and
+ * moe_forward.  Used together:
+ *   moe_norm_quant     h = x + residual; y = RMSNorm(h) as BF16 for the
+ *                      router, and as E4M3 + UE8M0 (moe_forward's x, x_sf)
+ *   moe_router_logits  logits = y W^T
+ *   moe_gate           logits -> topk_idx, topk_w (moe_plan's and
+ *                      moe_forward's inputs)
+ * The library is a forward with FP4 experts, so none of them has a backward.
+ * The conventions at the top of this file hold (validation order: NULL
+ * shape, shape limits and divisibility, NULL pointers, alignment, workspace
+ * size, architecture), except that rows of the inputs may be strided: a
+ * stride is the number of ELEMENTS from one row to the next, 0 means
+ * contiguous rows. */
+
+/* Element types of the inputs below. */
+enum moe_dtype {
+    MOE_BF16 = 0,
+    MOE_F32 = 1
+};
+
+/* Residual addition, RMS norm and quantisation of one row per token:
+ *   h      = x + residual            (FP32; h = x without a residual)
+ *   v      = h / sqrt(mean(h^2) + eps) * weight
+ *   residual_out = h                 rounded to residual_type
+ *   y      = v                       rounded to BF16
+ *   x_q, x_sf = v in blocks of 32 columns: scale 2^s, the smallest power of
+ *            two with max|v| / 2^s <= 448 (s in [-127, 127], -127 where all
+ *            of the block is 0), x_sf = s + 127, x_q = E4M3(v / 2^s).
+ * The norm and both outputs come from h before its rounding to
+ * residual_type.  The mean is summed in 64 bits, v is computed in 32, and
+ * the scale is the one of the formula also where max|v| rounds across
+ * 448 * 2^s in 32 bits.  A NaN in a row makes the row's v NaN (E4M3 code
+ * 0x7F or 0xFF); an infinite element becomes NaN and the others of its row 0;
+ * a row of zeros with eps = 0 is NaN.
+ * Limits (else MOE_ERR_SHAPE, or MOE_ERR_ALIGN for the divisibility rules):
+ *   num_tokens >= 0; hidden 32 .. 2^20, a multiple of 32; eps finite, >= 0;
+ *   strides >= hidden and multiples of 8 elements.
+ * x, residual, residual_out, weight, y and x_q: 16-byte aligned. */
+typedef struct moe_norm_shape {
+    int64_t x_stride;
+    int64_t residual_stride;
+    int64_t residual_out_stride;
+    int32_t num_tokens;
+    int32_t hidden;
+    int32_t x_type;         /* of x: MOE_BF16 or MOE_F32 */
+    int32_t residual_type;  /* of residual and residual_out */
+    int32_t weight_type;
+    float eps;
+} moe_norm_shape;
+/*   x            [T, H] x_type
+ *   residual     [T, H] residual_type, or NULL
+ *   weight       [H] weight_type
+ *   residual_out [T, H] residual_type, or NULL.  May be residual itself
+ *                (same stride), or x itself where type and stride agree;
+ *                no other overlap of outputs and inputs is allowed.
+ *   y            [T, H] BF16, or NULL
+ *   x_q, x_sf    uint8 [T, H] and [T, H/32], or both NULL
+ * At least one of y and x_q must be given. */
+MOE_API int moe_norm_quant(const moe_norm_shape* shape, const void* x, const void* residual,
+                const void* weight, void* residual_out, uint16_t* y,
+                uint8_t* x_q, uint8_t* x_sf, void* stream);
+
+/* Router product: logits[t, e] = sum over k of x[t, k] * w[e, k], in FP32.
+ * Products are exact in FP32 and sums are held in FP32, for FP32 weights too
+ * (a weight is split into three BF16 parts, 8 bits each).
+ * Limits: num_tokens >= 0; hidden 32 .. 2^20, a multiple of 32; num_experts
+ * 1 .. 1024 (all ranks' experts); x_stride >= hidden and a multiple of 8. */
+typedef struct moe_router_shape {
+    int64_t x_stride;
+    int32_t num_tokens;
+    int32_t hidden;
+    int32_t num_experts;
+    int32_t weight_type;    /* MOE_BF16 or MOE_F32 */
+} moe_router_shape;
+
+/* One-time re-layout of the router weights (num_tokens and x_stride are
+ * ignored).  P = 1 for BF16, 3 for FP32:
+ *   w_tiled [ceil(E/16)][H/32][P][64 lanes][8] BF16: lane l of a block holds
+ *   expert 16 * block + l % 16 (zeros past the last expert), columns
+ *   32 * step + 8 * (l / 16) .. + 8; part p of an FP32 weight is BF16(w - the
+ *   parts before it).  FP32 weights that are not finite give NaN logits, and
+ *   those below 2^-110 in magnitude may lose low bits.
+ * w [E, H] contiguous; w_tiled of moe_router_weight_bytes; both 16-byte
+ * aligned, not overlapping. */
+MOE_API int moe_router_weight_bytes(const moe_router_shape* shape, size_t* bytes);
+MOE_API int moe_router_prepare(const moe_router_shape* shape, const void* w, uint8_t* w_tiled, void* stream);
+
+/* Bytes of moe_router_logits' workspace (partial sums); may be 0, and then
+ * ws may be NULL. */
+MOE_API int moe_router_workspace_bytes(const moe_router_shape* shape, size_t* bytes);
+
+/*   x        [T, H] BF16 (moe_norm_quant's y)
+ *   w_tiled  from moe_router_prepare for the same hidden, num_experts and
+ *            weight_type
+ *   logits   float [T, E], 16-byte aligned
+ *   ws       any initial contents, 256-byte aligned */
+MOE_API int moe_router_logits(const moe_router_shape* shape, const uint16_t* x, const uint8_t* w_tiled,
+                float* logits, void* ws, size_t ws_bytes, void* stream);
+
+/* Gate: the top-k experts of every token and their weights.
+ *   score s[e]  MOE_SCORE_SOFTMAX: exp(l[e]) / sum over e of exp(l[e]);
+ *               MOE_SCORE_SIGMOID: 1 / (1 + exp(-l[e]))
+ *   order c[e]  s[e] + bias[e]; without a bias the logit l[e] itself
+ *   groups      with num_groups > 1 the experts form groups of
+ *               num_experts / num_groups neighbours.  A group's mark is its
+ *               largest c (MOE_GROUP_MAX) or the sum of its two largest c
+ *               (MOE_GROUP_TOP2; of s without a bias); only the experts of
+ *               the topk_groups groups with the largest marks are candidates.
+ *   topk_idx    the candidates with the largest c, in falling order
+ *   topk_w      s of those, divided by their sum if renormalize is set (all
+ *               0 where that sum is 0), times scale
+ * Ties, of experts and of groups, go to the lowest index.  Scores, sums and
+ * comparisons hold in 64 bits wherever they decide an order.
+ * An expert whose logit or c is -infinity is never chosen; a row with fewer
+ * than topk candidates ends in entries of id -1 and weight 0, which
+ * moe_plan drops (a padding row is a row of -infinities).  NaN ranks above
+ * every number, and its weight is NaN; a softmax row with a NaN or +infinity
+ * has NaN weights throughout.
+ * Limits: num_tokens >= 0, T * topk < 2^30; num_experts 1 .. 1024; topk 1 ..
+ * min(64, num_experts / num_groups * topk_groups); num_groups a divisor of
+ * num_experts, at most 64; topk_groups 1 .. num_groups; scale finite;
+ * logits_stride >= num_experts. */
+enum moe_score {
+    MOE_SCORE_SOFTMAX = 0,
+    MOE_SCORE_SIGMOID = 1
+};
+enum moe_group_score {
+    MOE_GROUP_MAX = 0,
+    MOE_GROUP_TOP2 = 1
+};
+typedef struct moe_gate_shape {
+    int64_t logits_stride;
+    int32_t num_tokens;
+    int32_t num_experts;    /* all ranks' experts */
+    int32_t topk;
+    int32_t num_groups;     /* 1: no groups */
+    int32_t topk_groups;
+    int32_t score;          /* moe_score */
+    int32_t group_score;    /* moe_group_score */
+    int32_t renormalize;    /* 0 or 1 */
+    float scale;
+    int32_t logits_type;    /* MOE_BF16 or MOE_F32 */
+} moe_gate_shape;
+/*   logits   [T, E] logits_type, aligned to its element
+ *   bias     float [E] (4-byte aligned), or NULL
+ *   topk_idx int64 [T, k], topk_w float [T, k] */
+MOE_API int moe_gate(const moe_gate_shape* shape, const void* logits, const float* bias,
+                int64_t* topk_idx, float* topk_w, void* stream);
+
 /* MOE_OK if `device` is a gfx950 GPU, MOE_ERR_ARCH if not, MOE_ERR_HIP if
  * the runtime cannot be queried. */
 MOE_API int moe_device_supported(int device);

@@ -19,6 +19,9 @@ STATUS = {0: "ok", -1: "null pointer", -2: "unsupported shape", -3: "misaligned 
           -7: "weights not declared in the tiled layout"}
 
 WEIGHTS_PLAIN, WEIGHTS_TILED = 0, 1   # moe_shape.weight_layout
+DTYPES = {torch.bfloat16: 0, torch.float32: 1}   # moe_dtype
+SCORES = {"softmax": 0, "sigmoid": 1}            # moe_score
+GROUP_SCORES = {"max": 0, "top2": 1}             # moe_group_score
 
 
 class MoeError(RuntimeError):
@@ -32,6 +35,24 @@ class MoeShape(ctypes.Structure):
                 ("num_experts", ctypes.c_int32), ("expert_begin", ctypes.c_int32), ("topk", ctypes.c_int32),
                 ("block_m", ctypes.c_int32), ("swiglu_limit", ctypes.c_float), ("exact_silu", ctypes.c_int32),
                 ("weight_layout", ctypes.c_int32)]
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("x_stride", "residual_stride", "residual_out_stride")] + \
+               [(n, ctypes.c_int32) for n in ("num_tokens", "hidden", "x_type", "residual_type", "weight_type")] + \
+               [("eps", ctypes.c_float)]
+
+
+class RouterShape(ctypes.Structure):
+    _fields_ = [("x_stride", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("num_tokens", "hidden", "num_experts", "weight_type")]
+
+
+class GateShape(ctypes.Structure):
+    _fields_ = [("logits_stride", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("num_tokens", "num_experts", "topk", "num_groups", "topk_groups", "score",
+                                              "group_score", "renormalize")] + \
+               [("scale", ctypes.c_float), ("logits_type", ctypes.c_int32)]
 
 
 class PlanView(ctypes.Structure):
@@ -50,6 +71,8 @@ _lib = None
 EXPORTS = ["moe_capacity_rows", "moe_suggest_block_m", "moe_gemm_launches", "moe_plan_workspace_bytes", "moe_plan", "moe_plan_view_get",
            "moe_forward_workspace_bytes", "moe_forward", "moe_linear1", "moe_linear2", "moe_combine",
            "moe_expert_ffn", "moe_prepare_weights", "moe_forward_noalloc",
+           "moe_norm_quant", "moe_router_weight_bytes", "moe_router_prepare", "moe_router_workspace_bytes",
+           "moe_router_logits", "moe_gate",
            "moe_forward_view_get", "moe_device_supported", "moe_status_str"]
 
 
@@ -77,6 +100,13 @@ def lib() -> ctypes.CDLL:
         L.moe_combine.argtypes = [S, VP, VP, SZ, VP, VP]
         L.moe_expert_ffn.argtypes = [S, VP, VP, VP, VP, VP, VP, VP, VP, VP, SZ, VP]
         L.moe_forward_view_get.argtypes = [S, VP, P(ForwardView)]
+        N, R, G = P(NormShape), P(RouterShape), P(GateShape)
+        L.moe_norm_quant.argtypes = [N, VP, VP, VP, VP, VP, VP, VP, VP]
+        L.moe_router_weight_bytes.argtypes = [R, P(SZ)]
+        L.moe_router_prepare.argtypes = [R, VP, VP, VP]
+        L.moe_router_workspace_bytes.argtypes = [R, P(SZ)]
+        L.moe_router_logits.argtypes = [R, VP, VP, VP, VP, SZ, VP]
+        L.moe_gate.argtypes = [G, VP, VP, VP, VP, VP]
         L.moe_device_supported.argtypes = [ctypes.c_int]
         L.moe_status_str.argtypes = [ctypes.c_int]
         L.moe_status_str.restype = ctypes.c_char_p
@@ -350,3 +380,124 @@ def forward_view(shape: MoeShape, ws: torch.Tensor) -> dict:
             "yslot": _slice(ws, v.yslot, torch.int16, cap * H).view(cap, H),
             "plan_ws": ws[plan_off:], "capacity_rows": cap,
             "sync_status": _slice(ws, v.sync_status, torch.int32, 1)}
+
+
+# ---- in front of the experts: norm, router product, gate
+
+def make_norm(num_tokens, hidden, eps=1e-6, x_dtype=torch.bfloat16, residual_dtype=torch.bfloat16,
+              weight_dtype=torch.bfloat16, x_stride=0, residual_stride=0, residual_out_stride=0) -> NormShape:
+    """A moe_norm_shape.  Strides are elements from one row to the next, 0 for contiguous rows."""
+    return NormShape(x_stride, residual_stride, residual_out_stride, num_tokens, hidden, DTYPES[x_dtype],
+                     DTYPES[residual_dtype], DTYPES[weight_dtype], float(eps))
+
+
+def make_router(num_tokens, hidden, num_experts, weight_dtype=torch.bfloat16, x_stride=0) -> RouterShape:
+    """A moe_router_shape; num_experts counts all ranks' experts."""
+    return RouterShape(x_stride, num_tokens, hidden, num_experts, DTYPES[weight_dtype])
+
+
+def make_gate(num_tokens, num_experts, topk, score="softmax", num_groups=1, topk_groups=1, group_score="max",
+              renormalize=True, scale=1.0, logits_dtype=torch.float32, logits_stride=0) -> GateShape:
+    """A moe_gate_shape; num_experts counts all ranks' experts."""
+    return GateShape(logits_stride, num_tokens, num_experts, topk, num_groups, topk_groups, SCORES[score],
+                     GROUP_SCORES[group_score], int(bool(renormalize)), float(scale), DTYPES[logits_dtype])
+
+
+def _dtype(code):
+    return next(t for t, c in DTYPES.items() if c == code)
+
+
+def _rows(t, dtype, name, device, rows, cols, stride):
+    """Pointer of a [rows, cols] tensor whose rows lie `stride` elements apart (0: cols)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name}: expected shape {(rows, cols)}, got {tuple(t.shape)}")
+    if rows and (t.stride(1) != 1 and cols > 1 or t.stride(0) != (stride or cols) and rows > 1):
+        raise ValueError(f"{name}: expected strides {(stride or cols, 1)}, got {t.stride()}")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _here(t, name):
+    """The device of `t`, which has to be the current one: the library launches there."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _bf16(t, name, device, numel):
+    """Pointer of a contiguous BF16 tensor, given as bfloat16 or as its int16 bits."""
+    if t is not None and t.dtype == torch.bfloat16 and t.is_contiguous():
+        t = t.view(torch.int16)
+    return _ptr(t, torch.int16, name, device, numel)
+
+
+def norm_quant(shape: NormShape, x, weight, x_q=None, x_sf=None, y=None, residual=None, residual_out=None,
+               stream=None, bind=False):
+    """moe_norm_quant: residual_out = x + residual, y = RMSNorm(x + residual) * weight as BF16 and, in x_q and
+    x_sf, as E4M3 with UE8M0 scales; bind=True: return the call as a Bound."""
+    T, H, u8 = shape.num_tokens, shape.hidden, torch.uint8
+    dev = _here(x, "x")
+    rt = _dtype(shape.residual_type)
+    args = [_rows(x, _dtype(shape.x_type), "x", dev, T, H, shape.x_stride),
+            _rows(residual, rt, "residual", dev, T, H, shape.residual_stride),
+            _ptr(weight, _dtype(shape.weight_type), "weight", dev, H),
+            _rows(residual_out, rt, "residual_out", dev, T, H, shape.residual_out_stride),
+            _bf16(y, "y", dev, T * H), _ptr(x_q, u8, "x_q", dev, T * H), _ptr(x_sf, u8, "x_sf", dev, T * H // 32)]
+    return _call("moe_norm_quant", shape, args, (x, weight, x_q, x_sf, y, residual, residual_out), stream, bind)
+
+
+def router_weight_bytes(shape: RouterShape) -> int:
+    v = ctypes.c_size_t()
+    _check("moe_router_weight_bytes", lib().moe_router_weight_bytes(ctypes.byref(shape), ctypes.byref(v)))
+    return v.value
+
+
+def router_workspace_bytes(shape: RouterShape) -> int:
+    v = ctypes.c_size_t()
+    _check("moe_router_workspace_bytes", lib().moe_router_workspace_bytes(ctypes.byref(shape), ctypes.byref(v)))
+    return v.value
+
+
+def router_prepare(shape: RouterShape, w, stream=None) -> torch.Tensor:
+    """moe_router_prepare: tiled copy (a new tensor) of the router weights w [num_experts, hidden]."""
+    dev = _here(w, "w")
+    out = torch.empty(router_weight_bytes(shape), dtype=torch.uint8, device=dev)
+    p = _ptr(w, _dtype(shape.weight_type), "w", dev, shape.num_experts * shape.hidden)
+    _check("moe_router_prepare", lib().moe_router_prepare(ctypes.byref(shape), p, _ptr(out, torch.uint8, "w_tiled"),
+                                                          _stream(stream)))
+    return out
+
+
+def router_logits(shape: RouterShape, x, w_tiled, logits, ws=None, stream=None, bind=False):
+    """moe_router_logits: logits = x W^T in FP32, W prepared by router_prepare; bind=True: return the call as a
+    Bound.  ws may be None where router_workspace_bytes is 0."""
+    T, H, E = shape.num_tokens, shape.hidden, shape.num_experts
+    dev = _here(x, "x")
+    args = [_rows(x, torch.bfloat16, "x", dev, T, H, shape.x_stride),
+            _ptr(w_tiled, torch.uint8, "w_tiled", dev, router_weight_bytes(shape)),
+            _ptr(logits, torch.float32, "logits", dev, T * E),
+            _ptr(ws, torch.uint8, "ws", dev), 0 if ws is None else ws.numel()]
+    return _call("moe_router_logits", shape, args, (x, w_tiled, logits, ws), stream, bind)
+
+
+def gate(shape: GateShape, logits, topk_idx, topk_w, bias=None, stream=None, bind=False):
+    """moe_gate: topk_idx and topk_w of every row of logits; bind=True: return the call as a Bound."""
+    T, E, k = shape.num_tokens, shape.num_experts, shape.topk
+    dev = _here(logits, "logits")
+    args = [_rows(logits, _dtype(shape.logits_type), "logits", dev, T, E, shape.logits_stride),
+            _ptr(bias, torch.float32, "bias", dev, E), _ptr(topk_idx, torch.int64, "topk_idx", dev, T * k),
+            _ptr(topk_w, torch.float32, "topk_w", dev, T * k)]
+    return _call("moe_gate", shape, args, (logits, bias, topk_idx, topk_w), stream, bind)

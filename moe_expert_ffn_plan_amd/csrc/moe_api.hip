@@ -384,3 +384,143 @@ int moe_forward_noalloc(const moe_shape* shape, const uint8_t* x, const uint8_t*
 }
 
 }  // extern "C"
+
+// ---- in front of the experts
+namespace {
+
+bool type_ok(int t) { return t == MOE_BF16 || t == MOE_F32; }
+bool flag_ok(int v) { return v == 0 || v == 1; }
+
+// A stride as given (0 = contiguous) against the row length; vectors of 8 elements start every row.
+int check_stride(int64_t stride, int64_t row) {
+    if (stride == 0) return MOE_OK;
+    if (stride < row || stride > (1ll << 40)) return MOE_ERR_SHAPE;
+    return stride % 8 == 0 ? MOE_OK : MOE_ERR_ALIGN;
+}
+int64_t stride_or(int64_t stride, int64_t row) { return stride ? stride : row; }
+
+int check_hidden(int h) {
+    if (h <= 0 || h > kMaxHidden) return MOE_ERR_SHAPE;
+    return h % 32 == 0 ? MOE_OK : MOE_ERR_ALIGN;
+}
+
+int check_norm(const moe_norm_shape* s) {
+    if (!s) return MOE_ERR_NULL;
+    if (s->num_tokens < 0 || !type_ok(s->x_type) || !type_ok(s->residual_type) || !type_ok(s->weight_type))
+        return MOE_ERR_SHAPE;
+    if (!(s->eps >= 0.0f && s->eps <= 3.0e38f)) return MOE_ERR_SHAPE;  // also rejects NaN
+    int st = check_hidden(s->hidden);
+    for (const int64_t stride : {s->x_stride, s->residual_stride, s->residual_out_stride})
+        if (st == MOE_OK) st = check_stride(stride, s->hidden);
+    return st;
+}
+
+int check_router(const moe_router_shape* s) {
+    if (!s) return MOE_ERR_NULL;
+    if (s->num_tokens < 0 || !type_ok(s->weight_type)) return MOE_ERR_SHAPE;
+    if (s->num_experts < 1 || s->num_experts > kMaxGateExperts) return MOE_ERR_SHAPE;
+    const int st = check_hidden(s->hidden);
+    return st != MOE_OK ? st : check_stride(s->x_stride, s->hidden);
+}
+
+int check_gate(const moe_gate_shape* s) {
+    if (!s) return MOE_ERR_NULL;
+    if (s->num_tokens < 0 || s->num_experts < 1 || s->num_experts > kMaxGateExperts) return MOE_ERR_SHAPE;
+    if (s->num_groups < 1 || s->num_groups > kMaxGateGroups || s->num_experts % s->num_groups != 0)
+        return MOE_ERR_SHAPE;
+    if (s->topk_groups < 1 || s->topk_groups > s->num_groups) return MOE_ERR_SHAPE;
+    if (s->topk < 1 || s->topk > kMaxTopk || s->topk > s->num_experts / s->num_groups * s->topk_groups)
+        return MOE_ERR_SHAPE;
+    if ((int64_t)s->num_tokens * s->topk >= (1ll << 30)) return MOE_ERR_SHAPE;
+    if (!flag_ok(s->score) || !flag_ok(s->group_score) || !flag_ok(s->renormalize) || !type_ok(s->logits_type))
+        return MOE_ERR_SHAPE;
+    if (!(s->scale >= -3.0e38f && s->scale <= 3.0e38f)) return MOE_ERR_SHAPE;  // also rejects NaN
+    if (s->logits_stride != 0 && (s->logits_stride < s->num_experts || s->logits_stride > (1ll << 40)))
+        return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_norm_quant(const moe_norm_shape* shape, const void* x, const void* residual, const void* weight,
+                   void* residual_out, uint16_t* y, uint8_t* x_q, uint8_t* x_sf, void* stream) {
+    int st = check_norm(shape);
+    if (st != MOE_OK) return st;
+    if (shape->num_tokens == 0) return MOE_OK;
+    if (!x || !weight || (!y && !x_q) || (x_q == nullptr) != (x_sf == nullptr)) return MOE_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16) ||
+        !aligned(y, 16) || !aligned(x_q, 16))
+        return MOE_ERR_ALIGN;
+    if ((st = check_arch_current()) != MOE_OK) return st;
+    const int H = shape->hidden;
+    const NormArgs a{x, residual, weight, residual_out, y, x_q, x_sf,
+                     stride_or(shape->x_stride, H), stride_or(shape->residual_stride, H),
+                     stride_or(shape->residual_out_stride, H), shape->num_tokens, H,
+                     shape->x_type, shape->residual_type, shape->weight_type, shape->eps};
+    return launch_norm_quant(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_router_weight_bytes(const moe_router_shape* shape, size_t* bytes) {
+    if (!bytes) return MOE_ERR_NULL;
+    const int st = check_router(shape);
+    if (st != MOE_OK) return st;
+    *bytes = (size_t)((shape->num_experts + 15) / 16) * 16 * shape->hidden * 2 * router_parts(shape->weight_type);
+    return MOE_OK;
+}
+
+int moe_router_workspace_bytes(const moe_router_shape* shape, size_t* bytes) {
+    if (!bytes) return MOE_ERR_NULL;
+    const int st = check_router(shape);
+    if (st != MOE_OK) return st;
+    *bytes = router_workspace_bytes(shape->num_tokens, shape->hidden, shape->num_experts,
+                                    router_parts(shape->weight_type));
+    return MOE_OK;
+}
+
+int moe_router_prepare(const moe_router_shape* shape, const void* w, uint8_t* w_tiled, void* stream) {
+    int st = check_router(shape);
+    if (st != MOE_OK) return st;
+    if (!w || !w_tiled) return MOE_ERR_NULL;
+    if (!aligned(w, 16) || !aligned(w_tiled, 16)) return MOE_ERR_ALIGN;
+    if ((st = check_arch_current()) != MOE_OK) return st;
+    const hipError_t e = launch_router_prepare(shape->hidden, shape->num_experts, shape->weight_type, w, w_tiled,
+                                               static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_router_logits(const moe_router_shape* shape, const uint16_t* x, const uint8_t* w_tiled, float* logits,
+                      void* ws, size_t ws_bytes, void* stream) {
+    int st = check_router(shape);
+    if (st != MOE_OK) return st;
+    if (shape->num_tokens == 0) return MOE_OK;
+    const int T = shape->num_tokens, H = shape->hidden, E = shape->num_experts;
+    const int parts = router_parts(shape->weight_type);
+    const size_t need = router_workspace_bytes(T, H, E, parts);
+    if (!x || !w_tiled || !logits || (need > 0 && !ws)) return MOE_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(w_tiled, 16) || !aligned(logits, 16) || (need > 0 && !aligned(ws, kAlign)))
+        return MOE_ERR_ALIGN;
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+    if ((st = check_arch_current()) != MOE_OK) return st;
+    const RouterArgs a{x, w_tiled, logits, static_cast<float*>(ws), stride_or(shape->x_stride, H), T, H, E, parts};
+    return launch_router_logits(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_gate(const moe_gate_shape* shape, const void* logits, const float* bias, int64_t* topk_idx, float* topk_w,
+             void* stream) {
+    int st = check_gate(shape);
+    if (st != MOE_OK) return st;
+    if (shape->num_tokens == 0) return MOE_OK;
+    if (!logits || !topk_idx || !topk_w) return MOE_ERR_NULL;
+    if (!aligned(logits, shape->logits_type == MOE_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(topk_idx, 8) ||
+        !aligned(topk_w, 4))
+        return MOE_ERR_ALIGN;
+    if ((st = check_arch_current()) != MOE_OK) return st;
+    const GateArgs a{logits, bias, topk_idx, topk_w, stride_or(shape->logits_stride, shape->num_experts),
+                     shape->num_tokens, shape->num_experts, shape->topk, shape->num_groups, shape->topk_groups,
+                     shape->score, shape->group_score, shape->renormalize, shape->scale, shape->logits_type};
+    return launch_gate(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+}  // extern "C"

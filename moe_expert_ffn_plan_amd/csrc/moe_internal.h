@@ -193,4 +193,50 @@ hipError_t launch_tile_weights(int which, int N, int K, int E, const uint8_t* w,
 hipError_t launch_combine(const moe_shape& s, const uint16_t* yslot, const int32_t* slot, const uint32_t* status,
                           uint16_t* y, hipStream_t stream);
 
+// ---- in front of the experts
+constexpr int kMaxGateExperts = 1024;
+constexpr int kMaxGateGroups = 64;
+constexpr int kMaxHidden = 1 << 20;
+
+// Strides in elements, 0 already replaced by the row length.
+struct NormArgs {
+    const void* x;
+    const void* residual;   // or null
+    const void* weight;
+    void* residual_out;     // or null; may be residual or x
+    uint16_t* y;            // or null
+    uint8_t* x_q;           // or null, with x_sf
+    uint8_t* x_sf;
+    int64_t x_stride, residual_stride, residual_out_stride;
+    int T, H;
+    int x_type, residual_type, weight_type;
+    float eps;
+};
+hipError_t launch_norm_quant(const NormArgs& a, hipStream_t stream);
+
+struct RouterArgs {
+    const uint16_t* x;
+    const uint8_t* w;       // [ceil(E/16)][H/32][parts][64][8] BF16
+    float* logits;
+    float* partial;         // workspace
+    int64_t x_stride;
+    int T, H, E, parts;
+};
+inline int router_parts(int weight_type) { return weight_type == MOE_F32 ? 3 : 1; }
+size_t router_workspace_bytes(int T, int H, int E, int parts);
+hipError_t launch_router_prepare(int H, int E, int weight_type, const void* w, uint8_t* w_tiled, hipStream_t stream);
+hipError_t launch_router_logits(const RouterArgs& a, hipStream_t stream);
+
+struct GateArgs {
+    const void* logits;
+    const float* bias;      // or null
+    int64_t* topk_idx;
+    float* topk_w;
+    int64_t stride;
+    int T, E, k, groups, topk_groups, score, group_score, renorm;
+    float scale;
+    int logits_type;
+};
+hipError_t launch_gate(const GateArgs& a, hipStream_t stream);
+
 }  // namespace moe

@@ -1,0 +1,178 @@
+"""Argument checks of the norm, router and gate calls: the C ABI's statuses and the binding's errors (no GPU)."""
+import ctypes
+
+import pytest
+import torch
+
+from moe_expert_ffn_plan_amd import binding as B
+
+FAKE = ctypes.c_void_p(0x10000)
+ODD = ctypes.c_void_p(0x10008)       # 8-byte aligned only
+
+
+def norm(shape, x=FAKE, residual=None, weight=FAKE, residual_out=None, y=FAKE, x_q=FAKE, x_sf=FAKE):
+    return B.lib().moe_norm_quant(ctypes.byref(shape), x, residual, weight, residual_out, y, x_q, x_sf, None)
+
+
+NORM = dict(num_tokens=4, hidden=256)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(num_tokens=-1), -2), (dict(hidden=0), -2), (dict(hidden=-32), -2), (dict(hidden=(1 << 20) + 32), -2),
+    (dict(hidden=48), -3), (dict(hidden=33), -3), (dict(eps=-1e-6), -2), (dict(eps=float("nan")), -2),
+    (dict(eps=float("inf")), -2), (dict(x_stride=255), -2), (dict(x_stride=-256), -2), (dict(x_stride=260), -3),
+    (dict(residual_stride=128), -2), (dict(residual_stride=257), -3), (dict(residual_out_stride=250), -2),
+    (dict(residual_out_stride=258), -3), (dict(x_stride=1 << 41), -2)])
+def test_norm_shapes(change, status):
+    assert norm(B.make_norm(**{**NORM, **change})) == status
+
+
+@pytest.mark.parametrize("field", ["x_type", "residual_type", "weight_type"])
+def test_norm_types(field):
+    for bad in (-1, 2):
+        s = B.make_norm(**NORM)
+        setattr(s, field, bad)
+        assert norm(s) == -2
+
+
+def test_norm_pointers():
+    s = B.make_norm(**NORM)
+    assert B.lib().moe_norm_quant(None, FAKE, None, FAKE, None, FAKE, FAKE, FAKE, None) == -1
+    assert norm(s, x=None) == -1 and norm(s, weight=None) == -1
+    assert norm(s, y=None, x_q=None, x_sf=None) == -1           # nothing to write
+    assert norm(s, x_q=None) == -1 and norm(s, x_sf=None) == -1  # one without the other
+    for name in ("x", "residual", "weight", "residual_out", "y", "x_q"):
+        assert norm(s, **{name: ODD}) == -3, name
+    assert norm(B.make_norm(0, 256), x=None, weight=None, y=None, x_q=None, x_sf=None) == 0
+
+
+def router(shape, x=FAKE, w=FAKE, logits=FAKE, ws=FAKE, ws_bytes=1 << 40):
+    return B.lib().moe_router_logits(ctypes.byref(shape), x, w, logits, ws, ws_bytes, None)
+
+
+ROUTER = dict(num_tokens=4, hidden=256, num_experts=8)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(num_tokens=-1), -2), (dict(hidden=0), -2), (dict(hidden=100), -3), (dict(hidden=(1 << 20) + 32), -2),
+    (dict(num_experts=0), -2), (dict(num_experts=1025), -2), (dict(x_stride=200), -2), (dict(x_stride=257), -3)])
+def test_router_shapes(change, status):
+    s = B.make_router(**{**ROUTER, **change})
+    assert router(s) == status
+    v = ctypes.c_size_t()
+    assert B.lib().moe_router_weight_bytes(ctypes.byref(s), ctypes.byref(v)) == status
+    assert B.lib().moe_router_workspace_bytes(ctypes.byref(s), ctypes.byref(v)) == status
+    assert B.lib().moe_router_prepare(ctypes.byref(s), FAKE, FAKE, None) == status
+
+
+def test_router_pointers():
+    s = B.make_router(**ROUTER)
+    lib = B.lib()
+    assert lib.moe_router_logits(None, FAKE, FAKE, FAKE, FAKE, 0, None) == -1
+    assert lib.moe_router_weight_bytes(ctypes.byref(s), None) == -1
+    assert lib.moe_router_workspace_bytes(ctypes.byref(s), None) == -1
+    assert lib.moe_router_prepare(ctypes.byref(s), None, FAKE, None) == -1
+    assert lib.moe_router_prepare(ctypes.byref(s), FAKE, None, None) == -1
+    assert lib.moe_router_prepare(ctypes.byref(s), ODD, FAKE, None) == -3
+    for name in ("x", "w", "logits"):
+        assert router(s, **{name: None}) == -1 and router(s, **{name: ODD}) == -3, name
+    bad = B.make_router(**ROUTER)
+    bad.weight_type = 2
+    assert router(bad) == -2
+    assert router(B.make_router(0, 256, 8), x=None, w=None, logits=None, ws=None, ws_bytes=0) == 0
+
+
+def test_router_workspace():
+    """Every shape that needs a workspace refuses one that is missing, misaligned or a byte short."""
+    seen = 0
+    for T in (1, 64, 128, 1000, 4096, 65536):
+        for weight in (torch.bfloat16, torch.float32):
+            s = B.make_router(T, 7168, 256, weight_dtype=weight)
+            need = B.router_workspace_bytes(s)
+            if need == 0:
+                continue
+            seen += 1
+            assert router(s, ws=None) == -1
+            assert router(s, ws=ODD) == -3
+            assert router(s, ws_bytes=need - 1) == -4
+    print(f"{seen} shapes with a workspace")
+
+
+def test_router_weight_bytes():
+    assert B.router_weight_bytes(B.make_router(1, 64, 8)) == 16 * 64 * 2
+    assert B.router_weight_bytes(B.make_router(1, 64, 17, weight_dtype=torch.float32)) == 32 * 64 * 6
+
+
+def gate(shape, logits=FAKE, bias=None, ids=FAKE, w=FAKE):
+    return B.lib().moe_gate(ctypes.byref(shape), logits, bias, ids, w, None)
+
+
+GATE = dict(num_tokens=4, num_experts=32, topk=4)
+
+
+@pytest.mark.parametrize("change", [
+    dict(num_tokens=-1), dict(num_experts=0), dict(num_experts=1025), dict(topk=0), dict(topk=33),
+    dict(num_experts=128, topk=65), dict(num_groups=0), dict(num_groups=5), dict(num_groups=128, num_experts=1024),
+    dict(num_groups=4, topk_groups=0), dict(num_groups=4, topk_groups=5), dict(num_groups=16, topk_groups=1),
+    dict(num_tokens=1 << 28, topk=4), dict(scale=float("nan")), dict(scale=float("inf")), dict(logits_stride=31),
+    dict(logits_stride=-32)])
+def test_gate_shapes(change):
+    assert gate(B.make_gate(**{**GATE, **change})) == -2
+
+
+@pytest.mark.parametrize("field", ["score", "group_score", "renormalize", "logits_type"])
+def test_gate_switches(field):
+    for bad in (-1, 2):
+        s = B.make_gate(**GATE)
+        setattr(s, field, bad)
+        assert gate(s) == -2
+
+
+def test_gate_pointers():
+    s = B.make_gate(**GATE)
+    assert B.lib().moe_gate(None, FAKE, None, FAKE, FAKE, None) == -1
+    assert gate(s, logits=None) == -1 and gate(s, ids=None) == -1 and gate(s, w=None) == -1
+    at = lambda a: ctypes.c_void_p(a)  # noqa: E731
+    assert gate(s, logits=at(0x10002)) == -3 and gate(s, bias=at(0x10002)) == -3
+    assert gate(s, ids=at(0x10004)) == -3 and gate(s, w=at(0x10002)) == -3
+    assert gate(B.make_gate(**GATE, logits_dtype=torch.bfloat16), logits=at(0x10001)) == -3
+    assert gate(B.make_gate(0, 32, 4), logits=None, ids=None, w=None) == 0
+
+
+def test_binding_refuses_other_tensors():
+    """Types, shapes, strides and devices are checked before the library is called."""
+    cpu = torch.zeros(4, 256, dtype=torch.bfloat16)
+    w = torch.zeros(256, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        B.norm_quant(B.make_norm(4, 256), cpu, w, y=cpu)
+    with pytest.raises(ValueError):
+        B.router_logits(B.make_router(4, 256, 8), cpu, w, w)
+    with pytest.raises(ValueError):
+        B.gate(B.make_gate(4, 32, 4), torch.zeros(4, 32), torch.zeros(4, 4), torch.zeros(4, 4))
+    with pytest.raises(TypeError):
+        B.gate(B.make_gate(4, 32, 4), None, None, None)
+    for bad in (lambda: B.make_norm(4, 256, x_dtype=torch.float16), lambda: B.make_router(4, 256, 8, torch.float16),
+                lambda: B.make_gate(4, 32, 4, score="relu"), lambda: B.make_gate(4, 32, 4, group_score="sum")):
+        with pytest.raises(KeyError):
+            bad()
+
+
+def test_binding_row_checks(monkeypatch):
+    """Row shapes, strides and types, on tensors that only say they lie on a device."""
+    class Said(torch.Tensor):
+        is_cuda = True
+
+    dev = torch.device("cpu")
+    t = torch.zeros(4, 40).as_subclass(Said)
+    assert B._rows(t, torch.float32, "x", dev, 4, 40, 0) is not None
+    assert B._rows(t[:, :32], torch.float32, "x", dev, 4, 32, 40) is not None
+    assert B._rows(None, torch.float32, "x", dev, 4, 40, 0) is None
+    for args in ((torch.float32, "x", dev, 4, 32, 0), (torch.float32, "x", dev, 4, 40, 48)):
+        with pytest.raises(ValueError):
+            B._rows(t, *args)
+    with pytest.raises(ValueError):
+        B._rows(t[:, :32], torch.float32, "x", dev, 4, 32, 0)
+    with pytest.raises(ValueError):
+        B._rows(t.t(), torch.float32, "x", dev, 40, 4, 0)
+    with pytest.raises(TypeError):
+        B._rows(t, torch.bfloat16, "x", dev, 4, 40, 0)

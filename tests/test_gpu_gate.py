@@ -1,0 +1,193 @@
+"""GPU parity of moe_gate: ids equal to the float64 oracle's, weights within their roundings.
+
+Weights come from scores in 64 bits and are rounded once: 2^-24, and as much again for the exponentials'
+and the sum's own 64-bit error.  Softmax weights that are not renormalised are divided by a sum over the
+whole row that may be held in 32 bits: relative error at most 31 * 2^-24 < 2^-19 (the argument's rounding,
+weighted, at most ln(1024) < 7 times 2^-24; the exponential 2 * 2^-24; at most 22 additions).
+"""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+from moe_expert_ffn_plan_amd import binding as B
+from oracle.front import gate_ref
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+INF, NAN = float("inf"), float("nan")
+
+
+def run(logits, k, bias=None, shape=None, **kw):
+    T, E = logits.shape
+    s = shape or B.make_gate(T, E, k, logits_dtype=logits.dtype, **kw)
+    ids = torch.full((T, k), 777, dtype=torch.int64, device=logits.device)
+    w = torch.full((T, k), NAN, device=logits.device)
+    B.gate(s, logits, ids, w, bias=bias)
+    torch.cuda.synchronize()
+    return ids.cpu().numpy(), w.double().cpu().numpy()
+
+
+def check(logits, k, bias=None, **kw):
+    ids, w = run(logits, k, bias, **kw)
+    rids, rw = gate_ref(logits.double().cpu().numpy(), k, bias=None if bias is None else bias.cpu().numpy(), **kw)
+    assert np.array_equal(ids, rids)
+    whole_row = kw.get("score", "softmax") == "softmax" and not kw.get("renormalize", True)
+    tol = 2.0 ** -19 if whole_row else 2.0 ** -23
+    assert np.array_equal(np.isnan(w), np.isnan(rw))
+    fine = ~np.isnan(rw)
+    assert (np.abs(w - rw)[fine] <= tol * np.abs(rw)[fine] + 2.0 ** -140).all()
+
+
+def normal(T, E, seed, gpu, dtype=F32, scale=1.0):
+    return (torch.randn(T, E, generator=torch.Generator().manual_seed(seed)) * scale).to(dtype).to(gpu)
+
+
+def balance(E, seed, gpu):
+    return torch.randint(-100, 101, (E,), generator=torch.Generator().manual_seed(seed)).float().to(gpu) * 1e-3
+
+
+SIZES = [(1, 1, 1), (3, 2, 1), (2, 8, 2), (70, 8, 8), (5, 63, 6), (9, 64, 8), (9, 65, 8), (33, 100, 7), (130, 128, 64),
+         (4, 255, 8), (300, 256, 8), (7, 257, 1), (100, 384, 6), (3, 511, 12), (20, 512, 8), (3, 513, 5), (6, 1000, 33),
+         (5, 1024, 64)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,E,k", SIZES)
+def test_gate_sizes(gpu, T, E, k, dtype):
+    print(f"gate T={T} E={E} k={k} {dtype}", flush=True)
+    l = normal(T, E, T + E, gpu, dtype)
+    for score, renorm in itertools.product(["softmax", "sigmoid"], [True, False]):
+        check(l, k, score=score, renormalize=renorm, scale=2.5)
+        check(l, k, balance(E, 1, gpu), score=score, renormalize=renorm)
+
+
+GROUPS = [(32, 4, 2, 4), (256, 8, 4, 8), (256, 8, 1, 8), (64, 64, 5, 5), (60, 4, 3, 8), (120, 8, 2, 16), (384, 8, 3, 6),
+          (1024, 16, 4, 64), (1008, 63, 7, 10), (96, 2, 2, 4), (20, 5, 5, 20), (7, 7, 2, 1)]
+
+
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+@pytest.mark.parametrize("E,groups,kept,k", GROUPS)
+def test_gate_groups(gpu, E, groups, kept, k, group_score):
+    print(f"gate E={E} groups={groups} kept={kept} k={k} {group_score}", flush=True)
+    for score, biased, dtype in itertools.product(["softmax", "sigmoid"], [True, False], [F32, BF16]):
+        l = normal(60, E, E + kept, gpu, dtype)
+        check(l, k, balance(E, 2, gpu) if biased else None, score=score, num_groups=groups, topk_groups=kept,
+              group_score=group_score)
+
+
+@pytest.mark.parametrize("groups,kept", [(1, 1), (8, 3)])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_ties(gpu, score, biased, groups, kept):
+    """Few distinct logits and biases: most choices are ties, of experts and of groups, -0 and +0 among them."""
+    g = torch.Generator().manual_seed(3)
+    l = torch.randint(-2, 3, (200, 64), generator=g).float() * torch.where(torch.rand(200, 64, generator=g) < 0.5, 1, -1)
+    b = (torch.randint(0, 2, (64,), generator=g).float() * 0.25).to(gpu) if biased else None
+    for dtype, gs in itertools.product([F32, BF16], ["max", "top2"]):
+        check(l.to(dtype).to(gpu), 8, b, score=score, num_groups=groups, topk_groups=kept, group_score=gs)
+    check(torch.zeros(3, 64, device=gpu), 8, b, score=score, num_groups=groups, topk_groups=kept)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_near_ties(gpu, score):
+    """Orders that 32 bits would get wrong: sums of score and bias a few 2^-26 apart."""
+    g = torch.Generator().manual_seed(4)
+    T, E = 300, 64
+    l = torch.randn(T, E, generator=g) * 0.2
+    s = torch.sigmoid(l.double()) if score == "sigmoid" else torch.softmax(l.double(), -1)
+    bias = (1.0 - s[0]).float()
+    l[1:] = l[0] + torch.randint(-3, 4, (T - 1, E), generator=g) * 2.0 ** -26
+    l[150:] = l[0] + torch.randint(-1, 2, (150, E), generator=g) * 2.0 ** -23
+    for groups, kept in ((1, 1), (8, 4)):
+        for gs in ("max", "top2"):
+            check(l.to(gpu), 8, bias.to(gpu), score=score, num_groups=groups, topk_groups=kept, group_score=gs)
+            check(l.to(gpu), 8, score=score, num_groups=groups, topk_groups=kept, group_score=gs)
+
+
+@pytest.mark.parametrize("groups,kept", [(1, 1), (4, 2), (32, 8)])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_masks(gpu, score, biased, groups, kept):
+    """Rows from all experts down to none; experts masked by logit or by bias; groups masked whole."""
+    T, E, k = 65, 64, 8
+    l = normal(T, E, 5, gpu)
+    order = torch.rand(T, E, generator=torch.Generator().manual_seed(6)).argsort(1).to(gpu)
+    l[order < torch.arange(T, device=gpu)[:, None]] = -INF         # row t masks t experts; the last row all 64
+    l[3, 16:] = -INF
+    b = None
+    if biased:
+        b = balance(E, 7, gpu)
+        b[5], b[17], b[32:48] = -INF, -INF, -INF
+    for renorm, gs in itertools.product([True, False], ["max", "top2"]):
+        check(l, k, b, score=score, num_groups=groups, topk_groups=kept, group_score=gs, renormalize=renorm)
+    ids, w = run(l, k, b, score=score)
+    assert (ids[T - 1] == -1).all() and (w[T - 1] == 0).all()
+    check(torch.full((5, E), -INF, device=gpu).to(BF16), k, b, score=score, num_groups=groups, topk_groups=kept)
+
+
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_extreme_logits(gpu, score, biased):
+    """Far apart, saturated and lowest-value logits; a sum of scores that is zero."""
+    l = normal(40, 96, 8, gpu, scale=300.0)
+    l[1] = torch.finfo(F32).min
+    l[2] = -1e4 - torch.arange(96, device=gpu)
+    l[3] = 1e4 + torch.arange(96, device=gpu)
+    l[4, 1::2] = torch.finfo(F32).min
+    l[5] = torch.arange(96, device=gpu) * 1e-42                     # subnormal
+    b = balance(96, 9, gpu) if biased else None
+    for renorm in (True, False):
+        check(l, 8, b, score=score, renormalize=renorm)
+
+
+@pytest.mark.parametrize("groups,kept", [(1, 1), (8, 4)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_nan_and_infinity(gpu, score, groups, kept):
+    l = normal(6, 64, 10, gpu)
+    l[0, 40], l[1, 3], l[1, 50], l[2, 7] = NAN, NAN, NAN, INF
+    l[3, 5:] = -INF
+    l[3, 2] = NAN
+    for gs in ("max", "top2"):
+        for b in (None, balance(64, 11, gpu)):
+            check(l, 6, b, score=score, num_groups=groups, topk_groups=kept, group_score=gs)
+            check(l, 6, b, score=score, num_groups=groups, topk_groups=kept, group_score=gs, renormalize=False)
+
+
+def test_gate_rows(gpu):
+    """Strided rows at odd offsets, many rows, rows behind the last, and a scale of any sign."""
+    l = normal(3000, 60, 12, gpu)
+    want = run(l, 6)
+    for dtype, off, stride in ((F32, 1, 77), (BF16, 3, 63)):
+        wide = torch.full((3001, stride), INF, dtype=dtype, device=gpu)
+        flat = wide.view(-1)[off:]
+        rows = flat.as_strided((3000, 60), (stride, 1))
+        rows.copy_(l)
+        s = B.make_gate(3000, 60, 6, logits_dtype=dtype, logits_stride=stride)
+        ids, w = run(rows, 6, shape=s)
+        ref = run(l.to(dtype), 6)
+        assert np.array_equal(ids, ref[0]) and np.array_equal(w, ref[1])
+    ids = torch.full((10, 6), 9, dtype=torch.int64, device=gpu)
+    w = torch.full((10, 6), 9.0, device=gpu)
+    B.gate(B.make_gate(7, 60, 6), l[:7], ids[:7], w[:7])
+    torch.cuda.synchronize()
+    assert np.array_equal(ids[:7].cpu().numpy(), want[0][:7]) and (ids[7:] == 9).all() and (w[7:] == 9.0).all()
+    check(l[:50], 6, scale=-0.5)
+    check(l[:50], 6, scale=0.0)
+
+
+def test_gate_no_tokens(gpu):
+    e = torch.zeros(0, 8, device=gpu)
+    B.gate(B.make_gate(0, 8, 2), e, torch.zeros(0, 2, dtype=torch.int64, device=gpu), torch.zeros(0, 2, device=gpu))
+
+
+def test_gate_binding_refusals(gpu):
+    l, s = normal(4, 16, 13, gpu), B.make_gate(4, 16, 2)
+    ids, w = torch.empty(4, 2, dtype=torch.int64, device=gpu), torch.empty(4, 2, device=gpu)
+    for a, kw in (((l[:3], ids, w), {}), ((l.to(BF16), ids, w), {}), ((l, ids.int(), w), {}), ((l, ids, w.double()), {}),
+                  ((l, ids[:3], w), {}), ((l, ids, w), dict(bias=torch.zeros(15, device=gpu))),
+                  ((l, ids, w), dict(bias=torch.zeros(16))), ((l, ids, w), dict(bias=torch.zeros(16, device=gpu).to(BF16)))):
+        with pytest.raises((TypeError, ValueError)):
+            B.gate(s, *a, **kw)

@@ -1,0 +1,130 @@
+"""GPU parity of moe_router_logits.
+
+Small whole numbers make every product and partial sum exact in FP32, in any order, so those results are
+compared bit for bit.  Random operands are held to the worst case of an FP32 sum of n products in any order,
+n * 2^-23 of the sum of their magnitudes (2^-23: a sum inside a matrix instruction may truncate).
+"""
+import pytest
+import torch
+
+from moe_expert_ffn_plan_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def run(x, w, T=None, shape=None, fill=0x5A):
+    T = x.shape[0]
+    E, H = w.shape
+    s = shape or B.make_router(T, H, E, weight_dtype=w.dtype)
+    logits = torch.full((T, E), float("nan"), dtype=F32, device=x.device)
+    ws = torch.full((B.router_workspace_bytes(s),), fill, dtype=torch.uint8, device=x.device)
+    B.router_logits(s, x, B.router_prepare(s, w), logits, ws)
+    torch.cuda.synchronize()
+    return logits
+
+
+def whole(T, H, E, wt, seed, device):
+    """Operands whose sums stay below 2^24: |x| <= 15, |w| <= 3 (BF16) or up to 2^11 on few columns (FP32)."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randint(-15, 16, (T, H), generator=g).float()
+    w = torch.randint(-3, 4, (E, H), generator=g).float()
+    if wt == F32:   # more than 8 significant bits on every 61st column, so that the parts all take part
+        w[:, ::61] = torch.randint(-1500, 1501, (E, (H + 60) // 61), generator=g).float()
+    assert (x.abs().sum(1).max() * 3 + 15 * 1500 * (H // 61 + 1)) < 2 ** 24
+    return x.to(BF16).to(device), w.to(wt).to(device)
+
+
+# T around every tile edge, E that fill no tile, one K-step to long rows
+SIZES = [(1, 32, 1), (1, 7168, 256), (3, 64, 8), (16, 96, 16), (17, 4096, 64), (31, 1056, 100), (64, 7168, 384),
+         (65, 2048, 257), (127, 7168, 256), (128, 7168, 256), (129, 512, 512), (200, 4096, 1000), (255, 32, 1024),
+         (1000, 992, 77), (513, 7168, 129), (2047, 4096, 64), (4097, 1024, 255), (9000, 480, 48), (33000, 64, 40)]
+
+
+@pytest.mark.parametrize("wt", [BF16, F32])
+@pytest.mark.parametrize("T,H,E", SIZES)
+def test_router_exact(gpu, T, H, E, wt):
+    print(f"router T={T} H={H} E={E} {wt}", flush=True)
+    x, w = whole(T, H, E, wt, T + E, gpu)
+    got = run(x, w)
+    want = x.double() @ w.double().t().contiguous()
+    assert torch.equal(got.double(), want)
+
+
+@pytest.mark.parametrize("wt", [BF16, F32])
+@pytest.mark.parametrize("T,H,E", [(1, 7168, 256), (130, 7168, 256), (700, 4096, 64), (5000, 1024, 384)])
+def test_router_random(gpu, T, H, E, wt):
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(T, H, generator=g).to(BF16).to(gpu)
+    w = (torch.randn(E, H, generator=g) / H ** 0.5).to(wt).to(gpu)
+    got = run(x, w).double()
+    xd, wd = x.double(), w.double().t().contiguous()
+    n = H * (3 if wt == F32 else 1)
+    assert ((got - xd @ wd).abs() <= n * 2.0 ** -23 * (xd.abs() @ wd.abs())).all()
+
+
+def test_router_f32_weights_keep_all_bits(gpu):
+    """A row of x that picks one column returns that column of the weights, bit for bit."""
+    H, E = 128, 37
+    w = torch.randn(E, H, generator=torch.Generator().manual_seed(6)) * torch.exp2(torch.arange(H) % 60 - 30.0)
+    got = run(torch.eye(H).to(BF16).to(gpu), w.to(gpu))
+    assert torch.equal(got, w.t().contiguous().to(gpu))
+
+
+def test_router_rows(gpu):
+    """Strided rows of x, an x that ends where its memory ends, and rows of logits behind the last."""
+    x, w = whole(50, 256, 33, BF16, 9, gpu)
+    want = run(x, w)
+    wide = torch.full((50, 320), float("nan"), dtype=BF16, device=gpu)
+    wide[:, :256] = x
+    got = run(wide[:, :256], w, shape=B.make_router(50, 256, 33, x_stride=320))
+    assert torch.equal(got, want)
+    s = B.make_router(20, 256, 33)
+    logits = torch.full((50, 33), 4.0, device=gpu)
+    ws = torch.empty(B.router_workspace_bytes(s), dtype=torch.uint8, device=gpu)
+    B.router_logits(s, x[:20], B.router_prepare(s, w), logits[:20], ws)
+    torch.cuda.synchronize()
+    assert torch.equal(logits[:20], want[:20]) and (logits[20:] == 4.0).all()
+
+
+@pytest.mark.parametrize("T", [1, 40, 300, 3000])
+def test_router_same_for_a_row_alone_and_again(gpu, T):
+    """Bit-identical from call to call, whatever the workspace holds."""
+    g = torch.Generator().manual_seed(7)
+    x, w = torch.randn(T, 7168, generator=g).to(BF16).to(gpu), torch.randn(256, 7168, generator=g).to(BF16).to(gpu)
+    a = run(x, w)
+    for fill in (0x00, 0xFF):
+        assert torch.equal(a, run(x, w, fill=fill))
+
+
+def test_router_nan_rows_stay_apart(gpu):
+    x, w = whole(40, 512, 20, BF16, 10, gpu)
+    want = run(x, w)
+    x[7, 3], x[21, 500] = float("nan"), float("inf")
+    got = run(x, w)
+    keep = torch.ones(40, dtype=torch.bool)
+    keep[[7, 21]] = False
+    assert torch.isnan(got[7]).all() and not torch.isfinite(got[21]).any()
+    assert torch.equal(got[keep.to(gpu)], want[keep.to(gpu)])
+
+
+def test_router_no_tokens(gpu):
+    s = B.make_router(0, 64, 8)
+    w = torch.ones(8, 64, dtype=BF16, device=gpu)
+    x = torch.zeros(0, 64, dtype=BF16, device=gpu)
+    B.router_logits(s, x, B.router_prepare(s, w), torch.zeros(0, 8, device=gpu))
+
+
+def test_router_binding_refusals(gpu):
+    x, w = whole(20, 64, 8, BF16, 11, gpu)
+    s = B.make_router(20, 64, 8)
+    wt, out = B.router_prepare(s, w), torch.empty(20, 8, device=gpu)
+    for a in ((x[:19], wt, out), (x.float(), wt, out), (x, wt[:-16], out), (x, w, out), (x, wt, out[:, :7]),
+              (x, wt, out.half()), (x.cpu(), wt, out), (x, wt, out.cpu())):
+        with pytest.raises((TypeError, ValueError)):
+            B.router_logits(s, *a)
+    with pytest.raises(TypeError):
+        B.router_prepare(s, w.float())
+    with pytest.raises(ValueError):
+        B.router_prepare(s, w[:7])
