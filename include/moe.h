@@ -405,7 +405,8 @@ enum moe_dtype {
  * 0x7F or 0xFF); an infinite element becomes NaN and the others of its row 0;
  * a row of zeros with eps = 0 is NaN.
  * Limits (else MOE_ERR_SHAPE, or MOE_ERR_ALIGN for the divisibility rules):
- *   num_tokens >= 0; hidden 32 .. 2^20, a multiple of 32; eps finite, >= 0;
+ *   num_tokens 0 .. 2^30 - 1; hidden 32 .. 2^20, a multiple of 32; eps finite,
+ *   >= 0;
  *   strides >= hidden and multiples of 8 elements.
  * x, residual, residual_out, weight, y and x_q: 16-byte aligned. */
 typedef struct moe_norm_shape {
@@ -435,8 +436,8 @@ MOE_API int moe_norm_quant(const moe_norm_shape* shape, const void* x, const voi
 /* Router product: logits[t, e] = sum over k of x[t, k] * w[e, k], in FP32.
  * Products are exact in FP32 and sums are held in FP32, for FP32 weights too
  * (a weight is split into three BF16 parts, 8 bits each).
- * Limits: num_tokens >= 0; hidden 32 .. 2^20, a multiple of 32; num_experts
- * 1 .. 1024 (all ranks' experts); x_stride >= hidden and a multiple of 8. */
+ * Limits: num_tokens 0 .. 2^30 - 1; hidden 32 .. 2^20, a multiple of 32;
+ * num_experts 1 .. 1024 (all ranks' experts); x_stride >= hidden and a multiple of 8. */
 typedef struct moe_router_shape {
     int64_t x_stride;
     int32_t num_tokens;

@@ -390,6 +390,7 @@ namespace {
 
 bool type_ok(int t) { return t == MOE_BF16 || t == MOE_F32; }
 bool flag_ok(int v) { return v == 0 || v == 1; }
+bool tokens_ok(int t) { return t >= 0 && t < (1 << 30); }  // kernels count padded tokens in 32 bits
 
 // A stride as given (0 = contiguous) against the row length; vectors of 8 elements start every row.
 int check_stride(int64_t stride, int64_t row) {
@@ -406,7 +407,7 @@ int check_hidden(int h) {
 
 int check_norm(const moe_norm_shape* s) {
     if (!s) return MOE_ERR_NULL;
-    if (s->num_tokens < 0 || !type_ok(s->x_type) || !type_ok(s->residual_type) || !type_ok(s->weight_type))
+    if (!tokens_ok(s->num_tokens) || !type_ok(s->x_type) || !type_ok(s->residual_type) || !type_ok(s->weight_type))
         return MOE_ERR_SHAPE;
     if (!(s->eps >= 0.0f && s->eps <= 3.0e38f)) return MOE_ERR_SHAPE;  // also rejects NaN
     int st = check_hidden(s->hidden);
@@ -417,7 +418,7 @@ int check_norm(const moe_norm_shape* s) {
 
 int check_router(const moe_router_shape* s) {
     if (!s) return MOE_ERR_NULL;
-    if (s->num_tokens < 0 || !type_ok(s->weight_type)) return MOE_ERR_SHAPE;
+    if (!tokens_ok(s->num_tokens) || !type_ok(s->weight_type)) return MOE_ERR_SHAPE;
     if (s->num_experts < 1 || s->num_experts > kMaxGateExperts) return MOE_ERR_SHAPE;
     const int st = check_hidden(s->hidden);
     return st != MOE_OK ? st : check_stride(s->x_stride, s->hidden);

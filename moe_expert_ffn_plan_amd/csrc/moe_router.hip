@@ -10,6 +10,8 @@
 // experts 4 (l / 16) .. + 4, neighbours in a logits row.
 #include "moe_internal.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -69,27 +71,395 @@ __device__ __forceinline__ void store_logits(float* logits, int E, int64_t t, in
     }
 }
 
-// One wave per 16 tokens x 16 experts, operands straight from memory.
-template <int P>
-__global__ __launch_bounds__(64) void router_simple_kernel(RouterArgs a) {
-    const int lane = threadIdx.x, KT = a.H / 32;
-    const int t = blockIdx.y * 16 + (lane & 15);
-    const uint16_t* x = a.x + (int64_t)min(t, a.T - 1) * a.x_stride + (lane >> 4) * 8;
-    const uint8_t* w = a.w + ((int64_t)blockIdx.x * KT * P * 64 + lane) * 16;
-    v4f acc = {0.f, 0.f, 0.f, 0.f};
-    for (int kt = 0; kt < KT; ++kt) {
-        const bf16x8 b = *reinterpret_cast<const bf16x8*>(x + kt * 32);
+// ---- LDS DMA and waits (the compiler does not count what inline assembly issues; each kernel waits itself)
+
+// Lane l reads 16 bytes at its own address and writes them at LDS address lds + 16 l.  x is streamed about
+// once: the non-temporal hint keeps the weights in the L2 (16384 x 7168 x 256: 82 -> 78 us, and a pass that
+// only streams x 49 -> 41 us).
+__device__ __forceinline__ void dma16_stream(uint64_t addr, uint32_t lds) {
+    asm volatile("global_load_lds_dwordx4 %0, off nt" ::"v"(addr), "{m0}"(lds) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_and_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)p);
+}
+
+// The x operand lies in LDS as rows of whole 128-byte runs (64 columns), 16-byte chunk c of row r at chunk
+// c ^ ((r >> 1) & 7) of its run: a ds_read_b128 is conflict-free where lanes l, l^2, l^4, l^6 take different
+// 16-byte slots modulo 128 bytes, which this gives for 16 consecutive rows at one chunk.  Reading x into
+// registers directly puts neighbouring lanes on different rows, which the address unit takes one lane at a
+// time (128 x 7168 x 256: 10.0 us against 7.1 through LDS).
+__device__ __forceinline__ int swizzle(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
+
+// The sum over the parts of an FP32 weight: the first parts' products in one accumulator, those of the
+// other two in another, so that the small terms do not round the large sum twice more per step.
+template <int P, int N, int M>
+struct Sums {
+    static constexpr int SETS = P > 1 ? 2 : 1;
+    v4f v[SETS][N][M];
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                *reinterpret_cast<const bf16x8*>(w + ((int64_t)kt * P + p) * 1024), b, acc, 0, 0, 0);
+        for (int s = 0; s < SETS; ++s)
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int m = 0; m < M; ++m) v[s][n][m] = v4f{0.f, 0.f, 0.f, 0.f};
     }
-    if (t < a.T) store_logits(a.logits, a.E, t, blockIdx.x * 16 + (lane >> 4) * 4, acc);
+    __device__ __forceinline__ void add(int p, int n, int m, bf16x8 w, bf16x8 x) {
+        v4f& c = v[p > 0 ? SETS - 1 : 0][n][m];
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, c, 0, 0, 0);
+    }
+    __device__ __forceinline__ v4f total(int n, int m) const {
+        return SETS == 1 ? v[0][n][m] : v[0][n][m] + v[SETS - 1][n][m];
+    }
+};
+
+// ---- few tokens: one workgroup per MT x 16 tokens and 16 experts, in one launch
+//
+// Latency-bound: the 16 waves split the columns, wave w taking every 16th run of 64, each with its loads of
+// U runs in flight at once (x through its own piece of LDS, the weights straight into registers, 1 KiB a
+// load), and add up through LDS in the order of the waves.
+template <int MT_, int P_, int U_>
+struct Small {
+    static constexpr int MT = MT_, P = P_, U = U_, W = 16;
+    static constexpr int RUN = MT * 2048;  // bytes of one run of the workgroup's tokens
+    static constexpr int XS = W * U * RUN, RED = W * MT * 1024, LDS = XS > RED ? XS : RED;
+    static_assert(LDS <= 160 * 1024, "fits the LDS");
+};
+
+template <class C>
+__global__ __launch_bounds__(C::W * 64) void router_small_kernel(RouterArgs a) {
+    __shared__ __align__(1024) uint8_t lds[C::LDS];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int KT = a.H / 32, runs = (KT + 1) / 2;
+    const int m0 = blockIdx.y * C::MT * 16;
+    uint64_t xp[C::MT * 2];                          // transfer i: rows 8 i .. 8 i + 8 of the run
+    int xc[C::MT * 2];
+#pragma unroll
+    for (int i = 0; i < C::MT * 2; ++i) {
+        const int row = i * 8 + (lane >> 3);
+        xc[i] = swizzle(row, lane & 7);
+        xp[i] = reinterpret_cast<uint64_t>(a.x + (int64_t)min(m0 + row, a.T - 1) * a.x_stride + xc[i] * 8);
+    }
+    const uint8_t* wp = a.w + (int64_t)blockIdx.x * KT * C::P * 1024;
+    Sums<C::P, 1, C::MT> acc;
+    acc.clear();
+    const uint32_t mine = lds_addr(lds) + wave * C::U * C::RUN;
+    const uint8_t* xs = lds + wave * C::U * C::RUN;
+    for (int r0 = wave; r0 < runs; r0 += C::U * C::W) {
+        bf16x8 w[C::U][2][C::P];
+#pragma unroll
+        for (int u = 0; u < C::U; ++u) {
+            const int r = r0 + u * C::W;
+            if (r >= runs) break;
+            // a last run of 32 columns: the missing chunks read the run's first, and are not multiplied
+            const bool half = 2 * r + 1 >= KT;
+#pragma unroll
+            for (int i = 0; i < C::MT * 2; ++i)
+                dma16_stream(xp[i] + (int64_t)r * 128 - (half && xc[i] >= 4 ? xc[i] * 16 : 0),
+                             mine + u * C::RUN + i * 1024);
+        }
+#pragma unroll
+        for (int u = 0; u < C::U; ++u) {
+            const int r = r0 + u * C::W;
+            if (r >= runs) break;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int p = 0; p < C::P; ++p)
+                    w[u][j][p] = *reinterpret_cast<const bf16x8*>(
+                        wp + ((int64_t)min(2 * r + j, KT - 1) * C::P + p) * 1024 + lane * 16);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int u = 0; u < C::U; ++u) {
+            const int r = r0 + u * C::W;
+            if (r >= runs) break;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (2 * r + j >= KT) break;
+#pragma unroll
+                for (int m = 0; m < C::MT; ++m) {
+                    const int row = m * 16 + (lane & 15);
+                    const bf16x8 x = *reinterpret_cast<const bf16x8*>(xs + u * C::RUN + row * 128 +
+                                                                     swizzle(row, j * 4 + (lane >> 4)) * 16);
+#pragma unroll
+                    for (int p = 0; p < C::P; ++p) acc.add(p, 0, m, w[u][j][p], x);
+                }
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // x is read before the next runs overwrite it
+    }
+    __syncthreads();
+    v4f(*part)[C::MT][64] = reinterpret_cast<v4f(*)[C::MT][64]>(lds);
+#pragma unroll
+    for (int m = 0; m < C::MT; ++m) part[wave][m][lane] = acc.total(0, m);
+    __syncthreads();
+    if (wave < C::MT) {
+        v4f sum = part[0][wave][lane];
+#pragma unroll
+        for (int w = 1; w < C::W; ++w) sum += part[w][wave][lane];
+        const int t = m0 + wave * 16 + (lane & 15);
+        if (t < a.T) store_logits(a.logits, a.E, t, blockIdx.x * 16 + (lane >> 4) * 4, sum);
+    }
+}
+
+// ---- many tokens: tiles of BM tokens x 64 NF experts over a range of K-steps of BK columns
+//
+// Four producer waves stream x into an LDS ring of NS stages and do nothing else; four consumer waves, one
+// per SIMD, each own 16 NF experts and all BM tokens.  A consumer reads its weights from the L2 straight
+// into registers (they lie in operand order, so LDS would only add a round trip), one K-step ahead, and x
+// from the ring, four fragments ahead of the matrix instructions.  One barrier per step publishes a stage
+// and frees the one before it; producers wait for their own transfers ahead of it, consumers for their LDS
+// reads, and a consumer has the next step's first fragments in flight before it starts the last products
+// of its step.
+// Where it goes (16384 x 7168 x 256, 128 x 256 tiles, two splits, 61 of 71 us): x alone streams in 41 us, the
+// products with both operands in the L2 take 45.  The L1 delivers 64 bytes a clock and a CU moves 24 KiB per
+// 32 columns, 384 of the 512 clocks of its matrix instructions; 64 x 256 tiles need no second split but move
+// 20 KiB for half of the products and take 77 us.  BK of 64 (128-byte runs of each row) streams x at
+// 3.9 TB/s, 128 at 4.5, so a stage holds 128 columns where registers allow.
+template <int BM_, int NF_, int NS_, int BK_, int P_>
+struct Tile {
+    static constexpr int BM = BM_, NF = NF_, NS = NS_, BK = BK_, P = P_;
+    static constexpr int CW = 4, PW = 4, THREADS = (CW + PW) * 64, BN = NF * CW * 16;
+    static constexpr int KS = BK / 32, MT = BM / 16, CH = BK / 8;       // 16-byte chunks per row and step
+    static constexpr int STAGE = BM * BK * 2, PER = STAGE / 1024 / PW;  // transfers per producer and stage
+    static constexpr int GS = MT < 4 ? MT : 4, GPK = MT / GS, NG = KS * GPK;  // fragment groups of a step
+    static_assert(BK % 64 == 0 && MT % GS == 0 && NG % 2 == 0, "whole runs; two fragment buffers alternate");
+    static_assert(STAGE % (1024 * PW) == 0 && NS >= 2 && NS * STAGE <= 160 * 1024, "the ring");
+    static_assert(PER * (NS - 2) < 63, "vmcnt counts to 63");
+};
+
+struct TileArgs {
+    RouterArgs r;
+    int m_tiles, n_tiles, splits, steps;  // K-steps in all
+};
+
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void router_tile_kernel(TileArgs a) {
+    __shared__ __align__(1024) uint8_t ring[C::NS * C::STAGE];
+    // XCD b % 8 takes a contiguous run of the list [split][m tile][n tile]: what shares x or a part of the
+    // weights runs side by side on one L2
+    const int total = a.m_tiles * a.n_tiles * a.splits, share = (total + 7) / 8;
+    const int v = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
+    if (v >= total) return;  // the grid is 8 * share workgroups
+    const int split = v / (a.m_tiles * a.n_tiles), mn = v % (a.m_tiles * a.n_tiles);
+    const int m0 = mn / a.n_tiles * C::BM, n0 = mn % a.n_tiles * C::BN;
+    const int s_begin = (int)((int64_t)a.steps * split / a.splits);
+    const int s_end = (int)((int64_t)a.steps * (split + 1) / a.splits);
+    const int n_steps = s_end - s_begin;  // >= 1: splits <= steps
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int KT = a.r.H / 32;
+
+    if (wave >= C::CW) {
+        const int pw = wave - C::CW;
+        const uint32_t ring0 = lds_addr(ring);
+        uint64_t src[C::PER];
+        int chunk[C::PER];
+#pragma unroll
+        for (int i = 0; i < C::PER; ++i) {
+            const int slot = (pw + i * C::PW) * 64 + lane, row = slot / C::CH;
+            chunk[i] = swizzle(row, slot % C::CH);
+            src[i] = reinterpret_cast<uint64_t>(a.r.x + (int64_t)min(m0 + row, a.r.T - 1) * a.r.x_stride + chunk[i] * 8);
+        }
+        auto issue = [&](int step, int stage) {
+            // a last step of fewer columns: the missing chunks read the step's first, and are not multiplied
+            const int valid = (KT - step * C::KS) * 4;
+#pragma unroll
+            for (int i = 0; i < C::PER; ++i)
+                dma16_stream(src[i] + (int64_t)step * (C::BK * 2) - (chunk[i] >= valid ? chunk[i] * 16 : 0),
+                             ring0 + stage * C::STAGE + (pw + i * C::PW) * 1024);
+        };
+#pragma unroll
+        for (int s = 0; s < C::NS - 1; ++s)
+            if (s < n_steps) issue(s_begin + s, s);
+        int stage = 0;
+        for (int s = 0; s < n_steps; ++s) {
+            if (n_steps - 1 - s >= C::NS - 2) wait_and_barrier<(C::NS - 2) * C::PER>();
+            else wait_and_barrier<0>();
+            if (s + C::NS - 1 < n_steps) issue(s_begin + s + C::NS - 1, stage == 0 ? C::NS - 1 : stage - 1);
+            stage = stage == C::NS - 1 ? 0 : stage + 1;
+        }
+        return;
+    }
+
+    const uint8_t* wp[C::NF];  // wave-uniform; blocks past the last read the last, and are not stored
+#pragma unroll
+    for (int n = 0; n < C::NF; ++n)
+        wp[n] = a.r.w + (int64_t)min(n0 / 16 + wave * C::NF + n, (a.r.E + 15) / 16 - 1) * KT * C::P * 1024;
+    const uint32_t lane16 = lane * 16;
+    bf16x8 w[C::KS][C::P][C::NF];
+    auto load = [&](int k, bf16x8 (&b)[C::P][C::NF]) {
+        const int64_t kk = min(k, KT - 1);
+#pragma unroll
+        for (int p = 0; p < C::P; ++p)
+#pragma unroll
+            for (int n = 0; n < C::NF; ++n)
+                b[p][n] = *reinterpret_cast<const bf16x8*>(wp[n] + (kk * C::P + p) * 1024 + lane16);
+    };
+    bf16x8 xg[2][C::GS];
+    const int r16 = lane & 15, q = lane >> 4;
+    const uint32_t x_even = r16 * (C::BK * 2) + swizzle(r16, q) * 16;
+    const uint32_t x_odd = r16 * (C::BK * 2) + swizzle(r16, 4 + q) * 16;
+    auto read = [&](const uint8_t* stage, int g, bf16x8 (&x)[C::GS]) {
+        const int ks = g / C::GPK;
+        const uint8_t* p = stage + (ks & 1 ? x_odd : x_even) + (ks >> 1) * 128;
+#pragma unroll
+        for (int i = 0; i < C::GS; ++i)
+            x[i] = *reinterpret_cast<const bf16x8*>(p + (g % C::GPK * C::GS + i) * 16 * (C::BK * 2));
+    };
+    Sums<C::P, C::NF, C::MT> acc;
+    acc.clear();
+    auto multiply = [&](int g, const bf16x8 (&x)[C::GS]) {
+#pragma unroll
+        for (int p = 0; p < C::P; ++p)
+#pragma unroll
+            for (int n = 0; n < C::NF; ++n)
+#pragma unroll
+                for (int i = 0; i < C::GS; ++i) acc.add(p, n, g % C::GPK * C::GS + i, w[g / C::GPK][p][n], x[i]);
+    };
+
+#pragma unroll
+    for (int k = 0; k < C::KS; ++k) load(s_begin * C::KS + k, w[k]);
+    asm volatile("s_barrier" ::: "memory");
+    read(ring, 0, xg[0]);
+    int stage = 0;
+    for (int s = 0; s < n_steps - 1; ++s) {
+        const int next = stage == C::NS - 1 ? 0 : stage + 1;
+#pragma unroll
+        for (int g = 0; g < C::NG; ++g) {
+            if (g < C::NG - 1) {
+                read(ring + stage * C::STAGE, g + 1, xg[(g + 1) & 1]);
+            } else {
+                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                read(ring + next * C::STAGE, 0, xg[0]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(g, xg[g & 1]);
+            if (g % C::GPK == C::GPK - 1) load((s_begin + s + 1) * C::KS + g / C::GPK, w[g / C::GPK]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        stage = next;
+    }
+    const int valid = min(C::KS, KT - (s_end - 1) * C::KS);
+#pragma unroll
+    for (int g = 0; g < C::NG; ++g) {
+        if (g / C::GPK >= valid) break;
+        if (g < C::NG - 1) read(ring + stage * C::STAGE, g + 1, xg[(g + 1) & 1]);
+        multiply(g, xg[g & 1]);
+    }
+    float* out = a.splits > 1 ? a.r.partial + (int64_t)split * a.r.T * a.r.E : a.r.logits;
+#pragma unroll
+    for (int m = 0; m < C::MT; ++m) {
+        const int t = m0 + m * 16 + r16;
+        if (t >= a.r.T) continue;
+#pragma unroll
+        for (int n = 0; n < C::NF; ++n)
+            store_logits(out, a.r.E, t, n0 + (wave * C::NF + n) * 16 + q * 4, acc.total(n, m));
+    }
+}
+
+// Sums the splits' partial products [splits][n], in their order.
+__global__ __launch_bounds__(kThreads) void router_reduce_kernel(const float* __restrict__ part, int splits, int64_t n,
+                                                                 float* __restrict__ out) {
+    const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+    if (i >= n) return;
+    if (n % 4 == 0) {
+        v4f sum = *reinterpret_cast<const v4f*>(part + i);
+        for (int s = 1; s < splits; ++s) sum += *reinterpret_cast<const v4f*>(part + s * n + i);
+        *reinterpret_cast<v4f*>(out + i) = sum;
+    } else {
+        for (int64_t j = i; j < min(i + 4, n); ++j) {
+            float sum = part[j];
+            for (int s = 1; s < splits; ++s) sum += part[s * n + j];
+            out[j] = sum;
+        }
+    }
+}
+
+// ---- which kernel
+//
+// Few tokens: the small kernel while its workgroups fit the CUs once (128 x 7168 x 256: 7.1 us, against 15.2
+// for a tile kernel split 28 ways and its second launch), of 32 tokens where 16 no longer fit (512 x 7168 x
+// 256: 12.2 us against 14.9 and 16.2).
+// Then tiles, as small as give one workgroup per CU: 64 tokens x 64 or 128 experts split over K into what the
+// CUs hold (1024 x 7168 x 256: 15.7 us; 64 x 256 tiles 18.5), and above that 128-token tiles, whose operands
+// are read half as often (16384 x 7168 x 256: 71 us against 89), 192 experts wide where that covers E with
+// fewer columns (16384 x 7168 x 384: 86 us against 105 at 256).  FP32 weights hold three times the registers
+// for weights: 128 experts at most, K-steps of 64 columns from 128 on; 32-token tiles where 64 experts at 64
+// tokens leave most CUs without a tile (2048 x 4096 x 64: 10.4 us against 11.9).
+constexpr int kCus = 256;
+
+enum Kernel { kSmall16, kSmall32, kTile32x64, kTile64x64, kTile64x128, kTile128x128, kTile128x192, kTile128x256 };
+struct Choice {
+    Kernel kernel;
+    int splits;
+};
+
+int div_up(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+Choice choose(int T, int H, int E, int parts) {
+    const int64_t blocks = div_up(E, 16);
+    if (div_up(T, 16) * blocks <= kCus) return {kSmall16, 1};
+    if (div_up(T, 32) * blocks <= kCus) return {kSmall32, 1};
+    Kernel k;
+    int bm = 64, bn = 128, bk = 128;
+    if (E <= 64) {
+        bn = 64;
+        k = kTile64x64;
+        if (parts == 3 && div_up(T, 64) <= kCus / 4) {
+            bm = 32;
+            k = kTile32x64;
+        }
+    } else if ((int64_t)div_up(T, 64) * div_up(E, 128) <= kCus || (parts == 1 && E <= 128)) {
+        k = kTile64x128;
+        if (parts == 3) bk = 64;
+    } else if (parts == 3) {
+        bm = 128;
+        bk = 64;
+        k = kTile128x128;
+    } else {
+        bm = 128;
+        bn = div_up(E, 192) * 192 < div_up(E, 256) * 256 ? 192 : 256;
+        k = bn == 192 ? kTile128x192 : kTile128x256;
+    }
+    const int64_t tiles = (int64_t)div_up(T, bm) * div_up(E, bn);
+    const int64_t splits = std::min<int64_t>(kCus / std::max<int64_t>(tiles, 1), div_up(H, bk) / 4);
+    return {k, (int)std::max<int64_t>(splits, 1)};
+}
+
+template <class C>
+hipError_t launch_small(const RouterArgs& a, hipStream_t stream) {
+    const dim3 grid((unsigned)div_up(a.E, 16), (unsigned)div_up(a.T, C::MT * 16));
+    hipLaunchKernelGGL(router_small_kernel<C>, grid, dim3(C::W * 64), 0, stream, a);
+    return hipGetLastError();
+}
+
+template <class C>
+hipError_t launch_tile(const RouterArgs& r, int splits, hipStream_t stream) {
+    const TileArgs a{r, div_up(r.T, C::BM), div_up(r.E, C::BN), splits, div_up(r.H, C::BK)};
+    const int64_t total = (int64_t)a.m_tiles * a.n_tiles * splits;
+    hipLaunchKernelGGL(router_tile_kernel<C>, dim3((unsigned)div_up(total, 8) * 8), dim3(C::THREADS), 0, stream, a);
+    if (splits > 1) {
+        const int64_t n = (int64_t)r.T * r.E;
+        hipLaunchKernelGGL(router_reduce_kernel, dim3((unsigned)div_up(n, 4 * kThreads)), dim3(kThreads), 0, stream,
+                           r.partial, splits, n, r.logits);
+    }
+    return hipGetLastError();
 }
 
 }  // namespace
 
-size_t router_workspace_bytes(int, int, int, int) { return 0; }
+size_t router_workspace_bytes(int T, int H, int E, int parts) {
+    const Choice c = choose(T, H, E, parts);
+    return c.splits > 1 ? (size_t)c.splits * T * E * sizeof(float) : 0;
+}
 
 hipError_t launch_router_prepare(int H, int E, int weight_type, const void* w, uint8_t* w_tiled, hipStream_t stream) {
     const int64_t slots = (int64_t)((E + 15) / 16) * (H / 32) * 64;
@@ -102,10 +472,23 @@ hipError_t launch_router_prepare(int H, int E, int weight_type, const void* w, u
 }
 
 hipError_t launch_router_logits(const RouterArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)((a.E + 15) / 16), (unsigned)((a.T + 15) / 16));
-    if (a.parts == 3) hipLaunchKernelGGL(router_simple_kernel<3>, grid, dim3(64), 0, stream, a);
-    else hipLaunchKernelGGL(router_simple_kernel<1>, grid, dim3(64), 0, stream, a);
-    return hipGetLastError();
+    const Choice c = choose(a.T, a.H, a.E, a.parts);
+    const bool f32 = a.parts == 3;
+    switch (c.kernel) {
+        case kSmall16: return f32 ? launch_small<Small<1, 3, 4>>(a, stream) : launch_small<Small<1, 1, 4>>(a, stream);
+        case kSmall32: return f32 ? launch_small<Small<2, 3, 2>>(a, stream) : launch_small<Small<2, 1, 2>>(a, stream);
+        case kTile32x64: return launch_tile<Tile<32, 1, 8, 128, 3>>(a, c.splits, stream);
+        case kTile64x64:
+            return f32 ? launch_tile<Tile<64, 1, 8, 128, 3>>(a, c.splits, stream)
+                       : launch_tile<Tile<64, 1, 8, 128, 1>>(a, c.splits, stream);
+        case kTile64x128:
+            return f32 ? launch_tile<Tile<64, 2, 8, 64, 3>>(a, c.splits, stream)
+                       : launch_tile<Tile<64, 2, 8, 128, 1>>(a, c.splits, stream);
+        case kTile128x128: return launch_tile<Tile<128, 2, 8, 64, 3>>(a, c.splits, stream);
+        case kTile128x192: return launch_tile<Tile<128, 3, 4, 128, 1>>(a, c.splits, stream);
+        case kTile128x256: return launch_tile<Tile<128, 4, 4, 128, 1>>(a, c.splits, stream);
+    }
+    return hipErrorInvalidValue;
 }
 
 }  // namespace moe

@@ -52,6 +52,22 @@ def test_router_exact(gpu, T, H, E, wt):
     assert torch.equal(got.double(), want)
 
 
+# every tile shape, whole and with ragged tokens, experts and columns, in one piece and split
+TILES = [(257, 1056, 256), (600, 4128, 256), (1500, 2080, 100), (3000, 480, 60), (4200, 7168, 64), (8191, 288, 256),
+         (8300, 96, 200), (8300, 160, 300), (9000, 1120, 257), (16400, 160, 128), (16385, 64, 385), (20000, 96, 512),
+         (70000, 32, 64)]
+
+
+@pytest.mark.parametrize("wt", [BF16, F32])
+@pytest.mark.parametrize("T,H,E", TILES)
+def test_router_exact_tiles(gpu, T, H, E, wt):
+    print(f"router T={T} H={H} E={E} {wt}", flush=True)
+    x, w = whole(T, H, E, wt, T + E, gpu)
+    got = run(x, w)
+    want = x.double() @ w.double().t().contiguous()
+    assert torch.equal(got.double(), want)
+
+
 @pytest.mark.parametrize("wt", [BF16, F32])
 @pytest.mark.parametrize("T,H,E", [(1, 7168, 256), (130, 7168, 256), (700, 4096, 64), (5000, 1024, 384)])
 def test_router_random(gpu, T, H, E, wt):
