@@ -93,7 +93,7 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // c ^ ((r >> 1) & 7) of its run: a ds_read_b128 is conflict-free where lanes l, l^2, l^4, l^6 take different
 // 16-byte slots modulo 128 bytes, which this gives for 16 consecutive rows at one chunk.  Reading x into
 // registers directly puts neighbouring lanes on different rows, which the address unit takes one lane at a
-// time (128 x 7168 x 256: 10.0 us against 7.1 through LDS).
+// time (a kernel of 16-token tiles at 128 x 7168 x 256: 10.0 us against 7.1 through LDS).
 __device__ __forceinline__ int swizzle(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
 
 // The sum over the parts of an FP32 weight: the first parts' products in one accumulator, those of the
@@ -119,93 +119,82 @@ struct Sums {
     }
 };
 
-// ---- few tokens: one workgroup per MT x 16 tokens and 16 experts, in one launch
+// ---- up to 16 tokens: one workgroup per 16 experts, in one launch
 //
-// Latency-bound: the 16 waves split the columns, wave w taking every 16th run of 64, each with its loads of
-// U runs in flight at once (x through its own piece of LDS, the weights straight into registers, 1 KiB a
-// load), and add up through LDS in the order of the waves.
-template <int MT_, int P_, int U_>
-struct Small {
-    static constexpr int MT = MT_, P = P_, U = U_, W = 16;
-    static constexpr int RUN = MT * 2048;  // bytes of one run of the workgroup's tokens
-    static constexpr int XS = W * U * RUN, RED = W * MT * 1024, LDS = XS > RED ? XS : RED;
-    static_assert(LDS <= 160 * 1024, "fits the LDS");
-};
+// Latency-bound (1 x 7168 x 256: 4.6 us on the GPU): the 16 waves split the columns, wave w taking every 16th
+// run of 64, each with its loads of kRuns runs in flight at once (x through its own piece of LDS, the weights
+// straight into registers, 1 KiB a load), and add up through LDS in the order of the waves.
+constexpr int kSmallTokens = 16, kSmallWaves = 16, kRuns = 4;
 
-template <class C>
-__global__ __launch_bounds__(C::W * 64) void router_small_kernel(RouterArgs a) {
-    __shared__ __align__(1024) uint8_t lds[C::LDS];
+template <int P>
+__global__ __launch_bounds__(kSmallWaves * 64) void router_small_kernel(RouterArgs a) {
+    constexpr int RUN = kSmallTokens * 128;  // bytes of one run of x
+    __shared__ __align__(1024) uint8_t lds[kSmallWaves * kRuns * RUN];
+    static_assert(kRuns * RUN >= 1024, "holds the waves' sums");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int KT = a.H / 32, runs = (KT + 1) / 2;
-    const int m0 = blockIdx.y * C::MT * 16;
-    uint64_t xp[C::MT * 2];                          // transfer i: rows 8 i .. 8 i + 8 of the run
-    int xc[C::MT * 2];
+    const int r16 = lane & 15, q = lane >> 4;
+    uint64_t xp[2];                          // transfer i: rows 8 i .. 8 i + 8 of the run
+    int xc[2];
 #pragma unroll
-    for (int i = 0; i < C::MT * 2; ++i) {
+    for (int i = 0; i < 2; ++i) {
         const int row = i * 8 + (lane >> 3);
         xc[i] = swizzle(row, lane & 7);
-        xp[i] = reinterpret_cast<uint64_t>(a.x + (int64_t)min(m0 + row, a.T - 1) * a.x_stride + xc[i] * 8);
+        xp[i] = reinterpret_cast<uint64_t>(a.x + (int64_t)min(row, a.T - 1) * a.x_stride + xc[i] * 8);
     }
-    const uint8_t* wp = a.w + (int64_t)blockIdx.x * KT * C::P * 1024;
-    Sums<C::P, 1, C::MT> acc;
+    const uint8_t* wp = a.w + (int64_t)blockIdx.x * KT * P * 1024;
+    Sums<P, 1, 1> acc;
     acc.clear();
-    const uint32_t mine = lds_addr(lds) + wave * C::U * C::RUN;
-    const uint8_t* xs = lds + wave * C::U * C::RUN;
-    for (int r0 = wave; r0 < runs; r0 += C::U * C::W) {
-        bf16x8 w[C::U][2][C::P];
+    const uint32_t mine = lds_addr(lds) + wave * kRuns * RUN;
+    const uint8_t* xs = lds + wave * kRuns * RUN;
+    for (int r0 = wave; r0 < runs; r0 += kRuns * kSmallWaves) {
+        bf16x8 w[kRuns][2][P];
 #pragma unroll
-        for (int u = 0; u < C::U; ++u) {
-            const int r = r0 + u * C::W;
+        for (int u = 0; u < kRuns; ++u) {
+            const int r = r0 + u * kSmallWaves;
             if (r >= runs) break;
             // a last run of 32 columns: the missing chunks read the run's first, and are not multiplied
             const bool half = 2 * r + 1 >= KT;
 #pragma unroll
-            for (int i = 0; i < C::MT * 2; ++i)
+            for (int i = 0; i < 2; ++i)
                 dma16_stream(xp[i] + (int64_t)r * 128 - (half && xc[i] >= 4 ? xc[i] * 16 : 0),
-                             mine + u * C::RUN + i * 1024);
+                             mine + u * RUN + i * 1024);
         }
 #pragma unroll
-        for (int u = 0; u < C::U; ++u) {
-            const int r = r0 + u * C::W;
+        for (int u = 0; u < kRuns; ++u) {
+            const int r = r0 + u * kSmallWaves;
             if (r >= runs) break;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int p = 0; p < C::P; ++p)
+                for (int p = 0; p < P; ++p)
                     w[u][j][p] = *reinterpret_cast<const bf16x8*>(
-                        wp + ((int64_t)min(2 * r + j, KT - 1) * C::P + p) * 1024 + lane * 16);
+                        wp + ((int64_t)min(2 * r + j, KT - 1) * P + p) * 1024 + lane * 16);
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
-        for (int u = 0; u < C::U; ++u) {
-            const int r = r0 + u * C::W;
+        for (int u = 0; u < kRuns; ++u) {
+            const int r = r0 + u * kSmallWaves;
             if (r >= runs) break;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 if (2 * r + j >= KT) break;
+                const bf16x8 x = *reinterpret_cast<const bf16x8*>(xs + u * RUN + r16 * 128 + swizzle(r16, j * 4 + q) * 16);
 #pragma unroll
-                for (int m = 0; m < C::MT; ++m) {
-                    const int row = m * 16 + (lane & 15);
-                    const bf16x8 x = *reinterpret_cast<const bf16x8*>(xs + u * C::RUN + row * 128 +
-                                                                     swizzle(row, j * 4 + (lane >> 4)) * 16);
-#pragma unroll
-                    for (int p = 0; p < C::P; ++p) acc.add(p, 0, m, w[u][j][p], x);
-                }
+                for (int p = 0; p < P; ++p) acc.add(p, 0, 0, w[u][j][p], x);
             }
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // x is read before the next runs overwrite it
     }
     __syncthreads();
-    v4f(*part)[C::MT][64] = reinterpret_cast<v4f(*)[C::MT][64]>(lds);
-#pragma unroll
-    for (int m = 0; m < C::MT; ++m) part[wave][m][lane] = acc.total(0, m);
+    v4f(*part)[64] = reinterpret_cast<v4f(*)[64]>(lds);
+    part[wave][lane] = acc.total(0, 0);
     __syncthreads();
-    if (wave < C::MT) {
-        v4f sum = part[0][wave][lane];
+    if (wave == 0) {
+        v4f sum = part[0][lane];
 #pragma unroll
-        for (int w = 1; w < C::W; ++w) sum += part[w][wave][lane];
-        const int t = m0 + wave * 16 + (lane & 15);
-        if (t < a.T) store_logits(a.logits, a.E, t, blockIdx.x * 16 + (lane >> 4) * 4, sum);
+        for (int w = 1; w < kSmallWaves; ++w) sum += part[w][lane];
+        if (r16 < a.T) store_logits(a.logits, a.E, r16, blockIdx.x * 16 + q * 4, sum);
     }
 }
 
@@ -365,38 +354,43 @@ __global__ __launch_bounds__(C::THREADS) void router_tile_kernel(TileArgs a) {
     }
 }
 
-// Sums the splits' partial products [splits][n], in their order.
+// Sums the splits' partial products [splits][n], in their order; 8 loads in flight per thread, of V floats
+// (4 where n is a multiple of 4 and large; 1 keeps a small sum on many CUs).
+template <int V>
 __global__ __launch_bounds__(kThreads) void router_reduce_kernel(const float* __restrict__ part, int splits, int64_t n,
                                                                  float* __restrict__ out) {
-    const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+    typedef float vec __attribute__((ext_vector_type(V)));
+    const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * V;
     if (i >= n) return;
-    if (n % 4 == 0) {
-        v4f sum = *reinterpret_cast<const v4f*>(part + i);
-        for (int s = 1; s < splits; ++s) sum += *reinterpret_cast<const v4f*>(part + s * n + i);
-        *reinterpret_cast<v4f*>(out + i) = sum;
-    } else {
-        for (int64_t j = i; j < min(i + 4, n); ++j) {
-            float sum = part[j];
-            for (int s = 1; s < splits; ++s) sum += part[s * n + j];
-            out[j] = sum;
-        }
+    vec sum = {};
+    for (int s0 = 0; s0 < splits; s0 += 8) {
+        vec v[8];
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            if (s0 + s < splits) v[s] = *reinterpret_cast<const vec*>(part + (s0 + s) * n + i);
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            if (s0 + s < splits) sum += v[s];
     }
+    *reinterpret_cast<vec*>(out + i) = sum;
 }
 
 // ---- which kernel
 //
-// Few tokens: the small kernel while its workgroups fit the CUs once (128 x 7168 x 256: 7.1 us, against 15.2
-// for a tile kernel split 28 ways and its second launch), of 32 tokens where 16 no longer fit (512 x 7168 x
-// 256: 12.2 us against 14.9 and 16.2).
-// Then tiles, as small as give one workgroup per CU: 64 tokens x 64 or 128 experts split over K into what the
-// CUs hold (1024 x 7168 x 256: 15.7 us; 64 x 256 tiles 18.5), and above that 128-token tiles, whose operands
-// are read half as often (16384 x 7168 x 256: 71 us against 89), 192 experts wide where that covers E with
-// fewer columns (16384 x 7168 x 384: 86 us against 105 at 256).  FP32 weights hold three times the registers
-// for weights: 128 experts at most, K-steps of 64 columns from 128 on; 32-token tiles where 64 experts at 64
-// tokens leave most CUs without a tile (2048 x 4096 x 64: 10.4 us against 11.9).
+// The tile is the smallest that fills the CUs, split over K into what they hold: small tiles split less, and
+// each split adds a partial sum to write and read; large tiles read their operands less often.  Both sides of
+// each border (us, whole call, operands not in the L2; H 7168, E 256 unless named):
+//   T 16: small kernel 5.5, 32 x 64 split 14 ways 6.5; T 32: 11.4, 7.0 (the small kernel has 16 workgroups).
+//   T 256: 32 x 64 in 8 splits 7.6, 32 x 128 in 8 8.1; T 512: 10.5, 9.5.  E 64, H 4096: T 4096 32 x 64 in two
+//   splits 12.8, 64 x 64 in four 13.5.
+//   T 1024: 32 x 128 in 4 splits 13.9, 64 x 128 in 8 15.5; T 2048: 22.3, 20.9.
+//   T 8192: 64 x 128 45.2, 128 x 256 in 4 splits 43.5; T 16384: 89, 71.  192 experts wide where that covers E
+//   with fewer columns (E 384, T 16384: 86, 105 at 256).
+// FP32 weights (three times the registers for weights, so 128 experts at most): T 128 32 x 64 in 14 splits 8.5,
+// 64 x 64 in 14 9.3; T 1024: 24.3, 18.5, 64 x 128 in 8 20.2; T 16384: 64 x 128 178, 128 x 128 140.
 constexpr int kCus = 256;
 
-enum Kernel { kSmall16, kSmall32, kTile32x64, kTile64x64, kTile64x128, kTile128x128, kTile128x192, kTile128x256 };
+enum Kernel { kSmall, kTile32x64, kTile32x128, kTile64x64, kTile64x128, kTile128x128, kTile128x192, kTile128x256 };
 struct Choice {
     Kernel kernel;
     int splits;
@@ -405,39 +399,30 @@ struct Choice {
 int div_up(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 Choice choose(int T, int H, int E, int parts) {
-    const int64_t blocks = div_up(E, 16);
-    if (div_up(T, 16) * blocks <= kCus) return {kSmall16, 1};
-    if (div_up(T, 32) * blocks <= kCus) return {kSmall32, 1};
-    Kernel k;
-    int bm = 64, bn = 128, bk = 128;
-    if (E <= 64) {
-        bn = 64;
-        k = kTile64x64;
-        if (parts == 3 && div_up(T, 64) <= kCus / 4) {
-            bm = 32;
-            k = kTile32x64;
-        }
-    } else if ((int64_t)div_up(T, 64) * div_up(E, 128) <= kCus || (parts == 1 && E <= 128)) {
-        k = kTile64x128;
-        if (parts == 3) bk = 64;
-    } else if (parts == 3) {
-        bm = 128;
-        bk = 64;
-        k = kTile128x128;
-    } else {
-        bm = 128;
-        bn = div_up(E, 192) * 192 < div_up(E, 256) * 256 ? 192 : 256;
-        k = bn == 192 ? kTile128x192 : kTile128x256;
+    if (T <= kSmallTokens) return {kSmall, 1};
+    auto tiles = [&](int bm, int bn) { return (int64_t)div_up(T, bm) * div_up(E, bn); };
+    auto split = [&](Kernel k, int bm, int bn, int bk) {
+        // at least four K-steps each
+        const int64_t s = std::min<int64_t>(kCus / tiles(bm, bn), div_up(H, bk) / 4);
+        return Choice{k, (int)std::max<int64_t>(s, 1)};
+    };
+    if (parts == 3) {
+        if (tiles(32, 64) <= kCus / 4) return split(kTile32x64, 32, 64, 128);
+        if (E <= 64 || tiles(64, 64) <= kCus) return split(kTile64x64, 64, 64, 128);
+        if (tiles(64, 128) <= kCus) return split(kTile64x128, 64, 128, 64);
+        return split(kTile128x128, 128, 128, 64);
     }
-    const int64_t tiles = (int64_t)div_up(T, bm) * div_up(E, bn);
-    const int64_t splits = std::min<int64_t>(kCus / std::max<int64_t>(tiles, 1), div_up(H, bk) / 4);
-    return {k, (int)std::max<int64_t>(splits, 1)};
+    if (tiles(32, 64) <= (E <= 64 ? kCus / 2 : kCus / 8)) return split(kTile32x64, 32, 64, 128);
+    if (E <= 64) return split(kTile64x64, 64, 64, 128);
+    if (tiles(32, 128) <= kCus / 4) return split(kTile32x128, 32, 128, 128);
+    if (E <= 128 || tiles(64, 128) <= kCus) return split(kTile64x128, 64, 128, 128);
+    if (div_up(E, 192) * 192 < div_up(E, 256) * 256) return split(kTile128x192, 128, 192, 128);
+    return split(kTile128x256, 128, 256, 128);
 }
 
-template <class C>
+template <int P>
 hipError_t launch_small(const RouterArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)div_up(a.E, 16), (unsigned)div_up(a.T, C::MT * 16));
-    hipLaunchKernelGGL(router_small_kernel<C>, grid, dim3(C::W * 64), 0, stream, a);
+    hipLaunchKernelGGL(router_small_kernel<P>, dim3((unsigned)div_up(a.E, 16)), dim3(kSmallWaves * 64), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -448,8 +433,12 @@ hipError_t launch_tile(const RouterArgs& r, int splits, hipStream_t stream) {
     hipLaunchKernelGGL(router_tile_kernel<C>, dim3((unsigned)div_up(total, 8) * 8), dim3(C::THREADS), 0, stream, a);
     if (splits > 1) {
         const int64_t n = (int64_t)r.T * r.E;
-        hipLaunchKernelGGL(router_reduce_kernel, dim3((unsigned)div_up(n, 4 * kThreads)), dim3(kThreads), 0, stream,
-                           r.partial, splits, n, r.logits);
+        if (n % 4 == 0 && n >= (int64_t)4 * kThreads * kCus)
+            hipLaunchKernelGGL(router_reduce_kernel<4>, dim3((unsigned)div_up(n, 4 * kThreads)), dim3(kThreads), 0, stream,
+                               r.partial, splits, n, r.logits);
+        else
+            hipLaunchKernelGGL(router_reduce_kernel<1>, dim3((unsigned)div_up(n, kThreads)), dim3(kThreads), 0, stream,
+                               r.partial, splits, n, r.logits);
     }
     return hipGetLastError();
 }
@@ -475,9 +464,11 @@ hipError_t launch_router_logits(const RouterArgs& a, hipStream_t stream) {
     const Choice c = choose(a.T, a.H, a.E, a.parts);
     const bool f32 = a.parts == 3;
     switch (c.kernel) {
-        case kSmall16: return f32 ? launch_small<Small<1, 3, 4>>(a, stream) : launch_small<Small<1, 1, 4>>(a, stream);
-        case kSmall32: return f32 ? launch_small<Small<2, 3, 2>>(a, stream) : launch_small<Small<2, 1, 2>>(a, stream);
-        case kTile32x64: return launch_tile<Tile<32, 1, 8, 128, 3>>(a, c.splits, stream);
+        case kSmall: return f32 ? launch_small<3>(a, stream) : launch_small<1>(a, stream);
+        case kTile32x64:
+            return f32 ? launch_tile<Tile<32, 1, 8, 128, 3>>(a, c.splits, stream)
+                       : launch_tile<Tile<32, 1, 8, 128, 1>>(a, c.splits, stream);
+        case kTile32x128: return launch_tile<Tile<32, 2, 8, 128, 1>>(a, c.splits, stream);
         case kTile64x64:
             return f32 ? launch_tile<Tile<64, 1, 8, 128, 3>>(a, c.splits, stream)
                        : launch_tile<Tile<64, 1, 8, 128, 1>>(a, c.splits, stream);
