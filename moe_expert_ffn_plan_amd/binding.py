@@ -155,10 +155,17 @@ def _ptr(t, dtype, name, device=None, numel=None):
     return ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without building a torch.cuda.Stream, which takes 2.7 us of a call's 6.4.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    if _raw_stream is None or _device is None:
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return ctypes.c_void_p(_raw_stream(_device()))
 
 
 def capacity_rows(shape: MoeShape) -> int:
