@@ -4,8 +4,10 @@
 //   the block's largest magnitude to 448 or below.
 //
 // HBM-bound: a row is read once and written once (BF16 throughout: 2 + 2 bytes in, 2 + 2 + 1 + 1/32 out
-// per element).  A lane owns 8 consecutive columns at a time (16 bytes of BF16), so a block of 32 columns
-// is four neighbouring lanes and its maximum two DPP steps.
+// per element; 16384 x 7168: 1.06 GB in 180 us, 5.9 TB/s, where a copy of 2 GiB reaches 4.9 TB/s).  A lane owns
+// 8 consecutive columns at a time (16 bytes of BF16), so a block of 32 columns is four neighbouring lanes and
+// its maximum two DPP steps; the row stays in registers between the sum and the outputs.  Loads with the
+// non-temporal hint lost (2048 x 4096: 11.9 -> 16.9 us, the inputs then miss the memory-side cache).
 //
 // Roundings: h is one FP32 addition; the squares are summed in FP64 (their sum decides the scale of every
 // element of the row, and |h| above 2^64 must not overflow); v is two FP32 products.  The scale compares
@@ -50,35 +52,44 @@ struct Raw<MOE_F32> {
     __device__ __forceinline__ float at(int j) const { return v[j >> 2][j & 3]; }
 };
 
-template <int TYPE>
+// LATER: not read again before a whole layer has run, so past the caches.
+template <int TYPE, bool LATER>
 __device__ __forceinline__ void store8(void* base, int64_t i, const float (&f)[8]) {
+    auto put = [](auto v, auto* p) {
+        if constexpr (LATER) __builtin_nontemporal_store(v, p);
+        else *p = v;
+    };
     if constexpr (TYPE == MOE_BF16) {
         v4i o;
 #pragma unroll
         for (int q = 0; q < 4; ++q) o[q] = (int)pack_bf16(f[2 * q], f[2 * q + 1]);
-        *reinterpret_cast<v4i*>(static_cast<uint16_t*>(base) + i) = o;
+        put(o, reinterpret_cast<v4i*>(static_cast<uint16_t*>(base) + i));
     } else {
         v4f* p = reinterpret_cast<v4f*>(static_cast<float*>(base) + i);
-        p[0] = v4f{f[0], f[1], f[2], f[3]};
-        p[1] = v4f{f[4], f[5], f[6], f[7]};
+        put(v4f{f[0], f[1], f[2], f[3]}, p);
+        put(v4f{f[4], f[5], f[6], f[7]}, p + 1);
     }
 }
 
-// h of 8 columns.
+// x and the residual of 8 columns, and their h.
 template <int XT, int RT>
-__device__ __forceinline__ void load_h(const NormArgs& a, int64_t row, int c, float (&h)[8]) {
+struct Cell {
     Raw<XT> x;
-    x.load(a.x, row * a.x_stride + c);
-    if (a.residual) {
-        Raw<RT> r;
-        r.load(a.residual, row * a.residual_stride + c);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = x.at(j) + r.at(j);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = x.at(j);
+    Raw<RT> r;
+    __device__ __forceinline__ void load(const NormArgs& a, int64_t row, int c) {
+        x.load(a.x, row * a.x_stride + c);
+        if (a.residual) r.load(a.residual, row * a.residual_stride + c);
     }
-}
+    __device__ __forceinline__ void sum(const NormArgs& a, float (&h)[8]) const {
+        if (a.residual) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[j] = x.at(j) + r.at(j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) h[j] = x.at(j);
+        }
+    }
+};
 
 // Maximum over each four neighbouring lanes (quad_perm moves, inside the quad) of non-negative floats as
 // bit patterns, which order the same way and put NaN on top.
@@ -101,7 +112,7 @@ __device__ __forceinline__ bool near_border(uint32_t bits) {
 // scale_code of the block's maximum formed in FP64, for a block near a border; reads the columns again
 // (before residual_out, which may be the same memory, is written).  All four lanes of the block call it.
 template <int XT, int RT, int WT>
-__device__ __noinline__ int exact_code(const NormArgs& a, int64_t row, int c, double rstd) {
+__device__ __forceinline__ int exact_code(const NormArgs& a, int64_t row, int c, double rstd) {
     Raw<XT> x;
     Raw<RT> r;
     Raw<WT> w;
@@ -146,45 +157,128 @@ __device__ __forceinline__ void finish8(const NormArgs& a, int64_t row, int c, c
         *reinterpret_cast<int2*>(a.x_q + row * a.H + c) = make_int2(q0, q1);
         if ((c & 31) == 0) a.x_sf[row * (a.H / 32) + c / 32] = (uint8_t)code;
     }
-    if (a.residual_out) store8<RT>(a.residual_out, row * a.residual_out_stride + c, h);
-    if (a.y) store8<MOE_BF16>(a.y, row * a.H + c, v);
+    if (a.residual_out) store8<RT, true>(a.residual_out, row * a.residual_out_stride + c, h);
+    if (a.y) store8<MOE_BF16, false>(a.y, row * a.H + c, v);
 }
 
-constexpr int kThreads = 256;
+template <int CTRL>
+__device__ __forceinline__ double add_dpp(double v) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, CTRL, 0xF, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, true);
+    return v + __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+// Sum over the wave, in all lanes: inside rows of 16 lanes by DPP, across rows and halves by swaps.
+__device__ __forceinline__ double wave_sum(double v) {
+    v = add_dpp<0xB1>(v);   // lane ^ 1
+    v = add_dpp<0x4E>(v);   // lane ^ 2
+    v = add_dpp<0x141>(v);  // lane ^ 7
+    v = add_dpp<0x140>(v);  // lane ^ 15
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const uint64_t b = (uint64_t)__double_as_longlong(v);
+        const uint32_t lo = (uint32_t)b, hi = (uint32_t)(b >> 32);
+        const auto l = half ? __builtin_amdgcn_permlane32_swap(lo, lo, false, false)
+                            : __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+        const auto h = half ? __builtin_amdgcn_permlane32_swap(hi, hi, false, false)
+                            : __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+        v = __longlong_as_double((long long)(((uint64_t)h[0] << 32) | l[0])) +
+            __longlong_as_double((long long)(((uint64_t)h[1] << 32) | l[1]));
+    }
+    return v;
+}
+// Sum over the workgroup, in all threads; part: one double per wave.
+__device__ __forceinline__ double group_sum(double v, double* part) {
+    v = wave_sum(v);
+    const int waves = blockDim.x / 64;
+    if (waves == 1) return v;
+    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = v;
+    __syncthreads();
+    v = 0.0;
+    for (int i = 0; i < waves; ++i) v += part[i];
+    return v;
+}
 
-// One workgroup per row, two passes over it.
+__device__ __forceinline__ double square_sum(const float (&h)[8], double sum) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fma((double)h[j], (double)h[j], sum);
+    return sum;
+}
+
+constexpr int kMaxThreads = 1024;
+
+// One workgroup per row, the row in registers: V cells of 8 columns per thread, the threads' first cells side
+// by side.
+template <int XT, int RT, int WT, int V>
+__global__ __launch_bounds__(kMaxThreads) void norm_row_kernel(NormArgs a) {
+    __shared__ double part[kMaxThreads / 64];
+    const int64_t row = blockIdx.x;
+    const int step = blockDim.x * 8;
+    Cell<XT, RT> cell[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) cell[i].load(a, row, min((int)threadIdx.x * 8 + i * step, a.H - 8));
+    Raw<WT> w[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) w[i].load(a.weight, min((int)threadIdx.x * 8 + i * step, a.H - 8));
+    float h[V][8];
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        cell[i].sum(a, h[i]);
+        if ((int)threadIdx.x * 8 + i * step < a.H) sum = square_sum(h[i], sum);
+    }
+    sum = group_sum(sum, part);
+    const double rstd = 1.0 / sqrt(sum / a.H + (double)a.eps);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int c = threadIdx.x * 8 + i * step;
+        if (c < a.H) finish8<XT, RT, WT>(a, row, c, h[i], w[i], (float)rstd, rstd);
+    }
+}
+
+// Rows that the registers of a workgroup do not hold: two passes over the row.
 template <int XT, int RT, int WT>
-__global__ __launch_bounds__(kThreads) void norm_quant_kernel(NormArgs a) {
-    __shared__ double part[kThreads / 64];
+__global__ __launch_bounds__(kMaxThreads) void norm_long_kernel(NormArgs a) {
+    __shared__ double part[kMaxThreads / 64];
     const int64_t row = blockIdx.x;
     double sum = 0.0;
-    for (int c = threadIdx.x * 8; c < a.H; c += kThreads * 8) {
+    for (int c = threadIdx.x * 8; c < a.H; c += kMaxThreads * 8) {
+        Cell<XT, RT> cell;
         float h[8];
-        load_h<XT, RT>(a, row, c, h);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fma((double)h[j], (double)h[j], sum);
+        cell.load(a, row, c);
+        cell.sum(a, h);
+        sum = square_sum(h, sum);
     }
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) sum += __shfl_xor(sum, s);
-    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = sum;
-    __syncthreads();
-    sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 64; ++i) sum += part[i];
-    const double rstd_d = 1.0 / sqrt(sum / a.H + (double)a.eps);
-    const float rstd = (float)rstd_d;
-    for (int c = threadIdx.x * 8; c < a.H; c += kThreads * 8) {
-        float h[8];
-        load_h<XT, RT>(a, row, c, h);
+    sum = group_sum(sum, part);
+    const double rstd = 1.0 / sqrt(sum / a.H + (double)a.eps);
+    for (int c = threadIdx.x * 8; c < a.H; c += kMaxThreads * 8) {
+        Cell<XT, RT> cell;
         Raw<WT> w;
+        float h[8];
+        cell.load(a, row, c);
         w.load(a.weight, c);
-        finish8<XT, RT, WT>(a, row, c, h, w, rstd, rstd_d);
+        cell.sum(a, h);
+        finish8<XT, RT, WT>(a, row, c, h, w, (float)rstd, rstd);
     }
+}
+
+template <int XT, int RT, int WT, int V>
+hipError_t launch_row(const NormArgs& a, hipStream_t stream) {
+    const int threads = (a.H / 8 + V * 64 - 1) / (V * 64) * 64;
+    hipLaunchKernelGGL((norm_row_kernel<XT, RT, WT, V>), dim3((unsigned)a.T), dim3((unsigned)threads), 0, stream, a);
+    return hipGetLastError();
 }
 
 template <int XT, int RT, int WT>
 hipError_t launch(const NormArgs& a, hipStream_t stream) {
-    hipLaunchKernelGGL((norm_quant_kernel<XT, RT, WT>), dim3((unsigned)a.T), dim3(kThreads), 0, stream, a);
+    // One cell per thread where rows are few (128 x 7168: 3.9 us against 4.1 with two and 4.7 with four) or
+    // short (16384 x 1024: 28.8, 30.2, 29.5), else two: more loads in flight per thread, and at four too few
+    // threads (16384 x 7168: 191, 180, 186).
+    const int cells = a.H / 8;
+    if (cells <= 256 || (a.T <= 256 && cells <= kMaxThreads)) return launch_row<XT, RT, WT, 1>(a, stream);
+    if (cells <= 2 * kMaxThreads) return launch_row<XT, RT, WT, 2>(a, stream);
+    if (cells <= 4 * kMaxThreads) return launch_row<XT, RT, WT, 4>(a, stream);
+    hipLaunchKernelGGL((norm_long_kernel<XT, RT, WT>), dim3((unsigned)a.T), dim3(kMaxThreads), 0, stream, a);
     return hipGetLastError();
 }
 
