@@ -79,6 +79,10 @@ __device__ __forceinline__ void store_logits(float* logits, int E, int64_t t, in
 __device__ __forceinline__ void dma16_stream(uint64_t addr, uint32_t lds) {
     asm volatile("global_load_lds_dwordx4 %0, off nt" ::"v"(addr), "{m0}"(lds) : "memory");
 }
+// The same at a wave-uniform base and a 32-bit offset per lane, kept in the L2.
+__device__ __forceinline__ void dma16_at(uint32_t off, const void* base, uint32_t lds) {
+    asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void wait_and_barrier() {
     __builtin_amdgcn_sched_barrier(0);
@@ -89,12 +93,17 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
     return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)p);
 }
 
-// The x operand lies in LDS as rows of whole 128-byte runs (64 columns), 16-byte chunk c of row r at chunk
-// c ^ ((r >> 1) & 7) of its run: a ds_read_b128 is conflict-free where lanes l, l^2, l^4, l^6 take different
-// 16-byte slots modulo 128 bytes, which this gives for 16 consecutive rows at one chunk.  Reading x into
-// registers directly puts neighbouring lanes on different rows, which the address unit takes one lane at a
-// time (a kernel of 16-token tiles at 128 x 7168 x 256: 10.0 us against 7.1 through LDS).
-__device__ __forceinline__ int swizzle(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
+// The x operand lies in LDS as rows of CH 16-byte chunks (64 or 128 columns), chunk c of row r at a place
+// that gives the 16 rows that a ds_read_b128 takes at one chunk 16 different slots modulo the 256 bytes of the
+// banks: rows of 256 bytes swap chunks by r, rows of 128 bytes, of which two fit, by r >> 1.  (Rows of 256
+// bytes by r >> 1 were two-way conflicts, half of the LDS time.)  Reading x into registers directly puts
+// neighbouring lanes on different rows, which the address unit takes one lane at a time (a kernel of 16-token
+// tiles at 128 x 7168 x 256: 10.0 us against 7.1 through LDS).
+template <int CH>
+__device__ __forceinline__ int swizzle(int row, int chunk) {
+    static_assert(CH == 8 || CH == 16, "128 or 256 bytes");
+    return CH == 16 ? chunk ^ (row & 15) : chunk ^ ((row >> 1) & 7);
+}
 
 // The sum over the parts of an FP32 weight: the first parts' products in one accumulator, those of the
 // other two in another, so that the small terms do not round the large sum twice more per step.
@@ -139,7 +148,7 @@ __global__ __launch_bounds__(kSmallWaves * 64) void router_small_kernel(RouterAr
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int row = i * 8 + (lane >> 3);
-        xc[i] = swizzle(row, lane & 7);
+        xc[i] = swizzle<8>(row, lane & 7);
         xp[i] = reinterpret_cast<uint64_t>(a.x + (int64_t)min(row, a.T - 1) * a.x_stride + xc[i] * 8);
     }
     const uint8_t* wp = a.w + (int64_t)blockIdx.x * KT * P * 1024;
@@ -179,7 +188,7 @@ __global__ __launch_bounds__(kSmallWaves * 64) void router_small_kernel(RouterAr
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 if (2 * r + j >= KT) break;
-                const bf16x8 x = *reinterpret_cast<const bf16x8*>(xs + u * RUN + r16 * 128 + swizzle(r16, j * 4 + q) * 16);
+                const bf16x8 x = *reinterpret_cast<const bf16x8*>(xs + u * RUN + r16 * 128 + swizzle<8>(r16, j * 4 + q) * 16);
 #pragma unroll
                 for (int p = 0; p < P; ++p) acc.add(p, 0, 0, w[u][j][p], x);
             }
@@ -207,11 +216,12 @@ __global__ __launch_bounds__(kSmallWaves * 64) void router_small_kernel(RouterAr
 // and frees the one before it; producers wait for their own transfers ahead of it, consumers for their LDS
 // reads, and a consumer has the next step's first fragments in flight before it starts the last products
 // of its step.
-// Where it goes (16384 x 7168 x 256, 128 x 256 tiles, two splits, 61 of 71 us): x alone streams in 41 us, the
-// products with both operands in the L2 take 45.  The L1 delivers 64 bytes a clock and a CU moves 24 KiB per
-// 32 columns, 384 of the 512 clocks of its matrix instructions; 64 x 256 tiles need no second split but move
-// 20 KiB for half of the products and take 77 us.  BK of 64 (128-byte runs of each row) streams x at
-// 3.9 TB/s, 128 at 4.5, so a stage holds 128 columns where registers allow.
+// Where it goes (16384 x 7168 x 256, 128 x 256 tiles in two splits, 61 us of the call's 70): the matrix cores
+// are busy for 54% of the CUs' 107,000 clocks; x alone streams in 35 us and the products alone, with both
+// operands in the L2, take 45.  The L1 takes loads in order at about 50 bytes a clock, so the weights wait
+// behind x from memory: a CU moves 24 KiB per 32 columns, 480 of the 512 clocks of its matrix instructions.
+// 64 x 256 tiles need no second split but move 20 KiB for half of the products and take 75 us.  Writing the
+// result (all workgroups end together) and adding the splits take the other 20 us.
 template <int BM_, int NF_, int NS_, int BK_, int P_>
 struct Tile {
     static constexpr int BM = BM_, NF = NF_, NS = NS_, BK = BK_, P = P_;
@@ -219,7 +229,7 @@ struct Tile {
     static constexpr int KS = BK / 32, MT = BM / 16, CH = BK / 8;       // 16-byte chunks per row and step
     static constexpr int STAGE = BM * BK * 2, PER = STAGE / 1024 / PW;  // transfers per producer and stage
     static constexpr int GS = MT < 4 ? MT : 4, GPK = MT / GS, NG = KS * GPK;  // fragment groups of a step
-    static_assert(BK % 64 == 0 && MT % GS == 0 && NG % 2 == 0, "whole runs; two fragment buffers alternate");
+    static_assert((BK == 64 || BK == 128) && MT % GS == 0 && NG % 2 == 0, "whole runs; two fragment buffers alternate");
     static_assert(STAGE % (1024 * PW) == 0 && NS >= 2 && NS * STAGE <= 160 * 1024, "the ring");
     static_assert(PER * (NS - 2) < 63, "vmcnt counts to 63");
 };
@@ -254,7 +264,7 @@ __global__ __launch_bounds__(C::THREADS) void router_tile_kernel(TileArgs a) {
 #pragma unroll
         for (int i = 0; i < C::PER; ++i) {
             const int slot = (pw + i * C::PW) * 64 + lane, row = slot / C::CH;
-            chunk[i] = swizzle(row, slot % C::CH);
+            chunk[i] = swizzle<C::CH>(row, slot % C::CH);
             src[i] = reinterpret_cast<uint64_t>(a.r.x + (int64_t)min(m0 + row, a.r.T - 1) * a.r.x_stride + chunk[i] * 8);
         }
         auto issue = [&](int step, int stage) {
@@ -284,55 +294,55 @@ __global__ __launch_bounds__(C::THREADS) void router_tile_kernel(TileArgs a) {
         wp[n] = a.r.w + (int64_t)min(n0 / 16 + wave * C::NF + n, (a.r.E + 15) / 16 - 1) * KT * C::P * 1024;
     const uint32_t lane16 = lane * 16;
     bf16x8 w[C::KS][C::P][C::NF];
-    auto load = [&](int k, bf16x8 (&b)[C::P][C::NF]) {
-        const int64_t kk = min(k, KT - 1);
-#pragma unroll
-        for (int p = 0; p < C::P; ++p)
-#pragma unroll
-            for (int n = 0; n < C::NF; ++n)
-                b[p][n] = *reinterpret_cast<const bf16x8*>(wp[n] + (kk * C::P + p) * 1024 + lane16);
+    auto load = [&](int k, int p, int n) {
+        return *reinterpret_cast<const bf16x8*>(wp[n] + ((int64_t)min(k, KT - 1) * C::P + p) * 1024 + lane16);
     };
     bf16x8 xg[2][C::GS];
     const int r16 = lane & 15, q = lane >> 4;
-    const uint32_t x_even = r16 * (C::BK * 2) + swizzle(r16, q) * 16;
-    const uint32_t x_odd = r16 * (C::BK * 2) + swizzle(r16, 4 + q) * 16;
-    auto read = [&](const uint8_t* stage, int g, bf16x8 (&x)[C::GS]) {
-        const int ks = g / C::GPK;
-        const uint8_t* p = stage + (ks & 1 ? x_odd : x_even) + (ks >> 1) * 128;
+    uint32_t x_at[C::KS];
 #pragma unroll
-        for (int i = 0; i < C::GS; ++i)
-            x[i] = *reinterpret_cast<const bf16x8*>(p + (g % C::GPK * C::GS + i) * 16 * (C::BK * 2));
+    for (int ks = 0; ks < C::KS; ++ks) x_at[ks] = r16 * (C::BK * 2) + swizzle<C::CH>(r16, ks * 4 + q) * 16;
+    auto read = [&](const uint8_t* stage, int g, int i) {  // fragment i of group g
+        return *reinterpret_cast<const bf16x8*>(stage + x_at[g / C::GPK] + (g % C::GPK * C::GS + i) * 16 * (C::BK * 2));
     };
     Sums<C::P, C::NF, C::MT> acc;
     acc.clear();
-    auto multiply = [&](int g, const bf16x8 (&x)[C::GS]) {
+    auto multiply = [&](int g, int p, int n) {
 #pragma unroll
-        for (int p = 0; p < C::P; ++p)
-#pragma unroll
-            for (int n = 0; n < C::NF; ++n)
-#pragma unroll
-                for (int i = 0; i < C::GS; ++i) acc.add(p, n, g % C::GPK * C::GS + i, w[g / C::GPK][p][n], x[i]);
+        for (int i = 0; i < C::GS; ++i)
+            acc.add(p, n, g % C::GPK * C::GS + i, w[g / C::GPK][p][n], xg[g & 1][i]);
     };
 
 #pragma unroll
-    for (int k = 0; k < C::KS; ++k) load(s_begin * C::KS + k, w[k]);
+    for (int k = 0; k < C::KS; ++k)
+#pragma unroll
+        for (int p = 0; p < C::P; ++p)
+#pragma unroll
+            for (int n = 0; n < C::NF; ++n) w[k][p][n] = load(s_begin * C::KS + k, p, n);
     asm volatile("s_barrier" ::: "memory");
-    read(ring, 0, xg[0]);
+#pragma unroll
+    for (int i = 0; i < C::GS; ++i) xg[0][i] = read(ring, 0, i);
     int stage = 0;
     for (int s = 0; s < n_steps - 1; ++s) {
         const int next = stage == C::NS - 1 ? 0 : stage + 1;
 #pragma unroll
         for (int g = 0; g < C::NG; ++g) {
-            if (g < C::NG - 1) {
-                read(ring + stage * C::STAGE, g + 1, xg[(g + 1) & 1]);
-            } else {
-                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-                read(ring + next * C::STAGE, 0, xg[0]);
+            const uint8_t* from = ring + (g < C::NG - 1 ? stage : next) * C::STAGE;
+            if (g == C::NG - 1) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            // a load takes its wave's issue slot for as long as the L1 needs to take its kilobyte: one after
+            // the last products of each register that it fills, and the LDS reads between products as well
+#pragma unroll
+            for (int u = 0; u < C::P * C::NF; ++u) {
+                const int p = u / C::NF, n = u % C::NF;
+#pragma unroll
+                for (int i = u * C::GS / (C::P * C::NF); i < (u + 1) * C::GS / (C::P * C::NF); ++i)
+                    xg[(g + 1) & 1][i] = read(from, g < C::NG - 1 ? g + 1 : 0, i);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(g, p, n);
+                if (g % C::GPK == C::GPK - 1)
+                    w[g / C::GPK][p][n] = load((s_begin + s + 1) * C::KS + g / C::GPK, p, n);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(g, xg[g & 1]);
-            if (g % C::GPK == C::GPK - 1) load((s_begin + s + 1) * C::KS + g / C::GPK, w[g / C::GPK]);
-            __builtin_amdgcn_sched_barrier(0);
         }
         stage = next;
     }
@@ -340,8 +350,12 @@ __global__ __launch_bounds__(C::THREADS) void router_tile_kernel(TileArgs a) {
 #pragma unroll
     for (int g = 0; g < C::NG; ++g) {
         if (g / C::GPK >= valid) break;
-        if (g < C::NG - 1) read(ring + stage * C::STAGE, g + 1, xg[(g + 1) & 1]);
-        multiply(g, xg[g & 1]);
+        if (g < C::NG - 1) {
+#pragma unroll
+            for (int i = 0; i < C::GS; ++i) xg[(g + 1) & 1][i] = read(ring + stage * C::STAGE, g + 1, i);
+        }
+#pragma unroll
+        for (int u = 0; u < C::P * C::NF; ++u) multiply(g, u / C::NF, u % C::NF);
     }
     float* out = a.splits > 1 ? a.r.partial + (int64_t)split * a.r.T * a.r.E : a.r.logits;
 #pragma unroll
@@ -351,6 +365,122 @@ __global__ __launch_bounds__(C::THREADS) void router_tile_kernel(TileArgs a) {
 #pragma unroll
         for (int n = 0; n < C::NF; ++n)
             store_logits(out, a.r.E, t, n0 + (wave * C::NF + n) * 16 + q * 4, acc.total(n, m));
+    }
+}
+
+// ---- very many tokens at 257 to 384 experts: tiles of 256 tokens x 384 experts
+//
+// Held back by the clock (65536 x 7168 x 384 runs the tile kernel's matrix instructions at 1.7 GHz), so the
+// tile that moves the fewest bytes per product wins: 288 us against 343 for 128 x 192 (tiles of 256 x 256 at
+// 256 experts do not: 244 against 234).  Eight waves, two per SIMD, each own 128 tokens x 96 experts in 192
+// registers; both operands come through a ring of four 32-column stages in all of the LDS, transferred by
+// the waves themselves.  A wave reads its six weight fragments once per stage and its eight of x one by one,
+// two ahead; the barrier that publishes the next stage stands ahead of the last fragment's products, among
+// which the next weights replace the old.  Halves of x's 128-byte lines arrive a step apart, so x is kept in
+// the L2 (with the non-temporal hint 1.6 times its bytes came from memory: 312 us).
+struct Big {
+    static constexpr int BM = 256, NF = 6, WN = 4, BN = 16 * NF * WN, BK = 32, WAVES = 8, MT = 8, NS = 4;
+    static constexpr int X_BYTES = BM * 64, STAGE = X_BYTES + BN * 64;
+    static constexpr int PER = STAGE / 1024 / WAVES, X_PER = X_BYTES / 1024 / WAVES, W_PER = PER - X_PER;
+    static_assert(NS * STAGE <= 160 * 1024 && PER * 1024 * WAVES == STAGE && PER < MT, "the ring");
+};
+constexpr int64_t kBigMaxStride = 1 << 22;  // a tile's rows within 32-bit byte offsets
+
+// Chunk c of 64-byte row r lies at c ^ quarter(r): no bank conflicts counted (with (r >> 2) & 3 for quarter(r)
+// half of the reads of x conflicted).
+__device__ __forceinline__ int quarter(int row) { return (0x78 >> (((row >> 2) & 3) * 2)) & 3; }
+
+__global__ __launch_bounds__(Big::WAVES * 64) void router_big_kernel(RouterArgs a) {
+    using C = Big;
+    __shared__ __align__(1024) uint8_t ring[C::NS * C::STAGE];
+    const int lane = threadIdx.x & 63, r16 = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    const int steps = a.H / C::BK, m0 = blockIdx.x * C::BM;
+
+    uint32_t x_off[C::X_PER];  // transfers of 16 rows
+#pragma unroll
+    for (int i = 0; i < C::X_PER; ++i) {
+        const int row = (wave + i * C::WAVES) * 16 + (lane >> 2);
+        const int c = (lane & 3) ^ quarter(row);
+        x_off[i] = (uint32_t)((min(m0 + row, a.T - 1) - m0) * (int)a.x_stride + c * 8) * 2u;
+    }
+    const uint8_t* x0 = reinterpret_cast<const uint8_t*>(a.x + (int64_t)m0 * a.x_stride);
+    const uint8_t* w0[C::W_PER];  // blocks past the last read the last, and are not stored
+#pragma unroll
+    for (int i = 0; i < C::W_PER; ++i)
+        w0[i] = a.w + (int64_t)min(wave + i * C::WAVES, (a.E + 15) / 16 - 1) * steps * 1024;
+    const uint32_t lane16 = lane * 16;
+    const uint32_t ring0 = lds_addr(ring);
+    auto issue = [&](int i, int step, int stage) {
+        const uint32_t to = ring0 + stage * C::STAGE + (wave + i * C::WAVES) * 1024;
+        if (i < C::X_PER) dma16_at(x_off[i], x0 + (int64_t)step * 64, to);
+        else dma16_at(lane16, w0[i < C::X_PER ? 0 : i - C::X_PER] + (int64_t)step * 1024, to);
+    };
+    const uint32_t x_at = (wm * 128 + r16) * 64 + (q ^ quarter(r16)) * 16;
+    auto read_x = [&](int stage, int m) {
+        return *reinterpret_cast<const bf16x8*>(ring + stage * C::STAGE + x_at + m * 1024);
+    };
+    auto read_w = [&](int stage, int n) {
+        return *reinterpret_cast<const bf16x8*>(ring + stage * C::STAGE + C::X_BYTES + (wn * C::NF + n) * 1024 + lane16);
+    };
+    Sums<1, C::NF, C::MT> acc;
+    acc.clear();
+#pragma unroll
+    for (int s = 0; s < C::NS - 1; ++s)
+        if (s < steps) {
+#pragma unroll
+            for (int i = 0; i < C::PER; ++i) issue(i, s, s);
+        }
+    if (steps >= C::NS - 1) wait_and_barrier<(C::NS - 2) * C::PER>();
+    else wait_and_barrier<0>();
+    bf16x8 w[C::NF], x[3];
+#pragma unroll
+    for (int n = 0; n < C::NF; ++n) w[n] = read_w(0, n);
+    x[0] = read_x(0, 0);
+    x[1] = read_x(0, 1);
+    int stage = 0, freed = C::NS - 1;
+    // more: a stage is left to be transferred; last: none to be read
+    auto step = [&](int s, auto more, auto last) {
+        constexpr bool MORE = decltype(more)::value, LAST = decltype(last)::value;
+        const int next = stage == C::NS - 1 ? 0 : stage + 1;
+#pragma unroll
+        for (int m = 0; m < C::MT; ++m) {
+            if (m + 2 < C::MT) x[(m + 2) % 3] = read_x(stage, m + 2);
+            if constexpr (MORE)
+                if (m < C::PER) issue(m, s + C::NS - 1, freed);
+            __builtin_amdgcn_sched_barrier(0);
+            if (m < C::MT - 1 || LAST) {
+#pragma unroll
+                for (int n = 0; n < C::NF; ++n) acc.add(0, n, m, w[n], x[m % 3]);
+            } else {
+                if constexpr (MORE) wait_and_barrier<(C::NS - 2) * C::PER>();
+                else wait_and_barrier<0>();
+                static_assert((C::MT - 1) % 3 == 1, "x[0] and x[2] are free here");
+                x[0] = read_x(next, 0);
+#pragma unroll
+                for (int n = 0; n < C::NF; ++n) {
+                    acc.add(0, n, m, w[n], x[m % 3]);
+                    w[n] = read_w(next, n);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                x[1] = read_x(next, 1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        stage = next;
+        freed = freed == C::NS - 1 ? 0 : freed + 1;
+    };
+    int s = 0;
+    for (; s + C::NS - 1 < steps; ++s) step(s, std::true_type{}, std::false_type{});
+    for (; s < steps - 1; ++s) step(s, std::false_type{}, std::false_type{});
+    step(s, std::false_type{}, std::true_type{});
+#pragma unroll
+    for (int m = 0; m < C::MT; ++m) {
+        const int t = m0 + wm * 128 + m * 16 + r16;
+        if (t >= a.T) continue;
+#pragma unroll
+        for (int n = 0; n < C::NF; ++n) store_logits(a.logits, a.E, t, (wn * C::NF + n) * 16 + q * 4, acc.total(n, m));
     }
 }
 
@@ -384,13 +514,13 @@ __global__ __launch_bounds__(kThreads) void router_reduce_kernel(const float* __
 //   T 256: 32 x 64 in 8 splits 7.6, 32 x 128 in 8 8.1; T 512: 10.5, 9.5.  E 64, H 4096: T 4096 32 x 64 in two
 //   splits 12.8, 64 x 64 in four 13.5.
 //   T 1024: 32 x 128 in 4 splits 13.9, 64 x 128 in 8 15.5; T 2048: 22.3, 20.9.
-//   T 8192: 64 x 128 45.2, 128 x 256 in 4 splits 43.5; T 16384: 89, 71.  192 experts wide where that covers E
+//   T 8192: 64 x 128 45.2, 128 x 256 in 4 splits 43.5; T 16384: 89, 70.  192 experts wide where that covers E
 //   with fewer columns (E 384, T 16384: 86, 105 at 256).
 // FP32 weights (three times the registers for weights, so 128 experts at most): T 128 32 x 64 in 14 splits 8.5,
-// 64 x 64 in 14 9.3; T 1024: 24.3, 18.5, 64 x 128 in 8 20.2; T 16384: 64 x 128 178, 128 x 128 140.
+// 64 x 64 in 14 9.3; T 1024: 24.3, 18.5, 64 x 128 in 8 20.2; T 16384: 64 x 128 178, 128 x 128 134.
 constexpr int kCus = 256;
 
-enum Kernel { kSmall, kTile32x64, kTile32x128, kTile64x64, kTile64x128, kTile128x128, kTile128x192, kTile128x256 };
+enum Kernel { kSmall, kTile32x64, kTile32x128, kTile64x64, kTile64x128, kTile128x128, kTile128x192, kTile128x256, kBig };
 struct Choice {
     Kernel kernel;
     int splits;
@@ -416,6 +546,9 @@ Choice choose(int T, int H, int E, int parts) {
     if (E <= 64) return split(kTile64x64, 64, 64, 128);
     if (tiles(32, 128) <= kCus / 4) return split(kTile32x128, 32, 128, 128);
     if (E <= 128 || tiles(64, 128) <= kCus) return split(kTile64x128, 64, 128, 128);
+    // one 256 x 384 tile per CU and round: faster than the 128 x 192 tiles while over 0.84 of the CUs have one
+    const int64_t big = div_up(T, Big::BM);
+    if (E > 256 && E <= Big::BN && big * 100 > 84 * kCus * div_up(big, kCus)) return {kBig, 1};
     if (div_up(E, 192) * 192 < div_up(E, 256) * 256) return split(kTile128x192, 128, 192, 128);
     return split(kTile128x256, 128, 256, 128);
 }
@@ -477,6 +610,10 @@ hipError_t launch_router_logits(const RouterArgs& a, hipStream_t stream) {
                        : launch_tile<Tile<64, 2, 8, 128, 1>>(a, c.splits, stream);
         case kTile128x128: return launch_tile<Tile<128, 2, 8, 64, 3>>(a, c.splits, stream);
         case kTile128x192: return launch_tile<Tile<128, 3, 4, 128, 1>>(a, c.splits, stream);
+        case kBig:
+            if (a.x_stride >= kBigMaxStride) return launch_tile<Tile<128, 3, 4, 128, 1>>(a, 1, stream);
+            hipLaunchKernelGGL(router_big_kernel, dim3((unsigned)div_up(a.T, Big::BM)), dim3(Big::WAVES * 64), 0, stream, a);
+            return hipGetLastError();
         case kTile128x256: return launch_tile<Tile<128, 4, 4, 128, 1>>(a, c.splits, stream);
     }
     return hipErrorInvalidValue;

@@ -55,7 +55,7 @@ def test_router_exact(gpu, T, H, E, wt):
 # every tile shape, whole and with ragged tokens, experts and columns, in one piece and split
 TILES = [(257, 1056, 256), (600, 4128, 256), (1500, 2080, 100), (3000, 480, 60), (4200, 7168, 64), (8191, 288, 256),
          (8300, 96, 200), (8300, 160, 300), (9000, 1120, 257), (16400, 160, 128), (16385, 64, 385), (20000, 96, 512),
-         (70000, 32, 64)]
+         (70000, 32, 64), (60000, 96, 300), (65000, 32, 257), (65536, 160, 384)]
 
 
 @pytest.mark.parametrize("wt", [BF16, F32])
