@@ -405,7 +405,7 @@ enum moe_dtype {
  * 0x7F or 0xFF); an infinite element becomes NaN and the others of its row 0;
  * a row of zeros with eps = 0 is NaN.
  * Limits (else MOE_ERR_SHAPE, or MOE_ERR_ALIGN for the divisibility rules):
- *   num_tokens 0 .. 2^30 - 1; hidden 32 .. 2^20, a multiple of 32; eps finite,
+ *   num_tokens 0 .. 2^28 - 1; hidden 32 .. 2^20, a multiple of 32; eps finite,
  *   >= 0;
  *   strides >= hidden and multiples of 8 elements.
  * x, residual, residual_out, weight, y and x_q: 16-byte aligned. */
@@ -436,7 +436,7 @@ MOE_API int moe_norm_quant(const moe_norm_shape* shape, const void* x, const voi
 /* Router product: logits[t, e] = sum over k of x[t, k] * w[e, k], in FP32.
  * Products are exact in FP32 and sums are held in FP32, for FP32 weights too
  * (a weight is split into three BF16 parts, 8 bits each).
- * Limits: num_tokens 0 .. 2^30 - 1; hidden 32 .. 2^20, a multiple of 32;
+ * Limits: num_tokens 0 .. 2^28 - 1; hidden 32 .. 2^20, a multiple of 32;
  * num_experts 1 .. 1024 (all ranks' experts); x_stride >= hidden and a multiple of 8. */
 typedef struct moe_router_shape {
     int64_t x_stride;
@@ -489,7 +489,7 @@ MOE_API int moe_router_logits(const moe_router_shape* shape, const uint16_t* x, 
  * moe_plan drops (a padding row is a row of -infinities).  NaN ranks above
  * every number, and its weight is NaN; a softmax row with a NaN or +infinity
  * has NaN weights throughout.
- * Limits: num_tokens >= 0, T * topk < 2^30; num_experts 1 .. 1024; topk 1 ..
+ * Limits: num_tokens 0 .. 2^28 - 1, T * topk < 2^30; num_experts 1 .. 1024; topk 1 ..
  * min(64, num_experts / num_groups * topk_groups); num_groups a divisor of
  * num_experts, at most 64; topk_groups 1 .. num_groups; scale finite;
  * logits_stride >= num_experts. */

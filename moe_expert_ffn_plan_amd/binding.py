@@ -446,7 +446,9 @@ def _here(t, name):
 
 def _bf16(t, name, device, numel):
     """Pointer of a contiguous BF16 tensor, given as bfloat16 or as its int16 bits."""
-    if t is not None and t.dtype == torch.bfloat16 and t.is_contiguous():
+    if isinstance(t, torch.Tensor) and t.dtype == torch.bfloat16:
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
         t = t.view(torch.int16)
     return _ptr(t, torch.int16, name, device, numel)
 

@@ -390,7 +390,7 @@ namespace {
 
 bool type_ok(int t) { return t == MOE_BF16 || t == MOE_F32; }
 bool flag_ok(int v) { return v == 0 || v == 1; }
-bool tokens_ok(int t) { return t >= 0 && t < (1 << 30); }  // kernels count padded tokens in 32 bits
+bool tokens_ok(int t) { return t >= 0 && t < kMaxTokens; }  // tiles times threads fit a launch's 32 bits
 
 // A stride as given (0 = contiguous) against the row length; vectors of 8 elements start every row.
 int check_stride(int64_t stride, int64_t row) {
@@ -426,7 +426,7 @@ int check_router(const moe_router_shape* s) {
 
 int check_gate(const moe_gate_shape* s) {
     if (!s) return MOE_ERR_NULL;
-    if (s->num_tokens < 0 || s->num_experts < 1 || s->num_experts > kMaxGateExperts) return MOE_ERR_SHAPE;
+    if (!tokens_ok(s->num_tokens) || s->num_experts < 1 || s->num_experts > kMaxGateExperts) return MOE_ERR_SHAPE;
     if (s->num_groups < 1 || s->num_groups > kMaxGateGroups || s->num_experts % s->num_groups != 0)
         return MOE_ERR_SHAPE;
     if (s->topk_groups < 1 || s->topk_groups > s->num_groups) return MOE_ERR_SHAPE;

@@ -6,10 +6,11 @@
 //
 // gate_kernel finds the same answer in 32 bits and proves it, row by row.  It takes the k + 2 best by 32-bit
 // keys that hold a shortened order value and the expert's index, ranks those among each other on the values
-// themselves (FP64), and checks that no other candidate reaches the k-th.  Without a bias the values are the
-// logits and the check is exact; with one it allows for the error of the FP32 scores.  A row that fails (more
-// than two further candidates within that error, marks of groups within theirs, a NaN, a spread that the
-// keys cannot hold) is done again by exact_row; random rows fail about once in 20,000.
+// themselves (FP64), and checks that the next key is too small to belong among the first k, its shortening
+// and the error of FP32 scores allowed for.  A row that fails (three candidates within that error, marks of
+// groups within theirs, a NaN, a spread that the keys cannot hold) is done again by exact_row: about 3 of
+// 100,000 random rows of sigmoid scores with a bias, 100 of softmax scores with one, none of BF16 logits
+// without.
 //
 // Bound by instructions, not by memory: 16 lanes share a row (four rows a wave; 64 lanes for long rows), a
 // lane keeps its D largest keys sorted, and a round of the selection is four DPP maxima and D moves for all
@@ -301,7 +302,7 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
     __shared__ uint64_t keys[kWaves][EXPERTS];
     const GateArgs& a = f.a;
     const int lane = threadIdx.x & 63, sub = lane & (L - 1);
-    const int64_t t0 = ((int64_t)blockIdx.x * kWaves + threadIdx.x / 64) * ROWS;
+    const int64_t t0 = (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kWaves + threadIdx.x / 64) * ROWS;
     if (t0 >= a.T) return;
     const int64_t t = min(t0 + lane / L, (int64_t)a.T - 1);  // lanes past the last row repeat it, and store nothing
     const bool soft = a.score == MOE_SCORE_SOFTMAX, grouped = a.groups > 1, biased = a.bias != nullptr;
@@ -358,8 +359,8 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
     float top = -INFINITY;
     // Softmax in units of 2^-24: an argument is d = top - l, off by 1 unit times d (by 3 with exp32's product),
     // and the mean of d under the softmax's own weights is at most ln 1024 < 7.  A sum that divides the weights
-    // is off by 7 + 2 (expf) + 22 (additions) < 32, one that only orders by 21 + 1 + 22; a score then by at
-    // most 53 (d e^-d < 0.37).
+    // is off by 7 + 2 (expf) + 22 (additions) < 32, one that only orders by 21 + 1 + 22.  A score is e^-d <= 1
+    // times inv, the largest score: off by at most 53 (d e^-d < 0.37) times inv.
     float sum = 0.0f, inv = 0.0f;
     if (soft) {
 #pragma unroll
@@ -377,7 +378,7 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
         sum = real(across(bits(sum), L, AddF{}));
         inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     }
-    const float err = soft ? 0x1p-18f : 0x1p-22f;  // at least that of an FP32 score
+    const float err = soft ? 0x1p-18f * inv : 0x1p-22f;  // at least that of an FP32 score
     auto to_scores = [&](float(&v)[V]) {           // of -infinity: 0
         if (soft) {
 #pragma unroll
@@ -459,13 +460,15 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
     // Keys below `none` are no candidates.
     const uint32_t mask = (1u << f.index_bits) - 1;
     uint32_t best[V], none;
+    float scale = 0.0f, base = 0.0f;
     if (biased) {
         float hi = -INFINITY;
 #pragma unroll
         for (int i = 0; i < V; ++i) hi = fmaxf(hi, c[i]);
         hi = real(across(bits(hi), L, MaxF{}));
-        const float steps = (float)(1u << (32 - f.index_bits)), scale = steps / kKeyRange;
-        const float base = (steps - 8.0f) - hi * scale;  // hi goes to steps - 8, a few up or down by rounding
+        const float steps = (float)(1u << (32 - f.index_bits));
+        scale = steps / kKeyRange;
+        base = (steps - 8.0f) - hi * scale;  // hi goes to steps - 8, a few up or down by rounding
         none = 1u << f.index_bits;
 #pragma unroll
         for (int i = 0; i < V; ++i) {  // a NaN (no candidate at all) goes to either end
@@ -506,9 +509,13 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
         lead[D - 1] &= ~up;
         if (sub == j) mine = w;
     }
+    // what is left is at most the largest key left, unless a lane gave all that its list held
+    const uint32_t left = across(lead[0], L, MaxU{}) >> f.index_bits;
+    if (D < V) doubt |= lead[0] == 0;
 
     // The picks' scores in FP64 (one exponential per lane serves all of the wave's rows), their order values
-    // and ranks.  Softmax values under a bias share FP32's sum: they have to differ by more than its error.
+    // and ranks.  Softmax scores under a bias are divided by FP32's sum, which moves two of them apart or together
+    // by its error of their difference: they have to differ by more.
     const bool picked = (sub < picks) & (mine >= none);
     const int id = picked ? (int)(mask - (mine & mask)) : 1 << 30;
     const float l = picked ? load_logit(a, t * a.stride + id) : -INFINITY;
@@ -518,7 +525,7 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
     if (soft && !(a.renorm && !biased)) s = sum > 0.0f ? s / (double)sum : 0.0;
     const double value = !picked ? -INFINITY : biased ? s + (double)b : (double)l;
     const float gap = biased ? 2.0f * err + 0x1p-22f * fabsf((float)value) : 0.0f;
-    const double apart = (picked & soft & biased) ? (double)gap : 0.0;  // lanes without a pick are infinitely far
+    const double apart = (picked & soft & biased) ? (double)err : 0.0;  // lanes without a pick are infinitely far
     int rank = 0;
     {
         double o = value;
@@ -532,19 +539,23 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
     }
     const bool chosen = picked & (rank < a.k);
 
-    // No other candidate reaches the last choice: as many values as picks lie at or above it less the errors.
+    // No other candidate reaches the last choice.
     const uint64_t row_lanes = L == 64 ? ~0ull : ((1ull << (L & 63)) - 1) << (lane & ~(L - 1));
     const int n_chosen = __popcll(__ballot(chosen) & row_lanes);
-    const uint64_t last = __ballot(picked & (rank == a.k - 1)) & row_lanes;
-    const float border =  // with fewer choices than k: every candidate is one
-        n_chosen < a.k ? -FLT_MAX : __shfl((float)value - gap, __ffsll((unsigned long long)last) - 1);
-    int count = 0;
+    const bool last = picked & (rank == a.k - 1);
+    if (biased) {
+        // in steps of the keys: one that the key cuts off and one for the rounding of each side
+        doubt |= last & !((float)left + 3.0f < fmaf((float)value - gap, scale, base));
+        if (__any(n_chosen < a.k)) {  // every candidate has to be a choice, those below the keys' range too
+            int count = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) count += c[i] >= border;
-    count = (int)across((uint32_t)count, L, AddU{});
-    // its FP32 value is at least this
-    const float near = (float)value - (biased ? err + 0x1p-23f * fabsf((float)value) : 0.0f);
-    doubt |= count > __popcll(__ballot(picked & (near >= border)) & row_lanes);
+            for (int i = 0; i < V; ++i) count += c[i] > -INFINITY;
+            doubt |= (n_chosen < a.k) & ((int)across((uint32_t)count, L, AddU{}) != n_chosen);
+        }
+    } else {
+        // keys of BF16 logits hold them whole, and order equal ones by their index
+        doubt |= last & (a.logits_type == MOE_F32) & (left >= mine >> f.index_bits);
+    }
 
     s = chosen ? s : 0.0;
     if (a.renorm) {
@@ -574,21 +585,19 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
 // Rows of more than 16 choices.
 __global__ __launch_bounds__(64 * kWaves) void gate_exact_kernel(GateArgs a) {
     __shared__ uint64_t keys[kWaves][kMaxGateExperts];
-    const int64_t t = (int64_t)blockIdx.x * kWaves + threadIdx.x / 64;
+    const int64_t t = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kWaves + threadIdx.x / 64;
     if (t < a.T) exact_row(a, t, (lds_u64*)keys[threadIdx.x / 64]);
 }
 
 hipError_t launch_exact(const GateArgs& a, hipStream_t stream) {
-    hipLaunchKernelGGL(gate_exact_kernel, dim3((unsigned)(((int64_t)a.T + kWaves - 1) / kWaves)), dim3(64 * kWaves), 0,
-                       stream, a);
+    hipLaunchKernelGGL(gate_exact_kernel, wide_grid(((int64_t)a.T + kWaves - 1) / kWaves), dim3(64 * kWaves), 0, stream, a);
     return hipGetLastError();
 }
 
 template <int L, int V, int D>
 hipError_t launch(const GateFast& f, hipStream_t stream) {
     constexpr int ROWS = kWaves * (64 / L);
-    hipLaunchKernelGGL((gate_kernel<L, V, D>), dim3((unsigned)(((int64_t)f.a.T + ROWS - 1) / ROWS)), dim3(64 * kWaves), 0,
-                       stream, f);
+    hipLaunchKernelGGL((gate_kernel<L, V, D>), wide_grid(((int64_t)f.a.T + ROWS - 1) / ROWS), dim3(64 * kWaves), 0, stream, f);
     return hipGetLastError();
 }
 
@@ -609,7 +618,7 @@ hipError_t launch_gate(const GateArgs& a, hipStream_t stream) {
     int slots = 4;  // values per lane of the kernel below
     while (slots < hold) slots += slots == 16 && L == 16 && a.k <= 8 ? 8 : slots == 24 ? 8 : slots;
     if (L == 64 && slots < 16) slots = 16;
-    int index_bits = 1;
+    int index_bits = 8;  // at least: FP32 counts the keys' steps, 2^(32 - index_bits) of them, one by one to 2^24
     while ((1 << index_bits) < (padded - 1) * n + lpg * slots) ++index_bits;
     const GateFast f{a, n, __builtin_ctz(lpg), index_bits, vec};
     if (L == 16) {

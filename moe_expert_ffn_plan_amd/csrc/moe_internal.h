@@ -197,6 +197,14 @@ hipError_t launch_combine(const moe_shape& s, const uint16_t* yslot, const int32
 constexpr int kMaxGateExperts = 1024;
 constexpr int kMaxGateGroups = 64;
 constexpr int kMaxHidden = 1 << 20;
+constexpr int kMaxTokens = 1 << 28;
+
+// n workgroups as a grid whose x extent times any workgroup size fits 32 bits; the kernel takes
+// blockIdx.y * gridDim.x + blockIdx.x and leaves where that is n or more.
+inline dim3 wide_grid(int64_t n) {
+    const int64_t x = std::min<int64_t>(n, 1 << 20);
+    return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
+}
 
 // Strides in elements, 0 already replaced by the row length.
 struct NormArgs {

@@ -212,7 +212,8 @@ constexpr int kMaxThreads = 1024;
 template <int XT, int RT, int WT, int V>
 __global__ __launch_bounds__(kMaxThreads) void norm_row_kernel(NormArgs a) {
     __shared__ double part[kMaxThreads / 64];
-    const int64_t row = blockIdx.x;
+    const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (row >= a.T) return;
     const int step = blockDim.x * 8;
     Cell<XT, RT> cell[V];
 #pragma unroll
@@ -240,7 +241,8 @@ __global__ __launch_bounds__(kMaxThreads) void norm_row_kernel(NormArgs a) {
 template <int XT, int RT, int WT>
 __global__ __launch_bounds__(kMaxThreads) void norm_long_kernel(NormArgs a) {
     __shared__ double part[kMaxThreads / 64];
-    const int64_t row = blockIdx.x;
+    const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (row >= a.T) return;
     double sum = 0.0;
     for (int c = threadIdx.x * 8; c < a.H; c += kMaxThreads * 8) {
         Cell<XT, RT> cell;
@@ -265,7 +267,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_long_kernel(NormArgs a) {
 template <int XT, int RT, int WT, int V>
 hipError_t launch_row(const NormArgs& a, hipStream_t stream) {
     const int threads = (a.H / 8 + V * 64 - 1) / (V * 64) * 64;
-    hipLaunchKernelGGL((norm_row_kernel<XT, RT, WT, V>), dim3((unsigned)a.T), dim3((unsigned)threads), 0, stream, a);
+    hipLaunchKernelGGL((norm_row_kernel<XT, RT, WT, V>), wide_grid(a.T), dim3((unsigned)threads), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -278,7 +280,7 @@ hipError_t launch(const NormArgs& a, hipStream_t stream) {
     if (cells <= 256 || (a.T <= 256 && cells <= kMaxThreads)) return launch_row<XT, RT, WT, 1>(a, stream);
     if (cells <= 2 * kMaxThreads) return launch_row<XT, RT, WT, 2>(a, stream);
     if (cells <= 4 * kMaxThreads) return launch_row<XT, RT, WT, 4>(a, stream);
-    hipLaunchKernelGGL((norm_long_kernel<XT, RT, WT>), dim3((unsigned)a.T), dim3(kMaxThreads), 0, stream, a);
+    hipLaunchKernelGGL((norm_long_kernel<XT, RT, WT>), wide_grid(a.T), dim3(kMaxThreads), 0, stream, a);
     return hipGetLastError();
 }
 

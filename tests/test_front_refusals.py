@@ -18,7 +18,7 @@ NORM = dict(num_tokens=4, hidden=256)
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(num_tokens=-1), -2), (dict(num_tokens=1 << 30), -2), (dict(hidden=0), -2), (dict(hidden=-32), -2), (dict(hidden=(1 << 20) + 32), -2),
+    (dict(num_tokens=-1), -2), (dict(num_tokens=1 << 28), -2), (dict(hidden=0), -2), (dict(hidden=-32), -2), (dict(hidden=(1 << 20) + 32), -2),
     (dict(hidden=48), -3), (dict(hidden=33), -3), (dict(eps=-1e-6), -2), (dict(eps=float("nan")), -2),
     (dict(eps=float("inf")), -2), (dict(x_stride=255), -2), (dict(x_stride=-256), -2), (dict(x_stride=260), -3),
     (dict(residual_stride=128), -2), (dict(residual_stride=257), -3), (dict(residual_out_stride=250), -2),
@@ -54,7 +54,7 @@ ROUTER = dict(num_tokens=4, hidden=256, num_experts=8)
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(num_tokens=-1), -2), (dict(num_tokens=1 << 30), -2), (dict(hidden=0), -2), (dict(hidden=100), -3), (dict(hidden=(1 << 20) + 32), -2),
+    (dict(num_tokens=-1), -2), (dict(num_tokens=1 << 28), -2), (dict(hidden=0), -2), (dict(hidden=100), -3), (dict(hidden=(1 << 20) + 32), -2),
     (dict(num_experts=0), -2), (dict(num_experts=1025), -2), (dict(x_stride=200), -2), (dict(x_stride=257), -3)])
 def test_router_shapes(change, status):
     s = B.make_router(**{**ROUTER, **change})
@@ -111,10 +111,10 @@ GATE = dict(num_tokens=4, num_experts=32, topk=4)
 
 
 @pytest.mark.parametrize("change", [
-    dict(num_tokens=-1), dict(num_experts=0), dict(num_experts=1025), dict(topk=0), dict(topk=33),
+    dict(num_tokens=-1), dict(num_tokens=1 << 28, topk=1), dict(num_experts=0), dict(num_experts=1025), dict(topk=0), dict(topk=33),
     dict(num_experts=128, topk=65), dict(num_groups=0), dict(num_groups=5), dict(num_groups=128, num_experts=1024),
     dict(num_groups=4, topk_groups=0), dict(num_groups=4, topk_groups=5), dict(num_groups=16, topk_groups=1),
-    dict(num_tokens=1 << 28, topk=4), dict(scale=float("nan")), dict(scale=float("inf")), dict(logits_stride=31),
+    dict(num_tokens=(1 << 28) - 1, topk=5), dict(scale=float("nan")), dict(scale=float("inf")), dict(logits_stride=31),
     dict(logits_stride=-32)])
 def test_gate_shapes(change):
     assert gate(B.make_gate(**{**GATE, **change})) == -2

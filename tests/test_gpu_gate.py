@@ -191,3 +191,19 @@ def test_gate_binding_refusals(gpu):
                   ((l, ids, w), dict(bias=torch.zeros(16))), ((l, ids, w), dict(bias=torch.zeros(16, device=gpu).to(BF16)))):
         with pytest.raises((TypeError, ValueError)):
             B.gate(s, *a, **kw)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("E,k,score,biased", [(256, 8, "sigmoid", True), (256, 8, "softmax", True), (384, 6, "sigmoid", False),
+                                              (100, 14, "sigmoid", True), (24, 5, "softmax", True), (520, 9, "sigmoid", True)])
+def test_gate_many_rows(gpu, E, k, score, biased, dtype):
+    """Enough rows that near ties of every kind occur, against a stable sort in 64 bits."""
+    T = 60000
+    l = normal(T, E, 21, gpu, dtype)
+    b = balance(E, 22, gpu) if biased else None
+    ids, _ = run(l, k, b, score=score)
+    d = l.double()
+    s = torch.softmax(d, -1) if score == "softmax" else 1 / (1 + torch.exp(-d))
+    c = s + b.double() if biased else d
+    want = torch.sort(c, dim=-1, descending=True, stable=True).indices[:, :k].cpu().numpy()
+    assert np.array_equal(ids, want)
