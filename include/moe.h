@@ -452,7 +452,8 @@ typedef struct moe_router_shape {
  *   expert 16 * block + l % 16 (zeros past the last expert), columns
  *   32 * step + 8 * (l / 16) .. + 8; part p of an FP32 weight is BF16(w - the
  *   parts before it).  FP32 weights that are not finite give NaN logits, and
- *   those below 2^-110 in magnitude may lose low bits.
+ *   those below 2^-110 in magnitude may lose low bits; with FP32 weights an
+ *   infinite x may give NaN where the formula gives an infinity.
  * w [E, H] contiguous; w_tiled of moe_router_weight_bytes; both 16-byte
  * aligned, not overlapping. */
 MOE_API int moe_router_weight_bytes(const moe_router_shape* shape, size_t* bytes);
@@ -486,9 +487,9 @@ MOE_API int moe_router_logits(const moe_router_shape* shape, const uint16_t* x, 
  * comparisons hold in 64 bits wherever they decide an order.
  * An expert whose logit or c is -infinity is never chosen; a row with fewer
  * than topk candidates ends in entries of id -1 and weight 0, which
- * moe_plan drops (a padding row is a row of -infinities).  NaN ranks above
- * every number, and its weight is NaN; a softmax row with a NaN or +infinity
- * has NaN weights throughout.
+ * moe_plan drops (a padding row is a row of -infinities).  NaN (of a
+ * logit or of the bias) ranks above every number, and the weight of a NaN logit
+ * is NaN; a softmax row with a NaN or +infinity has NaN weights throughout.
  * Limits: num_tokens 0 .. 2^28 - 1, T * topk < 2^30; num_experts 1 .. 1024; topk 1 ..
  * min(64, num_experts / num_groups * topk_groups); num_groups a divisor of
  * num_experts, at most 64; topk_groups 1 .. num_groups; scale finite;

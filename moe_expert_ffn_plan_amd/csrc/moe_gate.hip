@@ -8,13 +8,16 @@
 // keys that hold a shortened order value and the expert's index, ranks those among each other on the values
 // themselves (FP64), and checks that the next key is too small to belong among the first k, its shortening
 // and the error of FP32 scores allowed for.  A row that fails (three candidates within that error, marks of
-// groups within theirs, a NaN, a spread that the keys cannot hold) is done again by exact_row: about 3 of
-// 100,000 random rows of sigmoid scores with a bias, 100 of softmax scores with one, none of BF16 logits
-// without.
+// groups within theirs, a NaN, a spread that the keys cannot hold) is done again by exact_row: of 100,000
+// random rows of 256 experts none without a bias and none of sigmoid scores with one, 4 with groups marked by
+// pairs, 180 of softmax scores with a bias.
 //
 // Bound by instructions, not by memory: 16 lanes share a row (four rows a wave; 64 lanes for long rows), a
 // lane keeps its D largest keys sorted, and a round of the selection is four DPP maxima and D moves for all
 // rows of the wave.  Packing the index into the key makes a comparison of two candidates one instruction.
+// 65536 x 384, top 6, no bias: 25 us FP32 (106 MB, 4.2 TB/s), 23 BF16 (56 MB); with a bias 32.  16384 x 256,
+// top 8: 7.4 without a bias, 9.3 with one, 12 with 8 groups marked by pairs; 128 such rows 5.4, where a kernel
+// that stores one word takes 3.7 of launch.
 #include "moe_internal.h"
 
 #include <cfloat>

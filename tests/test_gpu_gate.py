@@ -178,6 +178,35 @@ def test_gate_rows(gpu):
     check(l[:50], 6, scale=0.0)
 
 
+@pytest.mark.parametrize("groups,kept,group_score", [(1, 1, "max"), (8, 4, "max"), (8, 4, "top2")])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_bias_without_bounds(gpu, score, groups, kept, group_score):
+    """Biases that are not finite, or that leave no room between the scores."""
+    E, big = 64, torch.finfo(F32).max
+    l = normal(9, E, 60, gpu)
+    l[2, 5::7], l[3] = -INF, -INF
+    for values in ({3: NAN, 40: NAN}, {7: INF}, {7: INF, 8: INF, 50: -INF}, {e: -INF for e in range(E) if e % 9},
+                   {1: big, 2: -big}, {e: -big for e in range(E)}, {e: big for e in range(E)}, {5: NAN, 6: INF, 7: -INF}):
+        bias = balance(E, 61, gpu)
+        for e, v in values.items():
+            bias[e] = v
+        check(l, 6, bias=bias, score=score, num_groups=groups, topk_groups=kept, group_score=group_score)
+
+
+def test_gate_more_rows_than_a_grid_axis(gpu):
+    """Over 2^24 rows of two experts; the larger sigmoid, rounded twice at most (64 bits, then 32)."""
+    T = (1 << 24) + 9
+    g = torch.Generator(device=gpu).manual_seed(62)
+    l = torch.randn(T, 2, generator=g, device=gpu)
+    ids = torch.full((T, 1), 777, dtype=torch.int64, device=gpu)
+    w = torch.full((T, 1), NAN, device=gpu)
+    B.gate(B.make_gate(T, 2, 1, score="sigmoid", renormalize=False), l, ids, w)
+    torch.cuda.synchronize()
+    assert torch.equal(ids[:, 0], (l[:, 1] > l[:, 0]).long())
+    want = torch.sigmoid(l.max(dim=1).values.double())
+    assert ((w[:, 0].double() - want).abs() <= 2.0 ** -23 * want).all()
+
+
 def test_gate_no_tokens(gpu):
     e = torch.zeros(0, 8, device=gpu)
     B.gate(B.make_gate(0, 8, 2), e, torch.zeros(0, 2, dtype=torch.int64, device=gpu), torch.zeros(0, 2, device=gpu))

@@ -119,6 +119,24 @@ def test_norm_strides(gpu):
     assert (ro[:, H:] == 3.0).all() and (xs[:, H:] == 7.0).all()
 
 
+def test_norm_more_rows_than_a_grid_axis(gpu):
+    """Over 2^20 rows; rows do not depend on where they lie, so the ends are compared with calls of their own."""
+    T, H = (1 << 20) + 5, 32
+    g = torch.Generator(device=gpu).manual_seed(21)
+    x = torch.randn(T, H, generator=g, device=gpu).to(BF16)
+    r = torch.randn(T, H, generator=g, device=gpu).to(BF16)
+    w = (1 + 0.3 * torch.randn(H, generator=g, device=gpu)).to(BF16)
+    got = run(x, r, w)
+    h = x.float() + r.float()
+    v = h.double() / torch.sqrt(h.double().square().mean(1, keepdim=True) + 1e-6) * w.double()
+    assert ((got["y"].double() - v).abs() <= v.abs() * (2.0 ** -8 + 1.01 * V_REL) + 2.0 ** -133).all()
+    for rows in (slice(0, 40), slice((1 << 20) - 20, T)):
+        alone = run(x[rows], r[rows], w)
+        check(alone, x[rows], r[rows], w, 1e-6)
+        for k in alone:
+            assert torch.equal(alone[k], got[k][rows]), k
+
+
 def test_norm_rows_behind_the_last_stay(gpu):
     x, r, w = draw(8, 7168, BF16, BF16, BF16, 9, gpu)
     y = torch.full((8, 7168), 5.0, dtype=BF16, device=gpu)

@@ -125,6 +125,53 @@ def test_router_nan_rows_stay_apart(gpu):
     assert torch.equal(got[keep.to(gpu)], want[keep.to(gpu)])
 
 
+@pytest.mark.parametrize("T", [5, 40, 3000])
+def test_router_infinite_x_with_f32_weights(gpu, T):
+    """A row with an infinity has no finite logit where its weight is not 0; the other rows keep theirs."""
+    x, w = whole(T, 512, 20, F32, 11, gpu)
+    w[:, 500] = torch.where(w[:, 500] == 0, 1.0, w[:, 500])
+    want = run(x, w)
+    x[3, 500] = float("inf")
+    got = run(x, w)
+    assert not torch.isfinite(got[3]).any()
+    keep = torch.arange(T, device=gpu) != 3
+    assert torch.equal(got[keep], want[keep])
+
+
+def test_router_graphs_share_a_workspace(gpu):
+    """Two captured products over one workspace of partial sums, replayed in turn on one stream with eager
+    products of the same workspace between them."""
+    (T, E, H), n = (300, 256, 4096), 2
+    shapes = [B.make_router(T, H, E, weight_dtype=wt) for wt in (BF16, F32)]
+    sizes = [B.router_workspace_bytes(s) for s in shapes]
+    assert min(sizes) > 0
+    ws = torch.full((max(sizes),), 0x5A, dtype=torch.uint8, device=gpu)
+    ops = [whole(T, H, E, wt, 12 + i, gpu) for i, wt in enumerate((BF16, F32))]
+    tiled = [B.router_prepare(s, w) for s, (_, w) in zip(shapes, ops)]
+    out = [torch.empty(T, E, device=gpu) for _ in range(n)]
+    graphs = []
+    for s, (x, _), t, o in zip(shapes, ops, tiled, out):
+        B.router_logits(s, x, t, o, ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            B.router_logits(s, x, t, o, ws)
+        graphs.append(graph)
+    for seed in (20, 21, 22):
+        for i, wt in enumerate((BF16, F32)):
+            ops[i][0].copy_(whole(T, H, E, wt, seed + 10 * i, gpu)[0])
+        eager = torch.empty(T, E, device=gpu)
+        for o in out:
+            o.fill_(float("nan"))
+        graphs[0].replay()
+        graphs[1].replay()
+        B.router_logits(shapes[0], ops[0][0], tiled[0], eager, ws)
+        torch.cuda.synchronize()
+        for (x, w), o in zip(ops, out):
+            assert torch.equal(o.double(), x.double() @ w.double().T)
+        assert torch.equal(eager, out[0])
+
+
 def test_router_no_tokens(gpu):
     s = B.make_router(0, 64, 8)
     w = torch.ones(8, 64, dtype=BF16, device=gpu)
