@@ -475,8 +475,8 @@ int moe_router_workspace_bytes(const moe_router_shape* shape, size_t* bytes) {
     if (!bytes) return MOE_ERR_NULL;
     const int st = check_router(shape);
     if (st != MOE_OK) return st;
-    *bytes = router_workspace_bytes(shape->num_tokens, shape->hidden, shape->num_experts,
-                                    router_parts(shape->weight_type));
+    *bytes = choose_router(shape->num_tokens, shape->hidden, shape->num_experts, router_parts(shape->weight_type))
+                 .workspace_bytes(shape->num_tokens, shape->num_experts);
     return MOE_OK;
 }
 
@@ -498,14 +498,15 @@ int moe_router_logits(const moe_router_shape* shape, const uint16_t* x, const ui
     if (shape->num_tokens == 0) return MOE_OK;
     const int T = shape->num_tokens, H = shape->hidden, E = shape->num_experts;
     const int parts = router_parts(shape->weight_type);
-    const size_t need = router_workspace_bytes(T, H, E, parts);
+    const RouterChoice choice = choose_router(T, H, E, parts);
+    const size_t need = choice.workspace_bytes(T, E);
     if (!x || !w_tiled || !logits || (need > 0 && !ws)) return MOE_ERR_NULL;
     if (!aligned(x, 16) || !aligned(w_tiled, 16) || !aligned(logits, 16) || (need > 0 && !aligned(ws, kAlign)))
         return MOE_ERR_ALIGN;
     if (ws_bytes < need) return MOE_ERR_WORKSPACE;
     if ((st = check_arch_current()) != MOE_OK) return st;
     const RouterArgs a{x, w_tiled, logits, static_cast<float*>(ws), stride_or(shape->x_stride, H), T, H, E, parts};
-    return launch_router_logits(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    return launch_router_logits(a, choice, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 int moe_gate(const moe_gate_shape* shape, const void* logits, const float* bias, int64_t* topk_idx, float* topk_w,

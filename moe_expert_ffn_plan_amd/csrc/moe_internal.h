@@ -231,9 +231,13 @@ struct RouterArgs {
     int T, H, E, parts;
 };
 inline int router_parts(int weight_type) { return weight_type == MOE_F32 ? 3 : 1; }
-size_t router_workspace_bytes(int T, int H, int E, int parts);
+struct RouterChoice {
+    int kernel, splits;  // kernel: moe_router.hip's own numbers
+    size_t workspace_bytes(int T, int E) const { return splits > 1 ? (size_t)splits * T * E * sizeof(float) : 0; }
+};
+RouterChoice choose_router(int T, int H, int E, int parts);
 hipError_t launch_router_prepare(int H, int E, int weight_type, const void* w, uint8_t* w_tiled, hipStream_t stream);
-hipError_t launch_router_logits(const RouterArgs& a, hipStream_t stream);
+hipError_t launch_router_logits(const RouterArgs& a, RouterChoice c, hipStream_t stream);
 
 struct GateArgs {
     const void* logits;

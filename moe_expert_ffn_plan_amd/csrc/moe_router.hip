@@ -73,11 +73,17 @@ __device__ __forceinline__ void store_logits(float* logits, int E, int64_t t, in
 
 // ---- LDS DMA and waits (the compiler does not count what inline assembly issues; each kernel waits itself)
 
-// Lane l reads 16 bytes at its own address and writes them at LDS address lds + 16 l.  x is streamed about
-// once: the non-temporal hint keeps the weights in the L2 (16384 x 7168 x 256: 82 -> 78 us, and a pass that
-// only streams x 49 -> 41 us).
+// Lane l reads 16 bytes at its own address and writes them at LDS address lds + 16 l.  With the non-temporal hint,
+// which keeps the weights in the L2, for an x that the memory-side cache (256 MB, which the hint passes by) does
+// not hold next to the rest of a layer: 8192 x 7168 x 256 44.2 us, 47.1 without; 16384: 71.5, 76.3.
+constexpr int64_t kStreamBytes = 1 << 26;
 __device__ __forceinline__ void dma16_stream(uint64_t addr, uint32_t lds) {
     asm volatile("global_load_lds_dwordx4 %0, off nt" ::"v"(addr), "{m0}"(lds) : "memory");
+}
+// Without it for a smaller x, that the norm wrote just before: 4096 x 7168 x 256 23.9 us, 30.6 with it; 2048 16.4,
+// 20.9; the small kernel at 16 tokens 5.5, 11.0.
+__device__ __forceinline__ void dma16(uint64_t addr, uint32_t lds) {
+    asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(addr), "{m0}"(lds) : "memory");
 }
 // The same at a wave-uniform base and a 32-bit offset per lane, kept in the L2.
 __device__ __forceinline__ void dma16_at(uint32_t off, const void* base, uint32_t lds) {
@@ -128,11 +134,11 @@ struct Sums {
     }
 };
 
-// ---- up to 16 tokens: one workgroup per 16 experts, in one launch
+// ---- few tokens or columns: one workgroup per 16 tokens and 16 experts, in one launch
 //
-// Latency-bound (1 x 7168 x 256: 4.6 us on the GPU): the 16 waves split the columns, wave w taking every 16th
-// run of 64, each with its loads of kRuns runs in flight at once (x through its own piece of LDS, the weights
-// straight into registers, 1 KiB a load), and add up through LDS in the order of the waves.
+// Latency-bound: the 16 waves split the columns, wave w taking every 16th run of 64, with kRuns runs in flight
+// (x through its own piece of LDS, the weights straight into registers, 1 KiB a load), and add up through LDS
+// in the order of the waves.
 constexpr int kSmallTokens = 16, kSmallWaves = 16, kRuns = 4;
 
 template <int P>
@@ -142,14 +148,14 @@ __global__ __launch_bounds__(kSmallWaves * 64) void router_small_kernel(RouterAr
     static_assert(kRuns * RUN >= 1024, "holds the waves' sums");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int KT = a.H / 32, runs = (KT + 1) / 2;
-    const int r16 = lane & 15, q = lane >> 4;
+    const int r16 = lane & 15, q = lane >> 4, m0 = blockIdx.y * kSmallTokens;
     uint64_t xp[2];                          // transfer i: rows 8 i .. 8 i + 8 of the run
     int xc[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int row = i * 8 + (lane >> 3);
         xc[i] = swizzle<8>(row, lane & 7);
-        xp[i] = reinterpret_cast<uint64_t>(a.x + (int64_t)min(row, a.T - 1) * a.x_stride + xc[i] * 8);
+        xp[i] = reinterpret_cast<uint64_t>(a.x + (int64_t)min(m0 + row, a.T - 1) * a.x_stride + xc[i] * 8);
     }
     const uint8_t* wp = a.w + (int64_t)blockIdx.x * KT * P * 1024;
     Sums<P, 1, 1> acc;
@@ -166,7 +172,7 @@ __global__ __launch_bounds__(kSmallWaves * 64) void router_small_kernel(RouterAr
             const bool half = 2 * r + 1 >= KT;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                dma16_stream(xp[i] + (int64_t)r * 128 - (half && xc[i] >= 4 ? xc[i] * 16 : 0),
+                dma16(xp[i] + (int64_t)r * 128 - (half && xc[i] >= 4 ? xc[i] * 16 : 0),
                              mine + u * RUN + i * 1024);
         }
 #pragma unroll
@@ -203,7 +209,7 @@ __global__ __launch_bounds__(kSmallWaves * 64) void router_small_kernel(RouterAr
         v4f sum = part[0][lane];
 #pragma unroll
         for (int w = 1; w < kSmallWaves; ++w) sum += part[w][lane];
-        if (r16 < a.T) store_logits(a.logits, a.E, r16, blockIdx.x * 16 + q * 4, sum);
+        if (m0 + r16 < a.T) store_logits(a.logits, a.E, m0 + r16, blockIdx.x * 16 + q * 4, sum);
     }
 }
 
@@ -237,6 +243,7 @@ struct Tile {
 struct TileArgs {
     RouterArgs r;
     int m_tiles, n_tiles, splits, steps;  // K-steps in all
+    bool stream_x;
 };
 
 template <class C>
@@ -271,9 +278,12 @@ __global__ __launch_bounds__(C::THREADS) void router_tile_kernel(TileArgs a) {
             // a last step of fewer columns: the missing chunks read the step's first, and are not multiplied
             const int valid = (KT - step * C::KS) * 4;
 #pragma unroll
-            for (int i = 0; i < C::PER; ++i)
-                dma16_stream(src[i] + (int64_t)step * (C::BK * 2) - (chunk[i] >= valid ? chunk[i] * 16 : 0),
-                             ring0 + stage * C::STAGE + (pw + i * C::PW) * 1024);
+            for (int i = 0; i < C::PER; ++i) {
+                const uint64_t from = src[i] + (int64_t)step * (C::BK * 2) - (chunk[i] >= valid ? chunk[i] * 16 : 0);
+                const uint32_t to = ring0 + stage * C::STAGE + (pw + i * C::PW) * 1024;
+                if (a.stream_x) dma16_stream(from, to);
+                else dma16(from, to);
+            }
         };
 #pragma unroll
         for (int s = 0; s < C::NS - 1; ++s)
@@ -507,61 +517,50 @@ __global__ __launch_bounds__(kThreads) void router_reduce_kernel(const float* __
 
 // ---- which kernel
 //
-// The tile is the smallest that fills the CUs, split over K into what they hold: small tiles split less, and
-// each split adds a partial sum to write and read; large tiles read their operands less often.  Both sides of
-// each border (us, whole call, operands not in the L2; H 7168, E 256 unless named):
-//   T 16: small kernel 5.5, 32 x 64 split 14 ways 6.5; T 32: 11.4, 7.0 (the small kernel has 16 workgroups).
-//   T 256: 32 x 64 in 8 splits 7.6, 32 x 128 in 8 8.1; T 512: 10.5, 9.5.  E 64, H 4096: T 4096 32 x 64 in two
-//   splits 12.8, 64 x 64 in four 13.5.
-//   T 1024: 32 x 128 in 4 splits 13.9, 64 x 128 in 8 15.5; T 2048: 22.3, 20.9.
-//   T 8192: 64 x 128 45.2, 128 x 256 in 4 splits 43.5; T 16384: 89, 70.  192 experts wide where that covers E
-//   with fewer columns (E 384, T 16384: 86, 105 at 256).
-// FP32 weights (three times the registers for weights, so 128 experts at most): T 128 32 x 64 in 14 splits 8.5,
-// 64 x 64 in 14 9.3; T 1024: 24.3, 18.5, 64 x 128 in 8 20.2; T 16384: 64 x 128 178, 128 x 128 134.
+// The one with the least estimated time (microseconds of the whole call), out of all tiles and of 1, 2, 4, 8 and
+// as many splits as fill the CUs:
+//   2.4 + rounds (0.84 + (H / 32 / splits) cost (1 + 0.44 share of the CUs in use))
+//       + (2.2 + 0.46 per MB of partial sums where there are splits), at least 4.1, or 6.6 with the second launch.
+// cost is a tile's time per 32 columns on an idle chip.  The constants are a fit to 3800 timings (T 8 .. 40000,
+// H 1024 .. 7168, E 32 .. 1024, every tile and several splits; operands that do not lie in the L2); over their 473
+// shapes its choice takes 1.3% more than the fastest on average, where borders on the number of tiles alone took
+// 15% more.  Both sides of some borders:
+//   128 x 2048 x 512: one launch of 16 x 16 tiles 4.1, 32 x 64 in 4 splits 6.9; 64 x 7168 x 256: 6.5, 7.0; 256 x 7168
+//   x 256: 8.6, 7.9.  2048 x 1024 x 256: 32 x 64 whole 5.3, 64 x 128 in two splits 10.2.
+//   512 x 7168 x 256: 32 x 64 in 4 splits 10.2, 32 x 128 in 8 9.7; 2048: 64 x 64 in two 18.2, 64 x 128 in four 16.3;
+//   8192: 64 x 128 46, 128 x 256 in four 44; 16384: 91, 71 in two.
+//   40000 x 7168 x 384: 128 x 192 249, 256 x 384 218; 8192: 49, 64.
+//   FP32 weights, H 7168, E 256: T 512 32 x 64 in 4 splits 12.8, 64 x 64 in 8 14.1; T 1024: 21.1 in 2, 16.4 in 4;
+//   T 16384: 64 x 128 178, 128 x 128 134.
 constexpr int kCus = 256;
+constexpr int kSmallMost = 1024;  // tokens, as measured; a grid axis holds 16 times 65535
 
 enum Kernel { kSmall, kTile32x64, kTile32x128, kTile64x64, kTile64x128, kTile128x128, kTile128x192, kTile128x256, kBig };
-struct Choice {
+struct Tiling {
     Kernel kernel;
-    int splits;
+    int bm, bn, bk;
+    double cost;  // us
 };
+constexpr Tiling kBf16[] = {
+    {kSmall, 16, 16, 64, 0.014},       {kTile32x64, 32, 64, 128, 0.052},    {kTile64x64, 64, 64, 128, 0.095},
+    {kTile32x128, 32, 128, 128, 0.075}, {kTile64x128, 64, 128, 128, 0.120},  {kTile128x192, 128, 192, 128, 0.250},
+    {kTile128x256, 128, 256, 128, 0.300}, {kBig, Big::BM, Big::BN, Big::BK, 0.865}};
+constexpr Tiling kF32[] = {
+    {kSmall, 16, 16, 64, 0.028}, {kTile32x64, 32, 64, 128, 0.095}, {kTile64x64, 64, 64, 128, 0.140},
+    {kTile64x128, 64, 128, 64, 0.235}, {kTile128x128, 128, 128, 64, 0.385}};
 
 int div_up(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-Choice choose(int T, int H, int E, int parts) {
-    if (T <= kSmallTokens) return {kSmall, 1};
-    auto tiles = [&](int bm, int bn) { return (int64_t)div_up(T, bm) * div_up(E, bn); };
-    auto split = [&](Kernel k, int bm, int bn, int bk) {
-        // at least four K-steps each
-        const int64_t s = std::min<int64_t>(kCus / tiles(bm, bn), div_up(H, bk) / 4);
-        return Choice{k, (int)std::max<int64_t>(s, 1)};
-    };
-    if (parts == 3) {
-        if (tiles(32, 64) <= kCus / 4) return split(kTile32x64, 32, 64, 128);
-        if (E <= 64 || tiles(64, 64) <= kCus) return split(kTile64x64, 64, 64, 128);
-        if (tiles(64, 128) <= kCus) return split(kTile64x128, 64, 128, 64);
-        return split(kTile128x128, 128, 128, 64);
-    }
-    if (tiles(32, 64) <= (E <= 64 ? kCus / 2 : kCus / 8)) return split(kTile32x64, 32, 64, 128);
-    if (E <= 64) return split(kTile64x64, 64, 64, 128);
-    if (tiles(32, 128) <= kCus / 4) return split(kTile32x128, 32, 128, 128);
-    if (E <= 128 || tiles(64, 128) <= kCus) return split(kTile64x128, 64, 128, 128);
-    // one 256 x 384 tile per CU and round: faster than the 128 x 192 tiles while over 0.84 of the CUs have one
-    const int64_t big = div_up(T, Big::BM);
-    if (E > 256 && E <= Big::BN && big * 100 > 84 * kCus * div_up(big, kCus)) return {kBig, 1};
-    if (div_up(E, 192) * 192 < div_up(E, 256) * 256) return split(kTile128x192, 128, 192, 128);
-    return split(kTile128x256, 128, 256, 128);
-}
-
 template <int P>
 hipError_t launch_small(const RouterArgs& a, hipStream_t stream) {
-    hipLaunchKernelGGL(router_small_kernel<P>, dim3((unsigned)div_up(a.E, 16)), dim3(kSmallWaves * 64), 0, stream, a);
+    hipLaunchKernelGGL(router_small_kernel<P>, dim3((unsigned)div_up(a.E, 16), (unsigned)div_up(a.T, kSmallTokens)), dim3(kSmallWaves * 64), 0, stream, a);
     return hipGetLastError();
 }
 
 template <class C>
 hipError_t launch_tile(const RouterArgs& r, int splits, hipStream_t stream) {
-    const TileArgs a{r, div_up(r.T, C::BM), div_up(r.E, C::BN), splits, div_up(r.H, C::BK)};
+    const TileArgs a{r, div_up(r.T, C::BM), div_up(r.E, C::BN), splits, div_up(r.H, C::BK),
+                     (int64_t)r.T * r.H * 2 > kStreamBytes};
     const int64_t total = (int64_t)a.m_tiles * a.n_tiles * splits;
     hipLaunchKernelGGL(router_tile_kernel<C>, dim3((unsigned)div_up(total, 8) * 8), dim3(C::THREADS), 0, stream, a);
     if (splits > 1) {
@@ -578,9 +577,34 @@ hipError_t launch_tile(const RouterArgs& r, int splits, hipStream_t stream) {
 
 }  // namespace
 
-size_t router_workspace_bytes(int T, int H, int E, int parts) {
-    const Choice c = choose(T, H, E, parts);
-    return c.splits > 1 ? (size_t)c.splits * T * E * sizeof(float) : 0;
+RouterChoice choose_router(int T, int H, int E, int parts) {
+    RouterChoice best{kSmall, 1};
+    if (T == 0) return best;
+    double least = INFINITY;
+    auto consider = [&](const Tiling& c) {
+        if (c.kernel == kSmall && T > kSmallMost) return;
+        if (c.kernel == kBig && (E <= 256 || E > Big::BN)) return;
+        if (c.bn > 64 && c.bn >= 2 * E) return;  // not measured
+        const int64_t tiles = (int64_t)div_up(T, c.bm) * div_up(E, c.bn);
+        if (tiles > 1 << 22) return;  // times 512 threads: what a launch takes
+        const int steps = div_up(H, c.bk);
+        const bool whole = c.kernel == kSmall || c.kernel == kBig;
+        const int fill = tiles < kCus ? std::min(kCus / (int)tiles, steps / 4) : 1;  // four K-steps at least
+        for (const int s : {1, 2, 4, 8, fill}) {
+            // splits: two K-steps at least, two workgroups a CU and 256 MB of partial sums at most
+            if (s < 1 || (s > 1 && (whole || 2 * s > steps || s * tiles > 2 * kCus || (int64_t)s * T * E > 1 << 26))) continue;
+            const int groups = (int)tiles * s;
+            double us = 2.4 + div_up(groups, kCus) * (0.84 + H / 32 * c.cost / s * (1.0 + 0.44 * std::min(groups, kCus) / kCus));
+            if (s > 1) us += 2.2 + 0.46e-6 * sizeof(float) * s * T * E;
+            us = std::max(us, s > 1 ? 6.6 : 4.1);
+            if (us < least) least = us, best = RouterChoice{c.kernel, s};
+        }
+    };
+    if (parts == 3)
+        for (const Tiling& c : kF32) consider(c);
+    else
+        for (const Tiling& c : kBf16) consider(c);
+    return best;
 }
 
 hipError_t launch_router_prepare(int H, int E, int weight_type, const void* w, uint8_t* w_tiled, hipStream_t stream) {
@@ -593,10 +617,9 @@ hipError_t launch_router_prepare(int H, int E, int weight_type, const void* w, u
     return hipGetLastError();
 }
 
-hipError_t launch_router_logits(const RouterArgs& a, hipStream_t stream) {
-    const Choice c = choose(a.T, a.H, a.E, a.parts);
+hipError_t launch_router_logits(const RouterArgs& a, RouterChoice c, hipStream_t stream) {
     const bool f32 = a.parts == 3;
-    switch (c.kernel) {
+    switch ((Kernel)c.kernel) {
         case kSmall: return f32 ? launch_small<3>(a, stream) : launch_small<1>(a, stream);
         case kTile32x64:
             return f32 ? launch_tile<Tile<32, 1, 8, 128, 3>>(a, c.splits, stream)

@@ -68,6 +68,21 @@ def test_router_exact_tiles(gpu, T, H, E, wt):
     assert torch.equal(got.double(), want)
 
 
+# the tiles of the larger shapes again with a split and without, ragged in every direction; many rows of 16-token tiles
+PIECES = [(40, 20000, 860), (130, 1056, 100), (1024, 1056, 40), (1100, 4128, 200), (1300, 7136, 257), (1030, 2080, 520),
+          (2100, 7136, 300), (4100, 4064, 500), (3100, 7136, 380), (17000, 2080, 250), (3000, 4128, 120)]
+
+
+@pytest.mark.parametrize("wt", [BF16, F32])
+@pytest.mark.parametrize("T,H,E", PIECES)
+def test_router_exact_pieces(gpu, T, H, E, wt):
+    print(f"router T={T} H={H} E={E} {wt}", flush=True)
+    x, w = whole(T, H, E, wt, T + E, gpu)
+    got = run(x, w)
+    want = x.double() @ w.double().t().contiguous()
+    assert torch.equal(got.double(), want)
+
+
 @pytest.mark.parametrize("wt", [BF16, F32])
 @pytest.mark.parametrize("T,H,E", [(1, 7168, 256), (130, 7168, 256), (700, 4096, 64), (5000, 1024, 384)])
 def test_router_random(gpu, T, H, E, wt):
