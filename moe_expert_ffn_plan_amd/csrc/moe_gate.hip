@@ -10,7 +10,7 @@
 // and the error of FP32 scores allowed for.  A row that fails (three candidates within that error, marks of
 // groups within theirs, a NaN, a spread that the keys cannot hold) is done again by exact_row: of 100,000
 // random rows of 256 experts none without a bias and none of sigmoid scores with one, 4 with groups marked by
-// pairs, 180 of softmax scores with a bias.
+// pairs, 3 of softmax scores with a bias.  A row done again adds 4 us to a call of 128.
 //
 // Bound by instructions, not by memory: 16 lanes share a row (four rows a wave; 64 lanes for long rows), a
 // lane keeps its D largest keys sorted, and a round of the selection is four DPP maxima and D moves for all
@@ -122,13 +122,6 @@ __device__ __forceinline__ float load_logit(const GateArgs& a, int64_t i) {
     if (a.logits_type == MOE_F32) return static_cast<const float*>(a.logits)[i];
     return __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.logits)[i] << 16);
 }
-// The largest key of the wave and the lowest index that has it.
-__device__ __forceinline__ void wave_best(uint64_t& key, int& idx) {
-    const uint64_t best = across64(key, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
-    idx = (int)across((uint32_t)(key == best ? idx : 1 << 30), 64, MinU{});
-    key = best;
-}
-
 // The number that order_key maps to key (its NaN for ~0).
 __device__ __forceinline__ double order_value(uint64_t key) {
     return __longlong_as_double((long long)(key >> 63 ? key & ~(1ull << 63) : ~key));
@@ -214,21 +207,41 @@ __device__ __forceinline__ void exact_row(const GateArgs& a, int64_t t, lds_u64*
         __builtin_amdgcn_wave_barrier();
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
-    // lane j keeps the j-th choice
-    int mine = -1;
-    for (int j = 0; j < a.k; ++j) {
+    // Lane j keeps the j-th choice.  A lane knows its own largest key, and looks for the next when that is taken; the
+    // high halves of the lanes' keys decide unless two are equal (0.31 us a choice; 0.37 with the whole keys and
+    // all lanes' indices compared).
+    uint32_t hi, lo;
+    int at;
+    auto own_best = [&] {
         uint64_t k = 0;
-        int at = 1 << 30;
+        at = 0;
 #pragma unroll 4
         for (int e = lane; e < a.E; e += 64) {
             const uint64_t o = keys[e];
             at = o > k ? e : at;
             k = max(k, o);
         }
-        wave_best(k, at);
-        if (k == 0) break;
-        if ((at & 63) == lane) keys[at] = 0;
-        if (lane == j) mine = at;
+        hi = (uint32_t)(k >> 32);
+        lo = (uint32_t)k;
+    };
+    own_best();
+    int mine = -1;
+    for (int j = 0; j < a.k; ++j) {
+        const uint32_t top_hi = across(hi, 64, MaxU{});
+        if (top_hi == 0) break;  // no candidate's
+        uint64_t who = __ballot(hi == top_hi);
+        if (who & (who - 1)) {
+            const uint32_t top_lo = across(hi == top_hi ? lo : 0, 64, MaxU{});
+            const bool same = (hi == top_hi) & (lo == top_lo);
+            const uint32_t first = across(same ? (uint32_t)at : ~0u, 64, MinU{});
+            who = __ballot(same & ((uint32_t)at == first));
+        }
+        const int winner = __ffsll((long long)who) - 1, taken = __builtin_amdgcn_readlane(at, winner);
+        if (lane == j) mine = taken;
+        if (lane == winner) {
+            keys[at] = 0;
+            own_best();
+        }
     }
     double w = mine >= 0 ? score(logit(mine)) : 0.0;
     if (a.renorm) {
@@ -287,6 +300,14 @@ __device__ __forceinline__ float sigmoid32(float l) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l * -1.44269504088896341f));
 }
 __device__ __forceinline__ float exp32(float d) { return __builtin_amdgcn_exp2f(d * 1.44269504088896341f); }
+// e^d for d <= 0 within 3 * 2^-24 of it: 2^(the product as rounded) by the hardware (2), times 1 + ln 2 times what
+// that rounding and the constant's left out (1).
+__device__ __forceinline__ float exp_whole(float d) {
+    const float t = d * 1.44269504088896341f;
+    const float rest = fmaf(d, 1.44269504088896341f, -t) + d * 1.92596299e-8f;
+    const float e = __builtin_amdgcn_exp2f(t);
+    return t < -200.0f ? 0.0f : fmaf(e, rest * 0.693147182f, e);
+}
 
 constexpr int kKeyRange = 4;  // order values from a row's largest down to this far below it have keys of their own
 
@@ -361,24 +382,34 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
     bool doubt = false;  // of this lane's row
     float top = -INFINITY;
     // Softmax in units of 2^-24: an argument is d = top - l, off by 1 unit times d (by 3 with exp32's product),
-    // and the mean of d under the softmax's own weights is at most ln 1024 < 7.  A sum that divides the weights
-    // is off by 7 + 2 (expf) + 22 (additions) < 32, one that only orders by 21 + 1 + 22.  A score is e^-d <= 1
-    // times inv, the largest score: off by at most 53 (d e^-d < 0.37) times inv.
+    // and the mean of d under the softmax's own weights is at most ln 1024 < 7.  A sum that divides scores is off
+    // by 7 + 3 (exp_whole) and added in FP64, one that only marks groups by 21 + 1 + 22 (additions).  An FP32 score
+    // is e^-d <= 1 times inv, the largest score: off by at most 53 (d e^-d < 0.37) times inv.
     float sum = 0.0f, inv = 0.0f;
+    double sum64 = 0.0;
     if (soft) {
 #pragma unroll
         for (int i = 0; i < V; ++i) top = fmaxf(top, c[i]);
         top = real(across(bits(top), L, MaxF{}));
         doubt |= top == INFINITY;
         top = top == -INFINITY ? 0.0f : top;
-        if (!a.renorm) {
+        if (biased || !a.renorm) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum += expf(c[i] - top);
-        } else if (biased || pair) {
+            for (int i = 0; i < V; ++i) sum64 += (double)exp_whole(c[i] - top);
+            if constexpr (L == 64) {
+                sum64 = wave_sum(sum64);
+            } else {
+                sum64 += dpp_f64<kXor1>(sum64);
+                sum64 += dpp_f64<kXor2>(sum64);
+                sum64 += dpp_f64<kXor7>(sum64);
+                sum64 += dpp_f64<kXor15>(sum64);
+            }
+            sum = (float)sum64;
+        } else if (pair) {
 #pragma unroll
             for (int i = 0; i < V; ++i) sum += exp32(c[i] - top);
+            sum = real(across(bits(sum), L, AddF{}));
         }
-        sum = real(across(bits(sum), L, AddF{}));
         inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     }
     const float err = soft ? 0x1p-18f * inv : 0x1p-22f;  // at least that of an FP32 score
@@ -517,18 +548,18 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
     if (D < V) doubt |= lead[0] == 0;
 
     // The picks' scores in FP64 (one exponential per lane serves all of the wave's rows), their order values
-    // and ranks.  Softmax scores under a bias are divided by FP32's sum, which moves two of them apart or together
-    // by its error of their difference: they have to differ by more.
+    // and ranks.  The error of a softmax's sum (10 units) moves two scores apart or together by that part of
+    // their difference: their order values under a bias have to differ by more, the 64-bit roundings of both
+    // allowed for, or score and bias be the same.
     const bool picked = (sub < picks) & (mine >= none);
     const int id = picked ? (int)(mask - (mine & mask)) : 1 << 30;
     const float l = picked ? load_logit(a, t * a.stride + id) : -INFINITY;
     const float b = (picked & biased) ? a.bias[id] : 0.0f;
     const double e = exp(soft ? (double)l - (double)top : -(double)l);
     double s = soft ? e : 1.0 / (1.0 + e);
-    if (soft && !(a.renorm && !biased)) s = sum > 0.0f ? s / (double)sum : 0.0;
+    if (soft && (biased || !a.renorm)) s = sum64 > 0.0 ? s / sum64 : 0.0;
     const double value = !picked ? -INFINITY : biased ? s + (double)b : (double)l;
     const float gap = biased ? 2.0f * err + 0x1p-22f * fabsf((float)value) : 0.0f;
-    const double apart = (picked & soft & biased) ? (double)err : 0.0;  // lanes without a pick are infinitely far
     int rank = 0;
     {
         double o = value;
@@ -537,7 +568,17 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
             o = dpp_f64<kRor1>(o);
             oid = dpp<kRor1>(oid);
             rank += (o > value) | ((o == value) & ((int)oid < id));
-            doubt |= fabs(o - value) < apart;
+        }
+    }
+    if (soft & biased) {
+        double o = value, os = s;
+        uint32_t ob = bits(b);
+        for (int r = 1; r < 16; ++r) {  // lanes without a pick are infinitely far
+            o = dpp_f64<kRor1>(o);
+            os = dpp_f64<kRor1>(os);
+            ob = dpp<kRor1>(ob);
+            doubt |= picked & ((os != s) | (real(ob) != b)) &
+                     (fabs(o - value) <= fabs(os - s) * 0x1p-20 + fabs(value) * 0x1p-51);
         }
     }
     const bool chosen = picked & (rank < a.k);

@@ -178,6 +178,21 @@ def test_gate_rows(gpu):
     check(l[:50], 6, scale=0.0)
 
 
+@pytest.mark.parametrize("part", [1.0, 0.5, 0.999])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gate_bias_cancels_scores(gpu, score, part):
+    """A bias that takes back the scores of the first row: order values that differ by the bias's rounding only,
+    where scores differ by all of their own."""
+    E = 128
+    l = normal(40, E, 63, gpu)
+    l[1:20] = l[0]
+    l[5, :64] += 2.0 ** -20
+    d = l[0].double()
+    s = torch.softmax(d, 0) if score == "softmax" else torch.sigmoid(d)
+    check(l, 8, bias=(-s * part).float(), score=score)
+    check(l, 8, bias=(s.mean() - s * part).float(), score=score, num_groups=4, topk_groups=2, group_score="top2")
+
+
 @pytest.mark.parametrize("groups,kept,group_score", [(1, 1, "max"), (8, 4, "max"), (8, 4, "top2")])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_gate_bias_without_bounds(gpu, score, groups, kept, group_score):
