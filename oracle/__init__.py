@@ -14,6 +14,8 @@ the pages' description step by step:
   a vectorised stable-argsort twin.
 * ``forward``  -- grouped Linear1, SwiGLU x top-k weight, FP8 requant,
   grouped Linear2, FP32 top-k combine written as BF16.
+* ``front``    -- what a layer computes before it: residual RMS norm with its
+  8-bit output, the router's product, the gate.
 
 Parity pins: every function is pinned by tests under ``tests/`` marked
 ``not gpu`` (exhaustive codec tables, library casts, brute force, exact
@@ -23,4 +25,4 @@ from library routines (torch's float8/bfloat16 casts and
 ``torch.nn.functional.silu`` in float64), which the whole forward matches bit
 for bit.  No function is left unpinned.
 """
-from . import formats, routing, forward  # noqa: F401
+from . import formats, routing, forward, front  # noqa: F401
