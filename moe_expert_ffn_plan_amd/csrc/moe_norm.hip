@@ -168,14 +168,16 @@ __device__ __forceinline__ double add_dpp(double v) {
     const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, true);
     return v + __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
 }
-// Sum over the wave, in all lanes: inside rows of 16 lanes by DPP, across rows and halves by swaps.
-__device__ __forceinline__ double wave_sum(double v) {
+// Sum over each L = 8, 16, 32 or 64 neighbouring lanes, in all of them: inside rows of 16 lanes by DPP, across
+// rows and halves by swaps.
+template <int L>
+__device__ __forceinline__ double lanes_sum(double v) {
     v = add_dpp<0xB1>(v);   // lane ^ 1
     v = add_dpp<0x4E>(v);   // lane ^ 2
     v = add_dpp<0x141>(v);  // lane ^ 7
-    v = add_dpp<0x140>(v);  // lane ^ 15
+    if constexpr (L > 8) v = add_dpp<0x140>(v);  // lane ^ 15
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int half = 0; half < (L == 64 ? 2 : L == 32 ? 1 : 0); ++half) {
         const uint64_t b = (uint64_t)__double_as_longlong(v);
         const uint32_t lo = (uint32_t)b, hi = (uint32_t)(b >> 32);
         const auto l = half ? __builtin_amdgcn_permlane32_swap(lo, lo, false, false)
@@ -189,7 +191,7 @@ __device__ __forceinline__ double wave_sum(double v) {
 }
 // Sum over the workgroup, in all threads; part: one double per wave.
 __device__ __forceinline__ double group_sum(double v, double* part) {
-    v = wave_sum(v);
+    v = lanes_sum<64>(v);
     const int waves = blockDim.x / 64;
     if (waves == 1) return v;
     if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = v;
@@ -203,6 +205,24 @@ __device__ __forceinline__ double square_sum(const float (&h)[8], double sum) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum = fma((double)h[j], (double)h[j], sum);
     return sum;
+}
+
+// Rows of up to 8 L columns, 64 / L of them in a wave.
+constexpr int kShortThreads = 256;
+template <int XT, int RT, int WT, int L>
+__global__ __launch_bounds__(kShortThreads) void norm_short_kernel(NormArgs a) {
+    const int64_t t = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (kShortThreads / L) + threadIdx.x / L;
+    const int64_t row = min(t, (int64_t)a.T - 1);  // lanes past the last row repeat it, and store nothing
+    const int c = (threadIdx.x & (L - 1)) * 8, at = min(c, a.H - 8);
+    Cell<XT, RT> cell;
+    Raw<WT> w;
+    cell.load(a, row, at);
+    w.load(a.weight, at);
+    float h[8];
+    cell.sum(a, h);
+    const double sum = lanes_sum<L>(c < a.H ? square_sum(h, 0.0) : 0.0);
+    const double rstd = 1.0 / sqrt(sum / a.H + (double)a.eps);
+    if (t < a.T && c < a.H) finish8<XT, RT, WT>(a, row, c, h, w, (float)rstd, rstd);
 }
 
 constexpr int kMaxThreads = 1024;
@@ -271,8 +291,21 @@ hipError_t launch_row(const NormArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <int XT, int RT, int WT, int L>
+hipError_t launch_short(const NormArgs& a, hipStream_t stream) {
+    constexpr int ROWS = kShortThreads / L;
+    hipLaunchKernelGGL((norm_short_kernel<XT, RT, WT, L>), wide_grid(((int64_t)a.T + ROWS - 1) / ROWS), dim3(kShortThreads), 0,
+                       stream, a);
+    return hipGetLastError();
+}
+
 template <int XT, int RT, int WT>
 hipError_t launch(const NormArgs& a, hipStream_t stream) {
+    // Rows that leave half of a wave without work share it (65536 x 64: 7.2 us, 22.7 with a workgroup each; 65536 x
+    // 256: 27.4, 29.6).
+    if (a.H <= 64) return launch_short<XT, RT, WT, 8>(a, stream);
+    if (a.H <= 128) return launch_short<XT, RT, WT, 16>(a, stream);
+    if (a.H <= 256) return launch_short<XT, RT, WT, 32>(a, stream);
     // One cell per thread where rows are few (128 x 7168: 3.9 us against 4.1 with two and 4.7 with four) or
     // short (16384 x 1024: 28.8, 30.2, 29.5), else two: more loads in flight per thread, and at four too few
     // threads (16384 x 7168: 191, 180, 186).

@@ -104,6 +104,26 @@ def test_norm_in_place(gpu, H):
             assert torch.equal(got[k].view(torch.uint8), want[k].view(torch.uint8)), (alias, k)
 
 
+@pytest.mark.parametrize("T,H", [(7, 32), (31, 64), (33, 96), (17, 128), (1000, 160), (9, 192), (63, 224), (4099, 256)])
+def test_norm_short_rows(gpu, T, H):
+    """Rows that share a wave: ragged counts, strides, in place, nothing behind the last row."""
+    x, r, w = draw(T, H, F32, BF16, F32, 22, gpu)
+    want = run(x, r, w)
+    check(want, x, r, w, 1e-6)
+    rs = torch.full((T + 40, H + 8), 9.0, dtype=BF16, device=gpu)
+    rs[:T, :H] = r
+    y = torch.full((T + 40, H), 5.0, dtype=BF16, device=gpu)
+    q = torch.full((T + 40, H), 0x11, dtype=torch.uint8, device=gpu)
+    sf = torch.full((T + 40, H // 32), 0x22, dtype=torch.uint8, device=gpu)
+    s = B.make_norm(T, H, 1e-6, F32, BF16, F32, residual_stride=H + 8, residual_out_stride=H + 8)
+    B.norm_quant(s, x, w, q[:T], sf[:T], y=y[:T], residual=rs[:T, :H], residual_out=rs[:T, :H])
+    torch.cuda.synchronize()
+    for got, k in ((y[:T], "y"), (q[:T], "x_q"), (sf[:T], "x_sf"), (rs[:T, :H], "residual_out")):
+        assert torch.equal(got, want[k]), k
+    assert (y[T:] == 5.0).all() and (q[T:] == 0x11).all() and (sf[T:] == 0x22).all()
+    assert (rs[T:] == 9.0).all() and (rs[:, H:] == 9.0).all()
+
+
 def test_norm_strides(gpu):
     """Rows of wider buffers; what lies between them stays as it is."""
     T, H = 11, 608
