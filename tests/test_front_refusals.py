@@ -82,6 +82,16 @@ def test_router_pointers():
     assert router(B.make_router(0, 256, 8), x=None, w=None, logits=None, ws=None, ws_bytes=0) == 0
 
 
+@pytest.mark.parametrize("weight", [torch.bfloat16, torch.float32])
+def test_router_workspace_sizes(weight):
+    """Whole copies of the logits, 256 MB of them at most, over all of the allowed sizes."""
+    for T in (0, 1, 16, 17, 129, 1024, 1025, 40000, 1 << 20, (1 << 28) - 1):
+        for hidden in (32, 96, 2048, 7168, 1 << 20):
+            for E in (1, 63, 64, 65, 257, 384, 385, 1024):
+                need = B.router_workspace_bytes(B.make_router(T, hidden, E, weight_dtype=weight))
+                assert need <= 1 << 28 and need % max(1, 4 * T * E) == 0 and need != 4 * T * E or need == 0
+
+
 def test_router_workspace():
     """Every shape that needs a workspace refuses one that is missing, misaligned or a byte short."""
     seen = 0
