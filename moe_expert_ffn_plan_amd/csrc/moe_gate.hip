@@ -560,25 +560,26 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
     if (soft && (biased || !a.renorm)) s = sum64 > 0.0 ? s / sum64 : 0.0;
     const double value = !picked ? -INFINITY : biased ? s + (double)b : (double)l;
     const float gap = biased ? 2.0f * err + 0x1p-22f * fabsf((float)value) : 0.0f;
-    int rank = 0;
-    {
-        double o = value;
-        uint32_t oid = (uint32_t)id;
+    // The picks come in the order of their keys, which is nearly always that of their values: one comparison with
+    // the pick before then says that of all.  Under a softmax and a bias neighbours that are apart by the error of
+    // the largest score's part say it of all pairs.
+    int rank = sub;
+    double o = dpp_f64<kRor1>(value);  // of the lane before
+    uint32_t oid = dpp<kRor1>((uint32_t)id);
+    const bool sorted = soft & biased ? o - value > (double)inv * 0x1.1p-20 + (fabs(o) + fabs(value)) * 0x1p-51
+                                      : (o > value) | ((o == value) & ((int)oid < id));
+    if (__any(picked & (sub > 0) & !sorted)) {
+        double os = dpp_f64<kRor1>(s);
+        uint32_t ob = dpp<kRor1>(bits(b));
+        rank = 0;
         for (int r = 1; r < 16; ++r) {  // all pairs of the row of 16 lanes that holds the picks
+            rank += (o > value) | ((o == value) & ((int)oid < id));
+            doubt |= soft & biased & picked & ((os != s) | (real(ob) != b)) &  // lanes without a pick are infinitely far
+                     (fabs(o - value) <= fabs(os - s) * 0x1p-20 + fabs(value) * 0x1p-51);
             o = dpp_f64<kRor1>(o);
             oid = dpp<kRor1>(oid);
-            rank += (o > value) | ((o == value) & ((int)oid < id));
-        }
-    }
-    if (soft & biased) {
-        double o = value, os = s;
-        uint32_t ob = bits(b);
-        for (int r = 1; r < 16; ++r) {  // lanes without a pick are infinitely far
-            o = dpp_f64<kRor1>(o);
             os = dpp_f64<kRor1>(os);
             ob = dpp<kRor1>(ob);
-            doubt |= picked & ((os != s) | (real(ob) != b)) &
-                     (fabs(o - value) <= fabs(os - s) * 0x1p-20 + fabs(value) * 0x1p-51);
         }
     }
     const bool chosen = picked & (rank < a.k);
