@@ -7,16 +7,16 @@
 // gate_kernel finds the same answer in 32 bits and proves it, row by row.  It takes the k + 2 best by 32-bit
 // keys that hold a shortened order value and the expert's index, ranks those among each other on the values
 // themselves (FP64), and checks that the next key is too small to belong among the first k, its shortening
-// and the error of FP32 scores allowed for.  A row that fails (three candidates within that error, marks of
-// groups within theirs, a NaN, a spread that the keys cannot hold) is done again by exact_row: of 100,000
-// random rows of 256 experts none without a bias and none of sigmoid scores with one, 4 with groups marked by
-// pairs, 3 of softmax scores with a bias.  A row done again adds 4 us to a call of 128.
+// and the error of FP32 scores allowed for.  Marks of groups too close for FP32 are formed again in FP64.  A row that
+// fails (three candidates within the error, marks of softmax scores within theirs, a NaN, a spread that the keys
+// cannot hold) is done again by exact_row: of 100,000 random rows of 256 experts none without a bias and none of
+// sigmoid scores, 3 to 4 of softmax scores with a bias.  A row done again adds 4 us to a call of 128.
 //
 // Bound by instructions, not by memory: 16 lanes share a row (four rows a wave; 64 lanes for long rows), a
 // lane keeps its D largest keys sorted, and a round of the selection is four DPP maxima and D moves for all
 // rows of the wave.  Packing the index into the key makes a comparison of two candidates one instruction.
-// 65536 x 384, top 6, no bias: 25 us FP32 (106 MB, 4.2 TB/s), 23 BF16 (56 MB); with a bias 32.  16384 x 256,
-// top 8: 7.4 without a bias, 9.3 with one, 12 with 8 groups marked by pairs; 128 such rows 5.4, where a kernel
+// 65536 x 384, top 6, no bias: 23.5 us FP32 (106 MB, 4.5 TB/s), 20.5 BF16 (56 MB); with a bias 29.  16384 x 256,
+// top 8: 7.4 without a bias, 8.8 with one, 11 with 8 groups marked by pairs; 128 such rows 5.0, where a kernel
 // that stores one word takes 3.7 of launch.
 #include "moe_internal.h"
 
@@ -462,6 +462,7 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
         if (lpg > 4) with(real(dpp<kXor7>(bits(m1))), real(dpp<kXor7>(bits(m2))));
         if (lpg > 8) with(real(dpp<kXor15>(bits(m1))), real(dpp<kXor15>(bits(m2))));
         if (lpg > 16) with(__shfl_xor(m1, 16), __shfl_xor(m2, 16));
+        const float least = pair ? m2 : m1;  // what counts for the mark is no lower
         if (pair && !biased) {  // scores rise with the logits
             m1 = m1 == -INFINITY ? m1 : soft ? exp32(m1 - top) * inv : sigmoid32(m1);
             m2 = m2 == -INFINITY ? m2 : soft ? exp32(m2 - top) * inv : sigmoid32(m2);
@@ -476,14 +477,48 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
                 rank += (g < a.groups) & ((o > mark) | ((o == mark) & (g < group)));
             }
         }
-        const bool kept = (rank < a.topk_groups) & (group < a.groups);
+        bool kept = (rank < a.topk_groups) & (group < a.groups);
         // logits compare exactly; sums of scores have to differ by more than the errors of both
         if (pair || biased) {
             const float low = real(across(bits((kept & (mark > -INFINITY)) ? mark : INFINITY), L, MinF{}));
             const float high = real(across(bits(kept ? -INFINITY : mark), L, MaxF{}));
             const float size = fmaxf(m1 > -INFINITY ? fabsf(m1) : 0.0f, m2 > -INFINITY ? fabsf(m2) : 0.0f);
             const float amp = real(across(bits(size), L, MaxF{}));  // four c and two sums, each rounded to 2^-24
-            doubt |= (high > -INFINITY) & !(low - high > 4.0f * err + 0x1p-21f * amp);
+            const float slack = 4.0f * err + 0x1p-21f * amp;
+            const bool close = (high > -INFINITY) & !(low - high > slack);
+            doubt |= close & (soft | !(amp < INFINITY));
+            if (!soft && __any(close)) {
+                // The marks again in FP64, as exact_row forms them, from the experts that may be the group's
+                // largest.  (4 of 100,000 random rows of 256 experts in 8 groups; 16384 such rows, of which some
+                // are among them, 11.0 us, 12.5 to 14 with the rows done again.)
+                const float from = biased ? least - slack : least;
+                uint32_t may = 0;
+#pragma unroll
+                for (int i = 0; i < V; ++i) may |= ((c[i] >= from) & (c[i] > -INFINITY)) ? 1u << i : 0;
+                double x1 = -INFINITY, x2 = -INFINITY;
+                auto add = [&](double o1, double o2) {
+                    x2 = fmax(fmin(x1, o1), fmax(x2, o2));
+                    x1 = fmax(x1, o1);
+                };
+                while (__any(may != 0)) {
+                    if (may) {
+                        const int e = expert(__ffs((int)may) - 1);
+                        double v = (double)load_logit(a, row + e);
+                        if (pair || biased) v = 1.0 / (1.0 + exp(-v));
+                        if (biased) v += (double)a.bias[e];
+                        add(v, -INFINITY);
+                    }
+                    may &= may - 1;
+                }
+                for (int r = 1; r < lpg; r *= 2) add(__shfl_xor(x1, r), __shfl_xor(x2, r));
+                const double exact = pair && x2 > -INFINITY ? x1 + x2 : x1;
+                rank = 0;
+                for (int g = 0; g < a.groups; ++g) {
+                    const double o = __shfl(exact, g << f.lpg_shift, L);
+                    rank += (o > exact) | ((o == exact) & (g < group));
+                }
+                kept = (rank < a.topk_groups) & (group < a.groups);
+            }
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) c[i] = kept ? c[i] : -INFINITY;

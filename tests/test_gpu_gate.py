@@ -178,6 +178,29 @@ def test_gate_rows(gpu):
     check(l[:50], 6, scale=0.0)
 
 
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,kept", [(64, 4, 2), (256, 8, 3), (64, 16, 5), (512, 8, 4), (320, 32, 7), (96, 3, 1)])
+def test_gate_groups_too_close_for_32_bits(gpu, E, groups, kept, score, biased):
+    """Pairs whose sums of scores differ by less than FP32 tells, another expert of each group just below them."""
+    g = torch.Generator().manual_seed(64)
+    T, n = 60, E // groups
+    l = torch.randn(T, groups, n, generator=g) * 0.3 - 3.0
+    a = torch.rand(T, groups, generator=g).double() + 0.5
+    if score == "sigmoid":      # s(a) + s(b) = 1.4
+        b = torch.logit(1.4 - torch.sigmoid(a))
+    else:                       # e^a + e^b = 6
+        b = torch.log(6.0 - torch.exp(a))
+    l[..., 0], l[..., n // 2], l[..., n - 1] = a.float(), b.float(), b.float() - 2.0 ** -21
+    l = l.reshape(T, E).to(gpu)
+    bias = torch.full((E,), 0.25, device=gpu) if biased else None
+    for group_score in ("top2", "max"):
+        check(l, min(4, n * kept), bias=bias, score=score, num_groups=groups, topk_groups=kept, group_score=group_score)
+    same = l[:1].repeat(T, 1).view(T, groups, n)    # all groups alike: the lowest are kept
+    same[1:] = same[1:, :1]
+    check(same.reshape(T, E), min(4, n * kept), bias=bias, score=score, num_groups=groups, topk_groups=kept, group_score="top2")
+
+
 @pytest.mark.parametrize("part", [1.0, 0.5, 0.999])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_gate_bias_cancels_scores(gpu, score, part):
