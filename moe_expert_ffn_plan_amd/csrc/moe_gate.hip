@@ -601,16 +601,17 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
     int rank = sub;
     double o = dpp_f64<kRor1>(value);  // of the lane before
     uint32_t oid = dpp<kRor1>((uint32_t)id);
-    const bool sorted = soft & biased ? o - value > (double)inv * 0x1.1p-20 + (fabs(o) + fabs(value)) * 0x1p-51
-                                      : (o > value) | ((o == value) & ((int)oid < id));
+    const bool weighed = soft && biased;  // order values that the sum's error moves
+    const bool sorted = weighed ? o - value > (double)inv * 0x1.1p-20 + (fabs(o) + fabs(value)) * 0x1p-51
+                                : (o > value) | ((o == value) & ((int)oid < id));
     if (__any(picked & (sub > 0) & !sorted)) {
         double os = dpp_f64<kRor1>(s);
         uint32_t ob = dpp<kRor1>(bits(b));
         rank = 0;
         for (int r = 1; r < 16; ++r) {  // all pairs of the row of 16 lanes that holds the picks
             rank += (o > value) | ((o == value) & ((int)oid < id));
-            doubt |= soft & biased & picked & ((os != s) | (real(ob) != b)) &  // lanes without a pick are infinitely far
-                     (fabs(o - value) <= fabs(os - s) * 0x1p-20 + fabs(value) * 0x1p-51);
+            const bool near = fabs(o - value) <= fabs(os - s) * 0x1p-20 + fabs(value) * 0x1p-51;
+            doubt |= weighed & picked & near & ((os != s) | (real(ob) != b));  // lanes without a pick: infinitely far
             o = dpp_f64<kRor1>(o);
             oid = dpp<kRor1>(oid);
             os = dpp_f64<kRor1>(os);
