@@ -294,8 +294,8 @@ hipError_t launch_row(const NormArgs& a, hipStream_t stream) {
 template <int XT, int RT, int WT, int L>
 hipError_t launch_short(const NormArgs& a, hipStream_t stream) {
     constexpr int ROWS = kShortThreads / L;
-    hipLaunchKernelGGL((norm_short_kernel<XT, RT, WT, L>), wide_grid(((int64_t)a.T + ROWS - 1) / ROWS), dim3(kShortThreads), 0,
-                       stream, a);
+    const dim3 grid = wide_grid(((int64_t)a.T + ROWS - 1) / ROWS);
+    hipLaunchKernelGGL((norm_short_kernel<XT, RT, WT, L>), grid, dim3(kShortThreads), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -556,7 +556,8 @@ int div_up(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 template <int P>
 hipError_t launch_small(const RouterArgs& a, hipStream_t stream) {
-    hipLaunchKernelGGL(router_small_kernel<P>, dim3((unsigned)div_up(a.E, 16), (unsigned)div_up(a.T, kSmallTokens)), dim3(kSmallWaves * 64), 0, stream, a);
+    const dim3 grid((unsigned)div_up(a.E, 16), (unsigned)div_up(a.T, kSmallTokens));
+    hipLaunchKernelGGL(router_small_kernel<P>, grid, dim3(kSmallWaves * 64), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -595,9 +596,11 @@ RouterChoice choose_router(int T, int H, int E, int parts) {
         const int fill = tiles < kCus ? std::min(kCus / (int)tiles, steps / 4) : 1;  // four K-steps at least
         for (const int s : {1, 2, 4, 8, fill}) {
             // splits: two K-steps at least, two workgroups a CU and 256 MB of partial sums at most
-            if (s < 1 || (s > 1 && (whole || 2 * s > steps || s * tiles > 2 * kCus || (int64_t)s * T * E > 1 << 26))) continue;
+            if (s < 1) continue;
+            if (s > 1 && (whole || 2 * s > steps || s * tiles > 2 * kCus || (int64_t)s * T * E > 1 << 26)) continue;
             const int groups = (int)tiles * s;
-            double us = 2.4 + div_up(groups, kCus) * (0.84 + H / 32 * c.cost / s * (1.0 + 0.44 * std::min(groups, kCus) / kCus));
+            const double used = (double)std::min(groups, kCus) / kCus;
+            double us = 2.4 + div_up(groups, kCus) * (0.84 + H / 32 * c.cost / s * (1.0 + 0.44 * used));
             if (s > 1) us += 2.2 + 0.46e-6 * sizeof(float) * s * T * E;
             us = std::max(us, s > 1 ? 6.6 : 4.1);
             if (us < least) least = us, best = RouterChoice{c.kernel, s};
