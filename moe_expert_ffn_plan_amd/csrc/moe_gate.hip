@@ -534,7 +534,9 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
         float hi = -INFINITY;
 #pragma unroll
         for (int i = 0; i < V; ++i) hi = fmaxf(hi, c[i]);
-        hi = real(across(bits(hi), L, MaxF{}));
+        // From -2^100 down the range stays where it is, so that base is finite: candidates below it get no keys, and the
+        // row is done again.  (With base = +infinity all keys were the range's upper end, in order of the index.)
+        hi = fmaxf(real(across(bits(hi), L, MaxF{})), -0x1p100f);
         const float steps = (float)(1u << (32 - f.index_bits));
         scale = steps / kKeyRange;
         base = (steps - 8.0f) - hi * scale;  // hi goes to steps - 8, a few up or down by rounding

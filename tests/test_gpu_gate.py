@@ -274,3 +274,19 @@ def test_gate_many_rows(gpu, E, k, score, biased, dtype):
     c = s + b.double() if biased else d
     want = torch.sort(c, dim=-1, descending=True, stable=True).indices[:, :k].cpu().numpy()
     assert np.array_equal(ids, want)
+
+
+@pytest.mark.parametrize("groups,kept,group_score", [(1, 1, "max"), (4, 2, "max"), (4, 2, "top2")])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [64, 100, 1024])
+def test_gate_biases_far_below_zero(gpu, E, score, groups, kept, group_score):
+    """Candidates whose biases are all far below zero, the best ones last: FP32 has no room for steps of 2^-22 there,
+    and sums of two of the lowest are beyond its range."""
+    print(f"gate E={E} {score} groups={groups} {group_score}", flush=True)
+    l = normal(5, E, 70, gpu)
+    l[2, 3::5], l[3] = -INF, -INF
+    rise = torch.arange(E, device=gpu, dtype=torch.float64) / E
+    for low, high in ((-1e9, -9e8), (-2e29, -1e29), (-2.0 ** 100, -2.0 ** 100 * (1 - 2.0 ** -13)), (-2e32, -1.4e32),
+                      (-3.4e38, -3.3e38), (-3.4e38, -1.0)):
+        check(l, 6, bias=(low + (high - low) * rise).float(), score=score, num_groups=groups, topk_groups=kept,
+              group_score=group_score)
