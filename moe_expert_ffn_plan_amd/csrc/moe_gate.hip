@@ -534,15 +534,17 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
         float hi = -INFINITY;
 #pragma unroll
         for (int i = 0; i < V; ++i) hi = fmaxf(hi, c[i]);
-        // From -2^100 down the range stays where it is, so that base is finite: candidates below it get no keys, and the
-        // row is done again.  (With base = +infinity all keys were the range's upper end, in order of the index.)
+        // From -2^100 down, and where there is no candidate, the range stays where it is, so that base is below infinity:
+        // candidates below the range get no keys, and the row is done again.  (With base = +infinity all keys were the
+        // range's upper end, in order of the index, and those of places past the row's end NaN.)  base is -infinity
+        // under a huge hi; then an infinite c makes a NaN, at either end: that is an expert, and the row in doubt.
         hi = fmaxf(real(across(bits(hi), L, MaxF{})), -0x1p100f);
         const float steps = (float)(1u << (32 - f.index_bits));
         scale = steps / kKeyRange;
         base = (steps - 8.0f) - hi * scale;  // hi goes to steps - 8, a few up or down by rounding
         none = 1u << f.index_bits;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {  // a NaN (no candidate at all) goes to either end
+        for (int i = 0; i < V; ++i) {  // base < infinity: what may not be chosen goes to 0, also where nothing may
             const float v = __builtin_amdgcn_fmed3f(fmaf(c[i], scale, base), 0.0f, steps - 1.0f);
             best[i] = ((uint32_t)v << f.index_bits) | (mask - expert(i));
         }

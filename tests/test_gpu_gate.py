@@ -290,3 +290,24 @@ def test_gate_biases_far_below_zero(gpu, E, score, groups, kept, group_score):
                       (-3.4e38, -3.3e38), (-3.4e38, -1.0)):
         check(l, 6, bias=(low + (high - low) * rise).float(), score=score, num_groups=groups, topk_groups=kept,
               group_score=group_score)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,kept", [(3, 1, 1), (33, 1, 1), (100, 1, 1), (257, 1, 1), (513, 1, 1), (60, 3, 2), (1008, 63, 7)])
+def test_gate_rows_without_candidates(gpu, E, groups, kept, score, dtype):
+    """Sizes at which lanes hold places past the row's end, in rows that leave no candidate, the last ones of their
+    memory: masked by the logits, by the bias, or by both; one candidate between them."""
+    print(f"gate E={E} groups={groups} {score} {dtype}", flush=True)
+    k = min(8, E // groups * kept)
+    l = normal(21, E, 71, gpu, dtype)
+    l[::2] = -INF
+    l[16, E - 1] = 0.5
+    half = balance(E, 72, gpu)
+    half[E // 2:] = -INF
+    l[19, :E // 2] = -INF
+    for bias in (torch.full((E,), -INF, device=gpu), half, balance(E, 73, gpu)):
+        for group_score in ("max", "top2"):
+            check(l, k, bias=bias, score=score, num_groups=groups, topk_groups=kept, group_score=group_score)
+    ids, w = run(l, k, half, score=score, num_groups=groups, topk_groups=kept)
+    assert (ids[[0, 19, 20]] == -1).all() and (w[[0, 19, 20]] == 0).all()
