@@ -9,10 +9,11 @@
 // its maximum two DPP steps; the row stays in registers between the sum and the outputs.  Loads with the
 // non-temporal hint lost (2048 x 4096: 11.9 -> 16.9 us, the inputs then miss the memory-side cache).
 //
-// Roundings: h is one FP32 addition; the squares are summed in FP64 (their sum decides the scale of every
-// element of the row, and |h| above 2^64 must not overflow); v is two FP32 products.  The scale compares
-// max|v| with 448 * 2^s: where the FP32 maximum lies within 4 units in the last place of that border, more
-// than v's three roundings can move it, the block's maximum is formed again in FP64.
+// Roundings: h is one FP32 addition for the outputs; the mean is that of the whole h, added and squared in FP64 (it
+// decides the scale of every element of the row, and |h| above 2^64 must not overflow); v is two FP32 products.  The
+// scale compares max|v| with 448 * 2^s: where the FP32 maximum lies within 4 units in the last place of that border,
+// more than v's four roundings can move it (h, 1 / rms, two products: 4 * 2^-24 of 1.75 are 3.5 units), the block's
+// maximum is formed again in FP64.
 #include "moe_internal.h"
 
 namespace moe {
@@ -88,6 +89,20 @@ struct Cell {
 #pragma unroll
             for (int j = 0; j < 8; ++j) h[j] = x.at(j);
         }
+    }
+    // sum + the squares of h, each h whole (the FP32 h is, where nothing was added)
+    __device__ __forceinline__ double squares(const NormArgs& a, const float (&h)[8], double sum) const {
+        if (a.residual) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const double d = (double)x.at(j) + (double)r.at(j);
+                sum = fma(d, d, sum);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum = fma((double)h[j], (double)h[j], sum);
+        }
+        return sum;
     }
 };
 
@@ -201,12 +216,6 @@ __device__ __forceinline__ double group_sum(double v, double* part) {
     return v;
 }
 
-__device__ __forceinline__ double square_sum(const float (&h)[8], double sum) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum = fma((double)h[j], (double)h[j], sum);
-    return sum;
-}
-
 // Rows of up to 8 L columns, 64 / L of them in a wave.
 constexpr int kShortThreads = 256;
 template <int XT, int RT, int WT, int L>
@@ -220,7 +229,7 @@ __global__ __launch_bounds__(kShortThreads) void norm_short_kernel(NormArgs a) {
     w.load(a.weight, at);
     float h[8];
     cell.sum(a, h);
-    const double sum = lanes_sum<L>(c < a.H ? square_sum(h, 0.0) : 0.0);
+    const double sum = lanes_sum<L>(c < a.H ? cell.squares(a, h, 0.0) : 0.0);
     const double rstd = 1.0 / sqrt(sum / a.H + (double)a.eps);
     if (t < a.T && c < a.H) finish8<XT, RT, WT>(a, row, c, h, w, (float)rstd, rstd);
 }
@@ -246,7 +255,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_row_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         cell[i].sum(a, h[i]);
-        if ((int)threadIdx.x * 8 + i * step < a.H) sum = square_sum(h[i], sum);
+        if ((int)threadIdx.x * 8 + i * step < a.H) sum = cell[i].squares(a, h[i], sum);
     }
     sum = group_sum(sum, part);
     const double rstd = 1.0 / sqrt(sum / a.H + (double)a.eps);
@@ -269,7 +278,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_long_kernel(NormArgs a) {
         float h[8];
         cell.load(a, row, c);
         cell.sum(a, h);
-        sum = square_sum(h, sum);
+        sum = cell.squares(a, h, sum);
     }
     sum = group_sum(sum, part);
     const double rstd = 1.0 / sqrt(sum / a.H + (double)a.eps);

@@ -243,3 +243,24 @@ def test_norm_binding_refusals(gpu):
         B.norm_quant(s, x, w)
     with pytest.raises(B.MoeError):
         B.norm_quant(B.make_norm(4, 48), x[:, :48].contiguous(), w[:48], y=y[:, :48].contiguous())
+
+
+@pytest.mark.parametrize("xt", [F32, BF16])
+def test_norm_scale_border_of_sums(gpu, xt):
+    """Rows whose FP32 sums x + residual are rounded, and whose largest v lies between what the rounded and the whole
+    sums give for 448 * 2^s: the scale is that of the whole sums."""
+    H, found = 32, 0
+    g = torch.Generator().manual_seed(77)
+    for _ in range(1500):
+        x, r = torch.randn(1, H, generator=g).to(xt), 4 * torch.randn(1, H, generator=g)
+        w = torch.full((H,), 0.25)
+        whole, rounded = x.double() + r.double(), (x.float() + r).double()
+        rstd = [1 / (h.square().mean() + 1e-6).sqrt() for h in (whole, rounded)]
+        w[31] = (3.5 / (whole[0, 31].abs() * (rstd[0] + rstd[1]) / 2)).float()
+        v = [(whole[0, 31].abs() * s * w[31].double()).item() / 3.5 - 1 for s in rstd]
+        if (v[0] > 0) == (v[1] > 0) or abs(v[0]) < 2.0 ** -40:   # 3.5 in both, or no clear side
+            continue
+        found += 1
+        x, r, w = x.to(gpu), r.to(gpu), w.to(gpu)
+        check(run(x, r, w), x, r, w, 1e-6)
+    assert found >= 20
