@@ -98,6 +98,10 @@ struct Cell {
                 const double d = (double)x.at(j) + (double)r.at(j);
                 sum = fma(d, d, sum);
             }
+            if (sum > 0x1p255) {  // an h that FP32 does not hold is infinite here too: 2^256 or more of the sum
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum = fabsf(h[j]) == INFINITY ? INFINITY : sum;
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum = fma((double)h[j], (double)h[j], sum);

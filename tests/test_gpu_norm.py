@@ -264,3 +264,20 @@ def test_norm_scale_border_of_sums(gpu, xt):
         x, r, w = x.to(gpu), r.to(gpu), w.to(gpu)
         check(run(x, r, w), x, r, w, 1e-6)
     assert found >= 20
+
+
+@pytest.mark.parametrize("H", [64, 2048, 40960])
+def test_norm_sums_beyond_fp32(gpu, H):
+    """x + residual over FP32's range is an infinity as any other: NaN at its place, 0 in the rest of its row."""
+    x, r, w = draw(5, H, F32, F32, F32, 16, gpu)
+    x[1, H - 2], r[1, H - 2] = 3e38, 3e38
+    x[2, 3], r[2, 3] = -3e38, -2e38
+    x[3, 5], r[3, 5] = 3e38, 3e37           # 3.3e38 is inside
+    x[4, 7], r[4, 7] = 3e38, -3e38
+    out = run(x, r, w)
+    y, q = out["y"].float().cpu(), values(out["x_q"])
+    for t, c in ((1, H - 2), (2, 3)):
+        assert torch.isinf(out["residual_out"][t, c]) and torch.isnan(y[t, c]) and np.isnan(q[t, c])
+        assert (np.delete(y[t].numpy(), c) == 0).all() and (np.delete(q[t], c) == 0).all()
+    keep = [0, 3, 4]
+    check({k: v[keep] for k, v in out.items()}, x[keep], r[keep], w, 1e-6)
