@@ -401,7 +401,8 @@ enum moe_dtype {
  * The norm and both outputs come from h before its rounding to
  * residual_type.  The mean is that of x + residual in 64 bits, v is computed
  * in 32, and the scale is the one of the formula in 64 bits also where an h or
- * max|v| rounds across 448 * 2^s in 32.  A NaN in a row makes the row's v NaN (E4M3 code
+ * max|v| rounds across 448 * 2^s in 32. (An h below 2^-126 of its row's
+ * rms may lose low bits, or all of them.)  A NaN in a row makes the row's v NaN (E4M3 code
  * 0x7F or 0xFF); an infinite element becomes NaN and the others of its row 0;
  * a row of zeros with eps = 0 is NaN.
  * Limits (else MOE_ERR_SHAPE, or MOE_ERR_ALIGN for the divisibility rules):

@@ -156,17 +156,27 @@ __device__ __forceinline__ int exact_code(const NormArgs& a, int64_t row, int c,
 // Outputs of 8 columns from their h.
 template <int XT, int RT, int WT>
 __device__ __forceinline__ void finish8(const NormArgs& a, int64_t row, int c, const float (&h)[8], const Raw<WT>& w,
-                                        float rstd, double rstd_d) {
+                                        double rstd) {
+    // FP32 holds 1 / rms in full once h is brought near 1 by a power of two, where it is far from it (an rms of
+    // subnormals has a 1 / rms beyond FP32's range, one near the largest value a subnormal 1 / rms).
+    const float by = (float)rstd;
     float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = h[j] * rstd * w.at(j);
+    for (int j = 0; j < 8; ++j) v[j] = h[j] * by * w.at(j);
+    // An rms of subnormals has a 1 / rms beyond FP32's range, one near the largest value a subnormal 1 / rms: far from
+    // 1, h is brought near it by a power of two first.
+    if (__builtin_expect(!(by < 0x1p64f && by > 0x1p-64f), 0)) {
+        const float up = by < 1.0f ? 0x1p-64f : 0x1p96f, rest = (float)(rstd * (by < 1.0f ? 0x1p64 : 0x1p-96));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = h[j] * up * rest * w.at(j);
+    }
     if (a.x_q) {
         uint32_t m = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
         m = quad_max(m);
         int code = scale_code(m);
-        if (near_border(m)) code = exact_code<XT, RT, WT>(a, row, c, rstd_d);
+        if (near_border(m)) code = exact_code<XT, RT, WT>(a, row, c, rstd);
         const float inv = __uint_as_float((uint32_t)(254 - code) << 23);  // 2^(127 - code)
         int q0 = 0, q1 = 0;
         q0 = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, q0, false);
@@ -235,7 +245,7 @@ __global__ __launch_bounds__(kShortThreads) void norm_short_kernel(NormArgs a) {
     cell.sum(a, h);
     const double sum = lanes_sum<L>(c < a.H ? cell.squares(a, h, 0.0) : 0.0);
     const double rstd = 1.0 / sqrt(sum / a.H + (double)a.eps);
-    if (t < a.T && c < a.H) finish8<XT, RT, WT>(a, row, c, h, w, (float)rstd, rstd);
+    if (t < a.T && c < a.H) finish8<XT, RT, WT>(a, row, c, h, w, rstd);
 }
 
 constexpr int kMaxThreads = 1024;
@@ -266,7 +276,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_row_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int c = threadIdx.x * 8 + i * step;
-        if (c < a.H) finish8<XT, RT, WT>(a, row, c, h[i], w[i], (float)rstd, rstd);
+        if (c < a.H) finish8<XT, RT, WT>(a, row, c, h[i], w[i], rstd);
     }
 }
 
@@ -293,7 +303,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_long_kernel(NormArgs a) {
         cell.load(a, row, c);
         w.load(a.weight, c);
         cell.sum(a, h);
-        finish8<XT, RT, WT>(a, row, c, h, w, (float)rstd, rstd);
+        finish8<XT, RT, WT>(a, row, c, h, w, rstd);
     }
 }
 

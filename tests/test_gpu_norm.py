@@ -281,3 +281,27 @@ def test_norm_sums_beyond_fp32(gpu, H):
         assert (np.delete(y[t].numpy(), c) == 0).all() and (np.delete(q[t], c) == 0).all()
     keep = [0, 3, 4]
     check({k: v[keep] for k, v in out.items()}, x[keep], r[keep], w, 1e-6)
+
+
+@pytest.mark.parametrize("power", [-140, -130, -120, -70, 70, 110, 124])
+def test_norm_far_from_one_without_eps(gpu, power):
+    """Rows whose 1 / rms FP32 does not hold, or not in full: sizes, and blocks on a border of the scale."""
+    for rt in (None, F32):
+        x, r, w = draw(4, 1024, F32, rt, F32, 15, gpu)
+        x = torch.ldexp(x.clamp(-4, 4), torch.tensor(power))
+        r = None if r is None else torch.ldexp(r.clamp(-4, 4), torch.tensor(power))
+        check(run(x, r, w, eps=0.0, rt=F32), x, r, w, 0.0)
+    g = torch.Generator().manual_seed(power + 200)
+    codes, H = set(), 224
+    for _ in range(40):
+        x = torch.ldexp(torch.randn(1, H, generator=g).clamp(-4, 4), torch.tensor(power))
+        x[0, 31::32] = x[0, 31::32].abs() + 2.0 ** (power - 1)
+        w = torch.full((H,), 0.25)
+        rstd = 1 / x.double().square().mean().sqrt()
+        step = 1 + torch.randint(-2, 3, (H // 32,), generator=g).double() * 2.0 ** -24
+        w[31::32] = (3.5 * step / (x[0, 31::32].double() * rstd)).float()
+        x, w = x.to(gpu), w.to(gpu)
+        out = run(x, None, w, eps=0.0, rt=F32, outs=("q", "y"))
+        codes |= set(norm_ref(f64(x), f64(w), 0.0)[2].ravel().tolist())
+        check(out, x, None, w, 0.0)
+    assert codes == {120, 121}
