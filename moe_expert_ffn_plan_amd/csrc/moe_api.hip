@@ -6,6 +6,7 @@
 // sections 5-6), one forward entry point with strict shape checks that
 // answer "unsupported" (reading notes, "host-side checks").
 #include <atomic>
+#include <cfloat>
 #include <cstring>
 #include <mutex>
 
@@ -409,7 +410,7 @@ int check_norm(const moe_norm_shape* s) {
     if (!s) return MOE_ERR_NULL;
     if (!tokens_ok(s->num_tokens) || !type_ok(s->x_type) || !type_ok(s->residual_type) || !type_ok(s->weight_type))
         return MOE_ERR_SHAPE;
-    if (!(s->eps >= 0.0f && s->eps <= 3.0e38f)) return MOE_ERR_SHAPE;  // also rejects NaN
+    if (!(s->eps >= 0.0f && s->eps <= FLT_MAX)) return MOE_ERR_SHAPE;  // also rejects NaN
     int st = check_hidden(s->hidden);
     for (const int64_t stride : {s->x_stride, s->residual_stride, s->residual_out_stride})
         if (st == MOE_OK) st = check_stride(stride, s->hidden);
@@ -435,7 +436,7 @@ int check_gate(const moe_gate_shape* s) {
     if ((int64_t)s->num_tokens * s->topk >= (1ll << 30)) return MOE_ERR_SHAPE;
     if (!flag_ok(s->score) || !flag_ok(s->group_score) || !flag_ok(s->renormalize) || !type_ok(s->logits_type))
         return MOE_ERR_SHAPE;
-    if (!(s->scale >= -3.0e38f && s->scale <= 3.0e38f)) return MOE_ERR_SHAPE;  // also rejects NaN
+    if (!(s->scale >= -FLT_MAX && s->scale <= FLT_MAX)) return MOE_ERR_SHAPE;  // also rejects NaN
     if (s->logits_stride != 0 && (s->logits_stride < s->num_experts || s->logits_stride > (1ll << 40)))
         return MOE_ERR_SHAPE;
     return MOE_OK;

@@ -186,3 +186,10 @@ def test_binding_row_checks(monkeypatch):
         B._rows(t.t(), torch.float32, "x", dev, 40, 4, 0)
     with pytest.raises(TypeError):
         B._rows(t, torch.bfloat16, "x", dev, 4, 40, 0)
+
+
+def test_every_finite_eps_and_scale():
+    """The largest finite values are allowed, either sign of the scale; no tokens, so that no GPU is asked for."""
+    for v in (0.0, 1e-45, 3.1e38, torch.finfo(torch.float32).max):
+        assert norm(B.make_norm(0, 256, eps=v)) == 0
+        assert gate(B.make_gate(0, 32, 4, scale=v)) == 0 and gate(B.make_gate(0, 32, 4, scale=-v)) == 0
