@@ -464,6 +464,11 @@ MOE_API int moe_router_prepare(const moe_router_shape* shape, const void* w, uin
  * ws may be NULL. */
 MOE_API int moe_router_workspace_bytes(const moe_router_shape* shape, size_t* bytes);
 
+/* How moe_router_logits takes a shape: the tokens and experts of a tile, and
+ * the parts that a tile's columns are split into (1: one pass, no workspace).
+ * For inspection. */
+MOE_API int moe_router_tile(const moe_router_shape* shape, int32_t* tokens, int32_t* experts, int32_t* splits);
+
 /*   x        [T, H] BF16 (moe_norm_quant's y)
  *   w_tiled  from moe_router_prepare for the same hidden, num_experts and
  *            weight_type

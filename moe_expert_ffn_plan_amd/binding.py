@@ -72,7 +72,7 @@ EXPORTS = ["moe_capacity_rows", "moe_suggest_block_m", "moe_gemm_launches", "moe
            "moe_forward_workspace_bytes", "moe_forward", "moe_linear1", "moe_linear2", "moe_combine",
            "moe_expert_ffn", "moe_prepare_weights", "moe_forward_noalloc",
            "moe_norm_quant", "moe_router_weight_bytes", "moe_router_prepare", "moe_router_workspace_bytes",
-           "moe_router_logits", "moe_gate",
+           "moe_router_tile", "moe_router_logits", "moe_gate",
            "moe_forward_view_get", "moe_device_supported", "moe_status_str"]
 
 
@@ -105,6 +105,7 @@ def lib() -> ctypes.CDLL:
         L.moe_router_weight_bytes.argtypes = [R, P(SZ)]
         L.moe_router_prepare.argtypes = [R, VP, VP, VP]
         L.moe_router_workspace_bytes.argtypes = [R, P(SZ)]
+        L.moe_router_tile.argtypes = [R, P(ctypes.c_int32), P(ctypes.c_int32), P(ctypes.c_int32)]
         L.moe_router_logits.argtypes = [R, VP, VP, VP, VP, SZ, VP]
         L.moe_gate.argtypes = [G, VP, VP, VP, VP, VP]
         L.moe_device_supported.argtypes = [ctypes.c_int]
@@ -478,6 +479,13 @@ def router_workspace_bytes(shape: RouterShape) -> int:
     v = ctypes.c_size_t()
     _check("moe_router_workspace_bytes", lib().moe_router_workspace_bytes(ctypes.byref(shape), ctypes.byref(v)))
     return v.value
+
+
+def router_tile(shape: RouterShape) -> tuple[int, int, int]:
+    """moe_router_tile: (tokens of a tile, experts of a tile, splits of its columns) of moe_router_logits."""
+    v = [ctypes.c_int32() for _ in range(3)]
+    _check("moe_router_tile", lib().moe_router_tile(ctypes.byref(shape), *(ctypes.byref(i) for i in v)))
+    return tuple(i.value for i in v)
 
 
 def router_prepare(shape: RouterShape, w, stream=None) -> torch.Tensor:

@@ -481,6 +481,18 @@ int moe_router_workspace_bytes(const moe_router_shape* shape, size_t* bytes) {
     return MOE_OK;
 }
 
+int moe_router_tile(const moe_router_shape* shape, int32_t* tokens, int32_t* experts, int32_t* splits) {
+    if (!tokens || !experts || !splits) return MOE_ERR_NULL;
+    const int st = check_router(shape);
+    if (st != MOE_OK) return st;
+    const RouterChoice c =
+        choose_router(shape->num_tokens, shape->hidden, shape->num_experts, router_parts(shape->weight_type));
+    *tokens = c.tokens;
+    *experts = c.experts;
+    *splits = c.splits;
+    return MOE_OK;
+}
+
 int moe_router_prepare(const moe_router_shape* shape, const void* w, uint8_t* w_tiled, void* stream) {
     int st = check_router(shape);
     if (st != MOE_OK) return st;

@@ -232,7 +232,7 @@ struct RouterArgs {
 };
 inline int router_parts(int weight_type) { return weight_type == MOE_F32 ? 3 : 1; }
 struct RouterChoice {
-    int kernel, splits;  // kernel: moe_router.hip's own numbers
+    int kernel, tokens, experts, splits;  // kernel: moe_router.hip's own numbers; a tile's tokens and experts
     size_t workspace_bytes(int T, int E) const { return splits > 1 ? (size_t)splits * T * E * sizeof(float) : 0; }
 };
 RouterChoice choose_router(int T, int H, int E, int parts);

@@ -552,6 +552,10 @@ constexpr Tiling kF32[] = {
     {kSmall, 16, 16, 64, 0.028}, {kTile32x64, 32, 64, 128, 0.095}, {kTile64x64, 64, 64, 128, 0.140},
     {kTile64x128, 64, 128, 64, 0.235}, {kTile128x128, 128, 128, 64, 0.385}};
 
+// Tokens of a launch: tiles of 64 x 128 or more, and of 64 x 64 up to 64 experts, then fit one for any number of experts,
+// and none of them is split (more tiles than CUs).
+constexpr int kLaunchRows = 1 << 24;
+
 int div_up(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 template <int P>
@@ -582,8 +586,9 @@ hipError_t launch_tile(const RouterArgs& r, int splits, hipStream_t stream) {
 }  // namespace
 
 RouterChoice choose_router(int T, int H, int E, int parts) {
-    RouterChoice best{kSmall, 1};
+    RouterChoice best{kSmall, kSmallTokens, 16, 1};
     if (T == 0) return best;
+    T = std::min(T, kLaunchRows);
     double least = INFINITY;
     auto consider = [&](const Tiling& c) {
         if (c.kernel == kSmall && T > kSmallMost) return;
@@ -603,7 +608,7 @@ RouterChoice choose_router(int T, int H, int E, int parts) {
             double us = 2.4 + div_up(groups, kCus) * (0.84 + H / 32 * c.cost / s * (1.0 + 0.44 * used));
             if (s > 1) us += 2.2 + 0.46e-6 * sizeof(float) * s * T * E;
             us = std::max(us, s > 1 ? 6.6 : 4.1);
-            if (us < least) least = us, best = RouterChoice{c.kernel, s};
+            if (us < least) least = us, best = RouterChoice{c.kernel, c.bm, c.bn, s};
         }
     };
     if (parts == 3)
@@ -623,7 +628,8 @@ hipError_t launch_router_prepare(int H, int E, int weight_type, const void* w, u
     return hipGetLastError();
 }
 
-hipError_t launch_router_logits(const RouterArgs& a, RouterChoice c, hipStream_t stream) {
+namespace {
+hipError_t launch_rows(const RouterArgs& a, RouterChoice c, hipStream_t stream) {
     const bool f32 = a.parts == 3;
     switch ((Kernel)c.kernel) {
         case kSmall: return f32 ? launch_small<3>(a, stream) : launch_small<1>(a, stream);
@@ -646,6 +652,19 @@ hipError_t launch_router_logits(const RouterArgs& a, RouterChoice c, hipStream_t
         case kTile128x256: return launch_tile<Tile<128, 4, 4, 128, 1>>(a, c.splits, stream);
     }
     return hipErrorInvalidValue;
+}
+}  // namespace
+
+hipError_t launch_router_logits(const RouterArgs& a, RouterChoice c, hipStream_t stream) {
+    for (int64_t t = 0; t < a.T; t += kLaunchRows) {
+        RouterArgs part = a;
+        part.x += t * a.x_stride;
+        part.logits += t * a.E;
+        part.T = (int)std::min<int64_t>(a.T - t, kLaunchRows);
+        const hipError_t e = launch_rows(part, c, stream);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace moe

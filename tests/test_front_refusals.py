@@ -193,3 +193,20 @@ def test_every_finite_eps_and_scale():
     for v in (0.0, 1e-45, 3.1e38, torch.finfo(torch.float32).max):
         assert norm(B.make_norm(0, 256, eps=v)) == 0
         assert gate(B.make_gate(0, 32, 4, scale=v)) == 0 and gate(B.make_gate(0, 32, 4, scale=-v)) == 0
+
+
+@pytest.mark.parametrize("weight", [torch.bfloat16, torch.float32])
+def test_router_tiles_of_all_sizes(weight):
+    """Tiles of 16 tokens have a grid axis of 65535 for them: no allowed size past 1024 tokens takes them, and the
+    tiles of a launch times its threads fit 32 bits."""
+    with pytest.raises(B.MoeError):
+        B.router_tile(B.make_router(4, 48, 8))
+    assert B.router_tile(B.make_router(0, 64, 8))[2] == 1
+    rows = (1, 16, 1024, 1025, 1 << 17, 1 << 24, (1 << 24) + 1, (1 << 27) - 1, (1 << 27) + 1, 180_000_000, (1 << 28) - 1)
+    for T in rows:
+        for hidden in (32, 96, 7168, 1 << 20):
+            for E in (1, 17, 64, 65, 129, 256, 257, 385, 513, 770, 1024):
+                m, n, splits = B.router_tile(B.make_router(T, hidden, E, weight_dtype=weight))
+                assert (m == 16) <= (T <= 1024), (T, hidden, E, m, n)
+                tiles = -(-min(T, 1 << 24) // m) * -(-E // n) * splits
+                assert tiles * (1024 if m == 16 else 512) < 1 << 32, (T, hidden, E, m, n)

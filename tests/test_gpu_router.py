@@ -206,3 +206,18 @@ def test_router_binding_refusals(gpu):
         B.router_prepare(s, w.float())
     with pytest.raises(ValueError):
         B.router_prepare(s, w[:7])
+
+
+@pytest.mark.parametrize("wt", [BF16, F32])
+def test_router_more_rows_than_a_launch(gpu, wt):
+    """Over 2^24 tokens, strided; sums of small whole numbers, so FP32 products of any order are exact too."""
+    T, H, E = (1 << 24) + 3001, 32, 20
+    g = torch.Generator(device=gpu).manual_seed(30)
+    wide = torch.randint(-15, 16, (T, 40), generator=g, device=gpu, dtype=torch.int8).to(BF16)
+    w = torch.randint(-3, 4, (E, H), generator=g, device=gpu).to(wt)
+    got = run(wide[:, :H], w, shape=B.make_router(T, H, E, weight_dtype=wt, x_stride=40))
+    for rows in (slice(0, 5000), slice((1 << 24) - 5000, T)):
+        assert torch.equal(got[rows], wide[rows, :H].float() @ w.float().t().contiguous())
+    both = w.float().sum(0)
+    for x, l in zip(wide.split(1 << 22), got.split(1 << 22)):    # (the library's product with a vector stops at 2^24 rows)
+        assert torch.equal(l.sum(1), (x[:, :H].float() * both).sum(1))
