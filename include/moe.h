@@ -460,9 +460,13 @@ typedef struct moe_router_shape {
 MOE_API int moe_router_weight_bytes(const moe_router_shape* shape, size_t* bytes);
 MOE_API int moe_router_prepare(const moe_router_shape* shape, const void* w, uint8_t* w_tiled, void* stream);
 
-/* Bytes of moe_router_logits' workspace (partial sums); may be 0, and then
- * ws may be NULL. */
+/* Bytes of moe_router_logits' workspace (partial sums) for this shape; may be
+ * 0, and then ws may be NULL.  More tokens may need LESS (0 where their tiles
+ * fill the GPU in one pass): a workspace that is to serve calls of different
+ * num_tokens takes moe_router_max_workspace_bytes of the most tokens, enough
+ * for every num_tokens from 0 to shape->num_tokens (256 MiB at most). */
 MOE_API int moe_router_workspace_bytes(const moe_router_shape* shape, size_t* bytes);
+MOE_API int moe_router_max_workspace_bytes(const moe_router_shape* shape, size_t* bytes);
 
 /* How moe_router_logits takes a shape: the tokens and experts of a tile, and
  * the parts that a tile's columns are split into (1: one pass, no workspace).

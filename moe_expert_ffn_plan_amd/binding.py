@@ -72,7 +72,7 @@ EXPORTS = ["moe_capacity_rows", "moe_suggest_block_m", "moe_gemm_launches", "moe
            "moe_forward_workspace_bytes", "moe_forward", "moe_linear1", "moe_linear2", "moe_combine",
            "moe_expert_ffn", "moe_prepare_weights", "moe_forward_noalloc",
            "moe_norm_quant", "moe_router_weight_bytes", "moe_router_prepare", "moe_router_workspace_bytes",
-           "moe_router_tile", "moe_router_logits", "moe_gate",
+           "moe_router_max_workspace_bytes", "moe_router_tile", "moe_router_logits", "moe_gate",
            "moe_forward_view_get", "moe_device_supported", "moe_status_str"]
 
 
@@ -105,6 +105,7 @@ def lib() -> ctypes.CDLL:
         L.moe_router_weight_bytes.argtypes = [R, P(SZ)]
         L.moe_router_prepare.argtypes = [R, VP, VP, VP]
         L.moe_router_workspace_bytes.argtypes = [R, P(SZ)]
+        L.moe_router_max_workspace_bytes.argtypes = [R, P(SZ)]
         L.moe_router_tile.argtypes = [R, P(ctypes.c_int32), P(ctypes.c_int32), P(ctypes.c_int32)]
         L.moe_router_logits.argtypes = [R, VP, VP, VP, VP, SZ, VP]
         L.moe_gate.argtypes = [G, VP, VP, VP, VP, VP]
@@ -478,6 +479,14 @@ def router_weight_bytes(shape: RouterShape) -> int:
 def router_workspace_bytes(shape: RouterShape) -> int:
     v = ctypes.c_size_t()
     _check("moe_router_workspace_bytes", lib().moe_router_workspace_bytes(ctypes.byref(shape), ctypes.byref(v)))
+    return v.value
+
+
+def router_max_workspace_bytes(shape: RouterShape) -> int:
+    """moe_router_max_workspace_bytes: enough for every number of tokens up to shape.num_tokens (more tokens may need
+    less, see router_workspace_bytes)."""
+    v = ctypes.c_size_t()
+    _check("moe_router_max_workspace_bytes", lib().moe_router_max_workspace_bytes(ctypes.byref(shape), ctypes.byref(v)))
     return v.value
 
 

@@ -481,6 +481,14 @@ int moe_router_workspace_bytes(const moe_router_shape* shape, size_t* bytes) {
     return MOE_OK;
 }
 
+int moe_router_max_workspace_bytes(const moe_router_shape* shape, size_t* bytes) {
+    if (!bytes) return MOE_ERR_NULL;
+    const int st = check_router(shape);
+    if (st != MOE_OK) return st;
+    *bytes = most_router_workspace(shape->num_tokens, shape->hidden, shape->num_experts, router_parts(shape->weight_type));
+    return MOE_OK;
+}
+
 int moe_router_tile(const moe_router_shape* shape, int32_t* tokens, int32_t* experts, int32_t* splits) {
     if (!tokens || !experts || !splits) return MOE_ERR_NULL;
     const int st = check_router(shape);

@@ -236,6 +236,7 @@ struct RouterChoice {
     size_t workspace_bytes(int T, int E) const { return splits > 1 ? (size_t)splits * T * E * sizeof(float) : 0; }
 };
 RouterChoice choose_router(int T, int H, int E, int parts);
+size_t most_router_workspace(int T, int H, int E, int parts);  // at least that of any choice for 0 .. T tokens
 hipError_t launch_router_prepare(int H, int E, int weight_type, const void* w, uint8_t* w_tiled, hipStream_t stream);
 hipError_t launch_router_logits(const RouterArgs& a, RouterChoice c, hipStream_t stream);
 

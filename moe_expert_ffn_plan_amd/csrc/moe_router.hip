@@ -583,6 +583,31 @@ hipError_t launch_tile(const RouterArgs& r, int splits, hipStream_t stream) {
     return hipGetLastError();
 }
 
+bool allowed(const Tiling& c, int E) {
+    if (c.kernel == kBig) return E > 256 && E <= Big::BN;
+    return c.bn <= 64 || c.bn < 2 * E;  // the others are not measured
+}
+
+// f(s) for each number of splits to choose from: two K-steps at least, two workgroups a CU at most.
+template <class F>
+void each_split(const Tiling& c, int64_t tiles, int H, F&& f) {
+    f(1);
+    if (c.kernel == kSmall || c.kernel == kBig || tiles > kCus) return;
+    const int steps = div_up(H, c.bk);
+    const int fill = std::min(kCus / (int)tiles, steps / 4);  // four K-steps at least
+    for (const int s : {2, 4, 8, fill})
+        if (s > 1 && 2 * s <= steps && s * tiles <= 2 * kCus) f(s);
+}
+constexpr int64_t kMostPartial = 1 << 26;  // floats of partial sums
+
+template <class F>
+void each_tiling(int parts, F&& f) {
+    if (parts == 3)
+        for (const Tiling& c : kF32) f(c);
+    else
+        for (const Tiling& c : kBf16) f(c);
+}
+
 }  // namespace
 
 RouterChoice choose_router(int T, int H, int E, int parts) {
@@ -590,32 +615,35 @@ RouterChoice choose_router(int T, int H, int E, int parts) {
     if (T == 0) return best;
     T = std::min(T, kLaunchRows);
     double least = INFINITY;
-    auto consider = [&](const Tiling& c) {
-        if (c.kernel == kSmall && T > kSmallMost) return;
-        if (c.kernel == kBig && (E <= 256 || E > Big::BN)) return;
-        if (c.bn > 64 && c.bn >= 2 * E) return;  // not measured
+    each_tiling(parts, [&](const Tiling& c) {
+        if (!allowed(c, E) || (c.kernel == kSmall && T > kSmallMost)) return;
         const int64_t tiles = (int64_t)div_up(T, c.bm) * div_up(E, c.bn);
         if (tiles > 1 << 22) return;  // times 512 threads: what a launch takes
-        const int steps = div_up(H, c.bk);
-        const bool whole = c.kernel == kSmall || c.kernel == kBig;
-        const int fill = tiles < kCus ? std::min(kCus / (int)tiles, steps / 4) : 1;  // four K-steps at least
-        for (const int s : {1, 2, 4, 8, fill}) {
-            // splits: two K-steps at least, two workgroups a CU and 256 MB of partial sums at most
-            if (s < 1) continue;
-            if (s > 1 && (whole || 2 * s > steps || s * tiles > 2 * kCus || (int64_t)s * T * E > 1 << 26)) continue;
+        each_split(c, tiles, H, [&](int s) {
+            if (s > 1 && (int64_t)s * T * E > kMostPartial) return;
             const int groups = (int)tiles * s;
             const double used = (double)std::min(groups, kCus) / kCus;
             double us = 2.4 + div_up(groups, kCus) * (0.84 + H / 32 * c.cost / s * (1.0 + 0.44 * used));
             if (s > 1) us += 2.2 + 0.46e-6 * sizeof(float) * s * T * E;
             us = std::max(us, s > 1 ? 6.6 : 4.1);
             if (us < least) least = us, best = RouterChoice{c.kernel, c.bm, c.bn, s};
-        }
-    };
-    if (parts == 3)
-        for (const Tiling& c : kF32) consider(c);
-    else
-        for (const Tiling& c : kBf16) consider(c);
+        });
+    });
     return best;
+}
+
+// Every tiling at every number of rows of tiles that it may split, whatever the estimate says of it.
+size_t most_router_workspace(int T, int H, int E, int parts) {
+    int64_t most = 0;
+    each_tiling(parts, [&](const Tiling& c) {
+        if (!allowed(c, E)) return;
+        const int across = div_up(E, c.bn);
+        for (int m = 1; m <= div_up(T, c.bm) && m * across <= kCus; ++m)
+            each_split(c, (int64_t)m * across, H, [&](int s) {
+                if (s > 1) most = std::max(most, std::min((int64_t)s * std::min(m * c.bm, T) * E, kMostPartial));
+            });
+    });
+    return (size_t)most * sizeof(float);
 }
 
 hipError_t launch_router_prepare(int H, int E, int weight_type, const void* w, uint8_t* w_tiled, hipStream_t stream) {

@@ -210,3 +210,24 @@ def test_router_tiles_of_all_sizes(weight):
                 assert (m == 16) <= (T <= 1024), (T, hidden, E, m, n)
                 tiles = -(-min(T, 1 << 24) // m) * -(-E // n) * splits
                 assert tiles * (1024 if m == 16 else 512) < 1 << 32, (T, hidden, E, m, n)
+
+
+@pytest.mark.parametrize("weight", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("hidden,E", [(7168, 256), (7168, 384), (4096, 64), (1 << 20, 1024), (512, 40), (64, 8), (32, 300)])
+def test_router_workspace_of_the_most_tokens(hidden, E, weight):
+    """One workspace for all batches up to the largest, which may itself need none."""
+    need = {T: B.router_workspace_bytes(B.make_router(T, hidden, E, weight_dtype=weight))
+            for T in [*range(0, 700), *range(700, 40000, 131), 65536, 1 << 20, (1 << 24) + 1, (1 << 28) - 1]}
+    before = seen = 0
+    for T in sorted(need):
+        seen = max(seen, need[T])
+        most = B.router_max_workspace_bytes(B.make_router(T, hidden, E, weight_dtype=weight))
+        assert max(seen, before) <= most <= 1 << 28, T
+        before = most
+    some = max(need, key=need.get)
+    if need[some]:
+        s = B.make_router(some, hidden, E, weight_dtype=weight)
+        assert router(s, ws_bytes=need[some] - 1) == -4
+    bad = B.make_router(4, 48, 8)
+    assert B.lib().moe_router_max_workspace_bytes(ctypes.byref(bad), ctypes.byref(ctypes.c_size_t())) == -3
+    assert B.lib().moe_router_max_workspace_bytes(ctypes.byref(bad), None) == -1

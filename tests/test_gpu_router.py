@@ -221,3 +221,22 @@ def test_router_more_rows_than_a_launch(gpu, wt):
     both = w.float().sum(0)
     for x, l in zip(wide.split(1 << 22), got.split(1 << 22)):    # (the library's product with a vector stops at 2^24 rows)
         assert torch.equal(l.sum(1), (x[:, :H].float() * both).sum(1))
+
+
+@pytest.mark.parametrize("wt", [BF16, F32])
+def test_router_one_workspace_for_all_batches(gpu, wt):
+    """A workspace of the largest batch serves the smaller ones, of which some need more than the largest."""
+    H, E, most = 7168, 256, 20000
+    x, w = whole(most, H, E, wt, 31, gpu)
+    want = x.double() @ w.double().t().contiguous()
+    shape = B.make_router(most, H, E, weight_dtype=wt)
+    tiled = B.router_prepare(shape, w)
+    ws = torch.full((B.router_max_workspace_bytes(shape),), 0x5A, dtype=torch.uint8, device=gpu)
+    own = []
+    for T in (most, 1, 33, 128, 300, 512, 1000, 2048, 4096, 8192, 16384):
+        s = B.make_router(T, H, E, weight_dtype=wt)
+        own.append(B.router_workspace_bytes(s))
+        logits = torch.full((T, E), float("nan"), device=gpu)
+        B.router_logits(s, x[:T], tiled, logits, ws)
+        assert torch.equal(logits.double(), want[:T])
+    assert max(own) > 0
