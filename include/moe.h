@@ -425,8 +425,9 @@ typedef struct moe_norm_shape {
  *   residual     [T, H] residual_type, or NULL
  *   weight       [H] weight_type
  *   residual_out [T, H] residual_type, or NULL.  May be residual itself
- *                (same stride), or x itself where type and stride agree;
- *                no other overlap of outputs and inputs is allowed.
+ *                (same stride), or x itself where type and stride agree
+ *                (else MOE_ERR_SHAPE); no other overlap of outputs and
+ *                inputs is allowed.
  *   y            [T, H] BF16, or NULL
  *   x_q, x_sf    uint8 [T, H] and [T, H/32], or both NULL
  * At least one of y and x_q must be given. */

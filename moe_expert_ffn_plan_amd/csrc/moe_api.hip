@@ -455,12 +455,18 @@ int moe_norm_quant(const moe_norm_shape* shape, const void* x, const void* resid
     if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16) ||
         !aligned(y, 16) || !aligned(x_q, 16))
         return MOE_ERR_ALIGN;
-    if ((st = check_arch_current()) != MOE_OK) return st;
     const int H = shape->hidden;
     const NormArgs a{x, residual, weight, residual_out, y, x_q, x_sf,
                      stride_or(shape->x_stride, H), stride_or(shape->residual_stride, H),
                      stride_or(shape->residual_out_stride, H), shape->num_tokens, H,
                      shape->x_type, shape->residual_type, shape->weight_type, shape->eps};
+    // in place an output element lies where its own input was, or it overwrites another row's
+    const bool rows = a.T > 1;
+    if (residual_out && residual_out == residual && rows && a.residual_out_stride != a.residual_stride) return MOE_ERR_SHAPE;
+    if (residual_out && residual_out == x &&
+        ((rows && a.residual_out_stride != a.x_stride) || shape->residual_type != shape->x_type))
+        return MOE_ERR_SHAPE;
+    if ((st = check_arch_current()) != MOE_OK) return st;
     return launch_norm_quant(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 

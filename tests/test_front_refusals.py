@@ -231,3 +231,17 @@ def test_router_workspace_of_the_most_tokens(hidden, E, weight):
     bad = B.make_router(4, 48, 8)
     assert B.lib().moe_router_max_workspace_bytes(ctypes.byref(bad), ctypes.byref(ctypes.c_size_t())) == -3
     assert B.lib().moe_router_max_workspace_bytes(ctypes.byref(bad), None) == -1
+
+
+def test_norm_in_place_needs_one_layout():
+    """residual_out on the memory of x or the residual, but with rows elsewhere: one row's output on another's input."""
+    at = lambda i: ctypes.c_void_p(0x10000 * i)  # noqa: E731
+    for change in (dict(residual_stride=512), dict(residual_out_stride=264)):
+        assert norm(B.make_norm(**NORM, **change), residual=at(2), residual_out=at(2)) == -2
+    for change in (dict(x_stride=512), dict(residual_out_stride=264), dict(x_dtype=torch.float32),
+                   dict(x_dtype=torch.float32, x_stride=264, residual_out_stride=264)):
+        assert norm(B.make_norm(**NORM, **change), residual=at(2), residual_out=FAKE) == -2
+        assert norm(B.make_norm(**NORM, **change), residual_out=FAKE) == -2
+    # x and the residual are one buffer of two layouts: residual_out has to be that of both
+    s = B.make_norm(**NORM, x_stride=512, residual_stride=256, residual_out_stride=256)
+    assert norm(s, residual=FAKE, residual_out=FAKE) == -2

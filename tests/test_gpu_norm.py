@@ -305,3 +305,12 @@ def test_norm_far_from_one_without_eps(gpu, power):
         codes |= set(norm_ref(f64(x), f64(w), 0.0)[2].ravel().tolist())
         check(out, x, None, w, 0.0)
     assert codes == {120, 121}
+
+
+def test_norm_one_row_in_place_of_any_stride(gpu):
+    """A single row has no next one for a stride to say anything about."""
+    x, r, w = draw(1, 512, BF16, BF16, BF16, 17, gpu)
+    want = run(x, r, w)
+    got = run(x, r, w, rout=r, shape=B.make_norm(1, 512, x_stride=512, residual_stride=1024, residual_out_stride=520))
+    for k in want:
+        assert torch.equal(got[k].view(torch.uint8), want[k].view(torch.uint8)), k
