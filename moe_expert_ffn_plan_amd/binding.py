@@ -170,6 +170,14 @@ def _stream(stream):
     return ctypes.c_void_p(_raw_stream(_device()))
 
 
+def _new(numel, device, stream):
+    """A uint8 tensor whose memory belongs to `stream` (None: the current one), which the caller writes it on."""
+    if stream is None:
+        return torch.empty(numel, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(numel, dtype=torch.uint8, device=device)
+
+
 def capacity_rows(shape: MoeShape) -> int:
     v = ctypes.c_int64()
     _check("moe_capacity_rows", lib().moe_capacity_rows(ctypes.byref(shape), ctypes.byref(v)))
@@ -290,8 +298,7 @@ def prepare_weights(shape: MoeShape, which: int, w, w_sf, stream=None):
     dev = w.device
     _ptr(w, torch.uint8, "w", dev, E * N * K // 2)
     _ptr(w_sf, torch.uint8, "w_sf", dev, E * N * K // 32)
-    wt = torch.empty(E * N * K // 2, dtype=torch.uint8, device=dev)
-    st_ = torch.empty(E * N * K // 32, dtype=torch.uint8, device=dev)
+    wt, st_ = _new(E * N * K // 2, dev, stream), _new(E * N * K // 32, dev, stream)
     st = lib().moe_prepare_weights(ctypes.byref(shape), which, _ptr(w, torch.uint8, "w"), _ptr(w_sf, torch.uint8, "w_sf"),
                                    _ptr(wt, torch.uint8, "w_tiled"), _ptr(st_, torch.uint8, "w_sf_tiled"), _stream(stream))
     _check("moe_prepare_weights", st)
@@ -500,7 +507,7 @@ def router_tile(shape: RouterShape) -> tuple[int, int, int]:
 def router_prepare(shape: RouterShape, w, stream=None) -> torch.Tensor:
     """moe_router_prepare: tiled copy (a new tensor) of the router weights w [num_experts, hidden]."""
     dev = _here(w, "w")
-    out = torch.empty(router_weight_bytes(shape), dtype=torch.uint8, device=dev)
+    out = _new(router_weight_bytes(shape), dev, stream)
     p = _ptr(w, _dtype(shape.weight_type), "w", dev, shape.num_experts * shape.hidden)
     _check("moe_router_prepare", lib().moe_router_prepare(ctypes.byref(shape), p, _ptr(out, torch.uint8, "w_tiled"),
                                                           _stream(stream)))

@@ -245,3 +245,41 @@ def test_norm_in_place_needs_one_layout():
     # x and the residual are one buffer of two layouts: residual_out has to be that of both
     s = B.make_norm(**NORM, x_stride=512, residual_stride=256, residual_out_stride=256)
     assert norm(s, residual=FAKE, residual_out=FAKE) == -2
+
+
+def test_prepared_weights_belong_to_the_stream(monkeypatch):
+    """The tensors that router_prepare and prepare_weights return are allocated on the stream that writes them: on
+    another, memory that its pending work still uses could be handed out."""
+    class Said(torch.Tensor):
+        is_cuda = True
+
+    class Stream:
+        cuda_stream = 7
+        inside = False
+
+        def __enter__(self):
+            Stream.inside = True
+
+        def __exit__(self, *_):
+            Stream.inside = False
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: 0
+
+    made, empty = [], torch.empty
+
+    def recorded(*a, **kw):
+        made.append(Stream.inside)
+        return empty(*a, **kw).as_subclass(Said)
+
+    monkeypatch.setattr(B, "lib", Lib)
+    monkeypatch.setattr(B, "_here", lambda t, name: t.device)
+    monkeypatch.setattr(B, "router_weight_bytes", lambda s: 1024)
+    monkeypatch.setattr(torch, "empty", recorded)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    w = torch.zeros(16, 32, dtype=torch.bfloat16).as_subclass(Said)
+    u8 = lambda n: torch.zeros(n, dtype=torch.uint8).as_subclass(Said)  # noqa: E731
+    B.router_prepare(B.make_router(1, 32, 16), w, stream=Stream())
+    B.prepare_weights(B.make_shape(1, 256, 256, 1, 1, 16), 1, u8(512 * 128), u8(512 * 8), stream=Stream())
+    assert made == [True, True, True]

@@ -203,3 +203,21 @@ def test_bound_calls(gpu):
         c()
     torch.cuda.synchronize()
     assert same(state(L, mine)[:7], want[:7])
+
+
+def test_weights_prepared_on_a_side_stream(gpu):
+    """Prepared weights do not share memory with pending work of the current stream, which is still to write it."""
+    L = Layer(gpu)
+    want, moe = L.router_t.clone(), {k: v.to(gpu) for k, v in L.weights.items()}
+    a = torch.randn(4096, 4096, device=gpu)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(60):                                    # keeps the current stream busy
+        a = (a @ a).clamp_(-1, 1)
+    for t in (L.router_t, *L.tiled.values()):
+        torch.empty_like(t).fill_(7)                       # written after that, and free at once
+    got = B.router_prepare(L.router, L.router_w, stream=side)
+    tiled = B.prepare_all(L.moe, moe, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert all(torch.equal(tiled[k], L.tiled[k]) for k in tiled)
