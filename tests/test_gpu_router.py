@@ -240,3 +240,43 @@ def test_router_one_workspace_for_all_batches(gpu, wt):
         B.router_logits(s, x[:T], tiled, logits, ws)
         assert torch.equal(logits.double(), want[:T])
     assert max(own) > 0
+
+
+# FP32 weights in every tile, whole and split, on runs of columns that do and do not fill the last step
+F32_TILES = [((16, 16), False, 100, 480, 40), ((16, 16), False, 20, 96, 8), ((32, 64), False, 1500, 480, 40),
+             ((32, 64), True, 20, 7136, 200), ((64, 64), False, 9000, 96, 40), ((64, 64), False, 2100, 480, 200),
+             ((64, 64), True, 300, 4128, 257), ((64, 64), True, 700, 2080, 100), ((64, 128), False, 4200, 480, 200),
+             ((64, 128), True, 700, 7136, 200), ((64, 128), True, 1100, 4128, 257), ((128, 128), False, 9000, 480, 200),
+             ((128, 128), True, 1100, 7136, 257), ((128, 128), True, 4200, 2080, 200)]
+
+
+def without(w, part):
+    """FP32 weights less one of their three parts of 8 bits."""
+    parts, rest = [], w.clone()
+    for _ in range(3):
+        parts.append((rest.view(torch.int32) & -65536).view(F32))
+        rest = rest - parts[-1]
+    assert not rest.any()
+    return w - parts[part]
+
+
+@pytest.mark.parametrize("tile,split,T,H,E", F32_TILES)
+def test_router_f32_weights_keep_all_parts(gpu, tile, split, T, H, E):
+    """Weights of 24 bits, one column to a row of x; then whole numbers of 20 bits, 15 columns to a row, whose sums stay
+    below 2^24.  Without any one of the parts nearly no logit is right."""
+    got_tile = B.router_tile(B.make_router(T, H, E, weight_dtype=F32))
+    print(f"router T={T} H={H} E={E} tile {got_tile}", flush=True)
+    assert got_tile[:2] == tile and (got_tile[2] > 1) == split
+    g = torch.Generator().manual_seed(T + H + E)
+    one = torch.zeros(T, H, dtype=BF16)
+    one[torch.arange(T), torch.randperm(max(T, H), generator=g)[:T] % H] = 1
+    bits24 = torch.randn(E, H, generator=g) * torch.exp2(torch.arange(H) % 60 - 30.0)
+    few = torch.zeros(T, H, dtype=BF16)
+    few.scatter_(1, torch.rand(T, H, generator=g).topk(15, dim=1).indices, 1)
+    whole20 = torch.randint(-2 ** 20 + 1, 2 ** 20, (E, H), generator=g).float()
+    for x, w in ((one, bits24), (few, whole20)):
+        want = x.double() @ w.double().t().contiguous()
+        assert torch.equal(run(x.to(gpu), w.to(gpu)).cpu().double(), want)
+        for part in range(3):
+            rows = x[:200].double() @ without(w, part).double().t().contiguous()
+            assert (rows != want[:200]).float().mean() > 0.8
