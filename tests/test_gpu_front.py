@@ -221,3 +221,84 @@ def test_weights_prepared_on_a_side_stream(gpu):
     torch.cuda.synchronize()
     assert torch.equal(got, want)
     assert all(torch.equal(tiled[k], L.tiled[k]) for k in tiled)
+
+
+def poison(layer):
+    """Every output buffer and workspace of the layer to values that no call leaves there (on the current stream)."""
+    layer.x_q.fill_(0x55), layer.x_sf.fill_(0x55), layer.ws.fill_(0x5A), layer.rws.fill_(0x5A)
+    for t in (layer.y, layer.logits, layer.w, layer.out):
+        t.fill_(float("nan"))
+    layer.ids.fill_(777)
+
+
+@pytest.mark.parametrize("explicit", [True, False])
+def test_layer_on_a_side_stream_from_nothing(gpu, explicit):
+    """The stream writes every output itself: its buffers are poisoned on it, after a pause, before each run; a call that
+    went to another stream would be overwritten, one that read too early would see the poison."""
+    L = Layer(gpu)
+    side = torch.cuda.Stream()
+    pause = torch.randn(2048, 2048, device=gpu)
+    for seed in (12, 13):
+        x, r = draw(gpu, seed)
+        ref = r.clone()
+        L.run(x, ref)
+        torch.cuda.synchronize()
+        want, mine = state(L, ref), r.clone()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                pause = (pause @ pause).clamp_(-1, 1)
+            poison(L)
+            if not explicit:
+                L.run(x, mine)
+        if explicit:
+            L.run(x, mine, stream=side)
+        side.synchronize()
+        assert same(state(L, mine), want)
+
+
+def test_two_layers_at_once_from_nothing(gpu):
+    layers, data = [Layer(gpu), Layer(gpu, BF16)], [draw(gpu, 14), draw(gpu, 15)]
+    want = []
+    for L, (x, r) in zip(layers, data):
+        ref = r.clone()
+        L.run(x, ref)
+        torch.cuda.synchronize()
+        want.append(state(L, ref))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        rs = [r.clone() for _, r in data]
+        for L in layers:
+            poison(L)
+        torch.cuda.synchronize()
+        for L, (x, _), r, s in zip(layers, data, rs, streams):
+            B.norm_quant(L.norm, x, L.norm_w, L.x_q, L.x_sf, L.y, r, r, stream=s)
+            B.router_logits(L.router, L.y, L.router_t, L.logits, L.rws, stream=s)
+            B.gate(L.gate, L.logits, L.ids, L.w, bias=L.bias, stream=s)
+        torch.cuda.synchronize()
+        for L, r, w in zip(layers, rs, want):
+            assert same(state(L, r)[:7], w[:7])
+
+
+def test_bound_calls_from_nothing(gpu):
+    """Bound calls write every output, each time they are called, on the stream that they are given."""
+    L = Layer(gpu)
+    x, r = draw(gpu, 16)
+    mine = r.clone()
+    calls = [B.norm_quant(L.norm, x, L.norm_w, L.x_q, L.x_sf, L.y, mine, mine, bind=True),
+             B.router_logits(L.router, L.y, L.router_t, L.logits, L.rws, bind=True),
+             B.gate(L.gate, L.logits, L.ids, L.w, bias=L.bias, bind=True)]
+    side = torch.cuda.Stream()
+    for seed, stream in ((17, None), (18, side), (17, side)):
+        nx, nr = draw(gpu, seed)
+        ref = nr.clone()
+        L.run(nx, ref)
+        torch.cuda.synchronize()
+        want = state(L, ref)
+        x.copy_(nx), mine.copy_(nr)
+        poison(L)
+        torch.cuda.synchronize()
+        for c in calls:
+            c(stream)
+        torch.cuda.synchronize()
+        assert same(state(L, mine)[:7], want[:7])
