@@ -532,6 +532,11 @@ typedef struct moe_gate_shape {
 MOE_API int moe_gate(const moe_gate_shape* shape, const void* logits, const float* bias,
                 int64_t* topk_idx, float* topk_w, void* stream);
 
+/* How moe_gate takes a shape whose logits and bias are 16-byte aligned: the
+ * lanes that share a row, the experts that a lane holds (0: every row is
+ * selected in 64 bits) and the keys that it keeps sorted.  For inspection. */
+MOE_API int moe_gate_lanes(const moe_gate_shape* shape, int32_t* lanes, int32_t* values, int32_t* keys);
+
 /* MOE_OK if `device` is a gfx950 GPU, MOE_ERR_ARCH if not, MOE_ERR_HIP if
  * the runtime cannot be queried. */
 MOE_API int moe_device_supported(int device);

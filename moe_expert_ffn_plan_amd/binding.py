@@ -73,6 +73,7 @@ EXPORTS = ["moe_capacity_rows", "moe_suggest_block_m", "moe_gemm_launches", "moe
            "moe_expert_ffn", "moe_prepare_weights", "moe_forward_noalloc",
            "moe_norm_quant", "moe_router_weight_bytes", "moe_router_prepare", "moe_router_workspace_bytes",
            "moe_router_max_workspace_bytes", "moe_router_tile", "moe_router_logits", "moe_gate",
+           "moe_gate_lanes",
            "moe_forward_view_get", "moe_device_supported", "moe_status_str"]
 
 
@@ -108,6 +109,7 @@ def lib() -> ctypes.CDLL:
         L.moe_router_max_workspace_bytes.argtypes = [R, P(SZ)]
         L.moe_router_tile.argtypes = [R, P(ctypes.c_int32), P(ctypes.c_int32), P(ctypes.c_int32)]
         L.moe_router_logits.argtypes = [R, VP, VP, VP, VP, SZ, VP]
+        L.moe_gate_lanes.argtypes = [G, P(ctypes.c_int32), P(ctypes.c_int32), P(ctypes.c_int32)]
         L.moe_gate.argtypes = [G, VP, VP, VP, VP, VP]
         L.moe_device_supported.argtypes = [ctypes.c_int]
         L.moe_status_str.argtypes = [ctypes.c_int]
@@ -524,6 +526,13 @@ def router_logits(shape: RouterShape, x, w_tiled, logits, ws=None, stream=None, 
             _ptr(logits, torch.float32, "logits", dev, T * E),
             _ptr(ws, torch.uint8, "ws", dev), 0 if ws is None else ws.numel()]
     return _call("moe_router_logits", shape, args, (x, w_tiled, logits, ws), stream, bind)
+
+
+def gate_lanes(shape: GateShape) -> tuple[int, int, int]:
+    """moe_gate_lanes: (lanes of a row, experts of a lane, keys that it keeps sorted) of moe_gate."""
+    v = [ctypes.c_int32() for _ in range(3)]
+    _check("moe_gate_lanes", lib().moe_gate_lanes(ctypes.byref(shape), *(ctypes.byref(i) for i in v)))
+    return tuple(i.value for i in v)
 
 
 def gate(shape: GateShape, logits, topk_idx, topk_w, bias=None, stream=None, bind=False):

@@ -442,6 +442,12 @@ int check_gate(const moe_gate_shape* s) {
     return MOE_OK;
 }
 
+GateArgs gate_args(const moe_gate_shape* s, const void* logits, const float* bias, int64_t* topk_idx, float* topk_w) {
+    return GateArgs{logits, bias, topk_idx, topk_w, stride_or(s->logits_stride, s->num_experts), s->num_tokens,
+                    s->num_experts, s->topk, s->num_groups, s->topk_groups, s->score, s->group_score, s->renormalize,
+                    s->scale, s->logits_type};
+}
+
 }  // namespace
 
 extern "C" {
@@ -546,10 +552,19 @@ int moe_gate(const moe_gate_shape* shape, const void* logits, const float* bias,
         !aligned(topk_w, 4))
         return MOE_ERR_ALIGN;
     if ((st = check_arch_current()) != MOE_OK) return st;
-    const GateArgs a{logits, bias, topk_idx, topk_w, stride_or(shape->logits_stride, shape->num_experts),
-                     shape->num_tokens, shape->num_experts, shape->topk, shape->num_groups, shape->topk_groups,
-                     shape->score, shape->group_score, shape->renormalize, shape->scale, shape->logits_type};
+    const GateArgs a = gate_args(shape, logits, bias, topk_idx, topk_w);
     return launch_gate(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_gate_lanes(const moe_gate_shape* shape, int32_t* lanes, int32_t* values, int32_t* keys) {
+    if (!lanes || !values || !keys) return MOE_ERR_NULL;
+    const int st = check_gate(shape);
+    if (st != MOE_OK) return st;
+    const GateChoice c = choose_gate(gate_args(shape, nullptr, nullptr, nullptr, nullptr));
+    *lanes = c.lanes;
+    *values = c.values;
+    *keys = c.list;
+    return MOE_OK;
 }
 
 }  // extern "C"

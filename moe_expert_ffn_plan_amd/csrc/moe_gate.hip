@@ -688,33 +688,44 @@ hipError_t launch(const GateFast& f, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_gate(const GateArgs& a, hipStream_t stream) {
-    if (a.k > 16) return launch_exact(a, stream);
+GateChoice choose_gate(const GateArgs& a) {
+    GateChoice c{};
+    c.lanes = 64;
+    if (a.k > 16) return c;
     int padded = 1;  // groups to a power of two
     while (padded < a.groups) padded *= 2;
     const int n = a.E / a.groups;
     // 16 lanes a row while a lane then holds at most 32 experts, else 64
     auto lanes_hold = [&](int L) { return padded > L ? 1 << 20 : (n + L / padded - 1) / (L / padded); };
-    const int L = lanes_hold(16) <= 32 ? 16 : 64, lpg = L / padded;
+    if (lanes_hold(16) <= 32) c.lanes = 16;
+    c.lpg = c.lanes / padded;
     const int64_t size = a.logits_type == MOE_F32 ? 4 : 2;
-    const bool vec = n % 4 == 0 && a.stride % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % (4 * size) == 0 &&
-                     reinterpret_cast<uintptr_t>(a.bias) % 16 == 0 && (n / 4 + lpg - 1) / lpg * 4 <= 32;
-    const int hold = vec ? (n / 4 + lpg - 1) / lpg * 4 : lanes_hold(L);
-    int slots = 4;  // values per lane of the kernel below
-    while (slots < hold) slots += slots == 16 && L == 16 && a.k <= 8 ? 8 : slots == 24 ? 8 : slots;
-    if (L == 64 && slots < 16) slots = 16;
-    int index_bits = 8;  // at least: FP32 counts the keys' steps, 2^(32 - index_bits) of them, one by one to 2^24
-    while ((1 << index_bits) < (padded - 1) * n + lpg * slots) ++index_bits;
-    const GateFast f{a, n, __builtin_ctz(lpg), index_bits, vec};
-    if (L == 16) {
-        if (slots == 4) return launch<16, 4, 4>(f, stream);
-        if (slots == 8) return launch<16, 8, 8>(f, stream);
-        if (a.k > 8) return slots == 16 ? launch<16, 16, 16>(f, stream) : launch<16, 32, 16>(f, stream);
-        if (slots == 16) return launch<16, 16, 8>(f, stream);
-        return slots == 24 ? launch<16, 24, 8>(f, stream) : launch<16, 32, 8>(f, stream);
+    c.vec = n % 4 == 0 && a.stride % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % (4 * size) == 0 &&
+            reinterpret_cast<uintptr_t>(a.bias) % 16 == 0 && (n / 4 + c.lpg - 1) / c.lpg * 4 <= 32;
+    const int hold = c.vec ? (n / 4 + c.lpg - 1) / c.lpg * 4 : lanes_hold(c.lanes);
+    c.values = 4;
+    while (c.values < hold)
+        c.values += c.values == 16 && c.lanes == 16 && a.k <= 8 ? 8 : c.values == 24 ? 8 : c.values;
+    if (c.lanes == 64 && c.values < 16) c.values = 16;
+    c.list = std::min(c.values, a.k > 8 ? 16 : 8);
+    c.index_bits = 8;  // at least: FP32 counts the keys' steps, 2^(32 - index_bits) of them, one by one to 2^24
+    while ((1 << c.index_bits) < (padded - 1) * n + c.lpg * c.values) ++c.index_bits;
+    return c;
+}
+
+hipError_t launch_gate(const GateArgs& a, hipStream_t stream) {
+    const GateChoice c = choose_gate(a);
+    if (c.values == 0) return launch_exact(a, stream);
+    const GateFast f{a, a.E / a.groups, __builtin_ctz(c.lpg), c.index_bits, c.vec};
+    if (c.lanes == 16) {
+        if (c.values == 4) return launch<16, 4, 4>(f, stream);
+        if (c.values == 8) return launch<16, 8, 8>(f, stream);
+        if (c.list == 16) return c.values == 16 ? launch<16, 16, 16>(f, stream) : launch<16, 32, 16>(f, stream);
+        if (c.values == 16) return launch<16, 16, 8>(f, stream);
+        return c.values == 24 ? launch<16, 24, 8>(f, stream) : launch<16, 32, 8>(f, stream);
     }
-    if (a.k > 8) return slots == 16 ? launch<64, 16, 16>(f, stream) : launch<64, 32, 16>(f, stream);
-    return slots == 16 ? launch<64, 16, 8>(f, stream) : launch<64, 32, 8>(f, stream);
+    if (c.list == 16) return c.values == 16 ? launch<64, 16, 16>(f, stream) : launch<64, 32, 16>(f, stream);
+    return c.values == 16 ? launch<64, 16, 8>(f, stream) : launch<64, 32, 8>(f, stream);
 }
 
 }  // namespace moe

@@ -250,6 +250,12 @@ struct GateArgs {
     float scale;
     int logits_type;
 };
+struct GateChoice {
+    int lanes, values, list;  // lanes of a row, experts of a lane (0: every row in 64 bits), keys that a lane keeps sorted
+    int lpg, index_bits;      // lanes of a group; bits of a key that name the expert
+    bool vec;                 // experts of a lane in runs of 4
+};
+GateChoice choose_gate(const GateArgs& a);
 hipError_t launch_gate(const GateArgs& a, hipStream_t stream);
 
 }  // namespace moe

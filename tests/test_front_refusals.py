@@ -283,3 +283,20 @@ def test_prepared_weights_belong_to_the_stream(monkeypatch):
     B.router_prepare(B.make_router(1, 32, 16), w, stream=Stream())
     B.prepare_weights(B.make_shape(1, 256, 256, 1, 1, 16), 1, u8(512 * 128), u8(512 * 8), stream=Stream())
     assert made == [True, True, True]
+
+
+def test_gate_kernels_of_all_shapes():
+    """Every kernel that any allowed shape takes is one that the GPU tests run by name."""
+    from test_gpu_gate import KERNELS
+    taken = set()
+    for E in range(1, 1025):
+        for groups in (d for d in range(1, 65) if E % d == 0):
+            for k in (1, 8, 9, 16, 17, 64):
+                if k <= E:
+                    taken.add(B.gate_lanes(B.make_gate(1, E, k, num_groups=groups, topk_groups=groups)))
+    assert taken == set(KERNELS)
+    for kernel, shapes in KERNELS.items():
+        for E, groups, kept, k in shapes:
+            assert B.gate_lanes(B.make_gate(1, E, k, num_groups=groups, topk_groups=kept)) == kernel
+    with pytest.raises(B.MoeError):
+        B.gate_lanes(B.make_gate(1, 8, 9))

@@ -311,3 +311,35 @@ def test_gate_rows_without_candidates(gpu, E, groups, kept, score, dtype):
             check(l, k, bias=bias, score=score, num_groups=groups, topk_groups=kept, group_score=group_score)
     ids, w = run(l, k, half, score=score, num_groups=groups, topk_groups=kept)
     assert (ids[[0, 19, 20]] == -1).all() and (w[[0, 19, 20]] == 0).all()
+
+
+# (lanes of a row, experts of a lane, keys it keeps) of every kernel, and shapes that it takes: E, groups, kept, k; the
+# second of each in lanes that hold no runs of 4
+KERNELS = {(16, 4, 4): [(64, 1, 1, 8), (45, 3, 2, 16)], (16, 8, 8): [(128, 4, 2, 8), (63, 9, 5, 16)],
+           (16, 16, 8): [(256, 8, 3, 8), (135, 9, 4, 5)], (16, 16, 16): [(256, 8, 3, 16), (135, 9, 4, 9)],
+           (16, 24, 8): [(384, 8, 3, 8), (331, 1, 1, 7)], (16, 32, 8): [(512, 16, 5, 8), (465, 15, 4, 8)],
+           (16, 32, 16): [(512, 16, 5, 12), (465, 15, 4, 16)], (64, 16, 8): [(1024, 1, 1, 8), (1001, 1, 1, 3)],
+           (64, 16, 16): [(1024, 16, 4, 16), (806, 13, 3, 9)],
+           (64, 32, 8): [(960, 5, 3, 8), (1023, 3, 2, 8), (1001, 7, 3, 8), (1023, 33, 9, 8)],
+           (64, 32, 16): [(960, 5, 3, 16), (1020, 6, 4, 12), (1023, 3, 2, 12), (561, 17, 5, 16)],
+           (64, 0, 0): [(128, 4, 2, 17), (1023, 3, 2, 64)]}
+
+
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+@pytest.mark.parametrize("kernel,shape", [(k, s) for k, v in KERNELS.items() for s in v])
+def test_gate_every_kernel(gpu, kernel, shape, group_score):
+    """Random rows, rows of near ties, masked rows, in both types, with and without a bias."""
+    E, groups, kept, k = shape
+    print(f"gate {kernel} E={E} groups={groups} kept={kept} k={k} {group_score}", flush=True)
+    assert B.gate_lanes(B.make_gate(1, E, k, num_groups=groups, topk_groups=kept)) == kernel
+    g = torch.Generator().manual_seed(E + k)
+    l = torch.randn(36, E, generator=g)
+    near = torch.randn(E, generator=g) * 0.2
+    l[12:18] = near + torch.randint(-2, 3, (6, E), generator=g) * 2.0 ** -24
+    l[18:24] = torch.randint(-3, 4, (6, E), generator=g).float()
+    l[24:34][torch.rand(10, E, generator=g) < torch.linspace(0.1, 0.99, 10)[:, None]] = -INF
+    l[34] = -INF
+    l[35, E - 1] = 9.0
+    bias = (1.0 - torch.sigmoid(near)).to(gpu)
+    for dtype, b, score in itertools.product([F32, BF16], [None, bias, balance(E, 74, gpu)], ["softmax", "sigmoid"]):
+        check(l.to(dtype).to(gpu), k, bias=b, score=score, num_groups=groups, topk_groups=kept, group_score=group_score)
