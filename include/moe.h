@@ -496,6 +496,9 @@ MOE_API int moe_router_logits(const moe_router_shape* shape, const uint16_t* x, 
  *               0 where that sum is 0), times scale
  * Ties, of experts and of groups, go to the lowest index.  Scores, sums and
  * comparisons hold in 64 bits wherever they decide an order.
+ * Weights are scores in 64 bits, rounded once; but softmax weights that are
+ * not renormalised are divided by a 64-bit sum of exponentials formed in 32
+ * bits, which is within 10 * 2^-24 of the row's.
  * An expert whose logit or c is -infinity is never chosen; a row with fewer
  * than topk candidates ends in entries of id -1 and weight 0, which
  * moe_plan drops (a padding row is a row of -infinities).  NaN (of a

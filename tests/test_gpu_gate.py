@@ -1,9 +1,10 @@
 """GPU parity of moe_gate: ids equal to the float64 oracle's, weights within their roundings.
 
 Weights come from scores in 64 bits and are rounded once: 2^-24, and as much again for the exponentials'
-and the sum's own 64-bit error.  Softmax weights that are not renormalised are divided by a sum over the
-whole row that may be held in 32 bits: relative error at most 31 * 2^-24 < 2^-19 (the argument's rounding,
-weighted, at most ln(1024) < 7 times 2^-24; the exponential 2 * 2^-24; at most 22 additions).
+and the sum's own 64-bit error.  Softmax weights that are not renormalised are divided by a 64-bit sum of the
+whole row's exponentials in 32 bits: 10 * 2^-24 relative (the argument's rounding, weighted, at most ln(1024) < 7
+times 2^-24, the exponential 3 * 2^-24), with the weight's own rounding below 2^-20 (test_gate_whole_row_sums);
+the tests of other things allow 2^-19.
 """
 import itertools
 
@@ -343,3 +344,19 @@ def test_gate_every_kernel(gpu, kernel, shape, group_score):
     bias = (1.0 - torch.sigmoid(near)).to(gpu)
     for dtype, b, score in itertools.product([F32, BF16], [None, bias, balance(E, 74, gpu)], ["softmax", "sigmoid"]):
         check(l.to(dtype).to(gpu), k, bias=b, score=score, num_groups=groups, topk_groups=kept, group_score=group_score)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("E,k,groups,kept", [(64, 8, 1, 1), (256, 8, 8, 4), (384, 6, 1, 1), (1024, 16, 1, 1), (96, 24, 1, 1)])
+def test_gate_whole_row_sums(gpu, E, k, groups, kept, dtype):
+    """Softmax weights over the whole row's sum: 10 units of 2^-24 of the sum and 1 of the weight, products of them
+    and 64-bit roundings below a tenth of a unit."""
+    for i, scale in enumerate((0.01, 1.0, 4.0, 30.0)):
+        l = normal(200, E, 80 + i, gpu, dtype, scale)
+        l[100:][torch.rand(100, E, generator=torch.Generator().manual_seed(i)).to(gpu) < 0.3] = -INF
+        for bias in (None, balance(E, 90, gpu)):
+            kw = dict(num_groups=groups, topk_groups=kept, renormalize=False)
+            ids, w = run(l, k, bias, **kw)
+            rids, rw = gate_ref(l.double().cpu().numpy(), k, bias=None if bias is None else bias.cpu().numpy(), **kw)
+            assert np.array_equal(ids, rids)
+            assert (np.abs(w - rw) <= 11.1 * 2.0 ** -24 * rw + 2.0 ** -150).all()
