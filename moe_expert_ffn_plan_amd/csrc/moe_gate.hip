@@ -9,14 +9,18 @@
 // themselves (FP64), and checks that the next key is too small to belong among the first k, its shortening
 // and the error of FP32 scores allowed for.  Marks of groups too close for FP32 are formed again in FP64.  A row that
 // fails (three candidates within the error, marks of softmax scores within theirs, a NaN, a spread that the keys
-// cannot hold) is done again by exact_row: of 100,000 random rows of 256 experts none without a bias and none of
-// sigmoid scores, 3 to 4 of softmax scores with a bias.  A row done again adds 4 us to a call of 128.
+// cannot hold) is done again by exact_row, which adds 5.5 us to a call of 128.
+// How many do depends on how far the k + 1st candidate is from the rest.  Of 262,144 rows of 256 experts, top 8, logits
+// N(0, 1): none without a bias, none of sigmoid scores, 10 of softmax scores under a bias of 201 steps of 0.001.  A call
+// of 65536 rows (18 to 31 us) takes up to 190 where nearly all rows fail, as rows do of equal FP32 logits without a bias
+// (147), of softmax scores with one logit of 16 and a bias of few distinct values (162; of 201 values 31, none fails),
+// and of sigmoid scores of N(0, 10), saturated, with a zero bias (147, 190 in groups).
 //
 // Bound by instructions, not by memory: 16 lanes share a row (four rows a wave; 64 lanes for long rows), a
 // lane keeps its D largest keys sorted, and a round of the selection is four DPP maxima and D moves for all
 // rows of the wave.  Packing the index into the key makes a comparison of two candidates one instruction.
-// 65536 x 384, top 6, no bias: 23.5 us FP32 (106 MB, 4.5 TB/s), 20.5 BF16 (56 MB); with a bias 29.  16384 x 256,
-// top 8: 7.4 without a bias, 8.8 with one, 11 with 8 groups marked by pairs; 128 such rows 5.0, where a kernel
+// 65536 x 384, top 6, no bias: 24 us FP32 (106 MB, 4.4 TB/s), 20.5 BF16 (56 MB); with a bias 28 to 32.  16384 x 256,
+// top 8: 7.7 without a bias, 9 with one, 10.7 with 8 groups marked by pairs; 128 such rows 5.1, where a kernel
 // that stores one word takes 3.7 of launch.
 #include "moe_internal.h"
 
@@ -384,7 +388,8 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
     // Softmax in units of 2^-24: an argument is d = top - l, off by 1 unit times d (by 3 with exp32's product),
     // and the mean of d under the softmax's own weights is at most ln 1024 < 7.  A sum that divides scores is off
     // by 7 + 3 (exp_whole) and added in FP64, one that only marks groups by 21 + 1 + 22 (additions).  An FP32 score
-    // is e^-d <= 1 times inv, the largest score: off by at most 53 (d e^-d < 0.37) times inv.
+    // is e^-d <= 1 times inv, the largest score: off by at most 53 (d e^-d < 0.37) times inv.  (Exponentials in FP64
+    // would be V a lane, where the picks take one; weights of a sum off by 10 are within 11 of the formula's.)
     float sum = 0.0f, inv = 0.0f;
     double sum64 = 0.0;
     if (soft) {
@@ -703,6 +708,9 @@ GateChoice choose_gate(const GateArgs& a) {
     c.vec = n % 4 == 0 && a.stride % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % (4 * size) == 0 &&
             reinterpret_cast<uintptr_t>(a.bias) % 16 == 0 && (n / 4 + c.lpg - 1) / c.lpg * 4 <= 32;
     const int hold = c.vec ? (n / 4 + c.lpg - 1) / c.lpg * 4 : lanes_hold(c.lanes);
+    // 4, 8, 16, 24 or 32 experts a lane; 24 for lists of 8 keys only, which divide it (65536 x 384, top 6, bias: 29.3 us,
+    // 36.2 with 32; BF16 without a bias 19.8, 25.7; 128 rows 4.5, 5.3), and
+    // for 16 lanes (at 64 it was not tried)
     c.values = 4;
     while (c.values < hold)
         c.values += c.values == 16 && c.lanes == 16 && a.k <= 8 ? 8 : c.values == 24 ? 8 : c.values;

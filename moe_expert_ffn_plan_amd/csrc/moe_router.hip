@@ -224,8 +224,8 @@ __global__ __launch_bounds__(kSmallWaves * 64) void router_small_kernel(RouterAr
 // and frees the one before it; producers wait for their own transfers ahead of it, consumers for their LDS
 // reads, and a consumer has the next step's first fragments in flight before it starts the last products
 // of its step.
-// Where it goes (16384 x 7168 x 256, 128 x 256 tiles in two splits, 61 us of the call's 70): the matrix cores
-// are busy for 54% of the CUs' 107,000 clocks; x alone streams in 35 us and the products alone, with both
+// Where it goes (16384 x 7168 x 256, 128 x 256 tiles in two splits, 62 us of the call's 70): the matrix cores
+// are busy for 48% of the CUs' 121,000 clocks; x alone streams in 35 us and the products alone, with both
 // operands in the L2, take 45.  The L1 takes loads in order at about 50 bytes a clock, so the weights wait
 // behind x from memory: a CU moves 24 KiB per 32 columns, 480 of the 512 clocks of its matrix instructions.
 // 64 x 256 tiles need no second split but move 20 KiB for half of the products and take 75 us.  Writing the
