@@ -473,6 +473,7 @@ __global__ __launch_bounds__(64 * kWaves) void gate_kernel(GateFast f) {
             m2 = m2 == -INFINITY ? m2 : soft ? exp32(m2 - top) * inv : sigmoid32(m2);
         }
         const float mark = pair && m2 > -INFINITY ? m1 + m2 : m1;
+        doubt |= (m2 > -INFINITY) & (mark == -INFINITY);  // a sum beyond FP32, that ranks with a group of no candidate
         int rank = 0;
         for (int g0 = 0; g0 < a.groups; g0 += 4) {
 #pragma unroll

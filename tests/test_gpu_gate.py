@@ -360,3 +360,21 @@ def test_gate_whole_row_sums(gpu, E, k, groups, kept, dtype):
             rids, rw = gate_ref(l.double().cpu().numpy(), k, bias=None if bias is None else bias.cpu().numpy(), **kw)
             assert np.array_equal(ids, rids)
             assert (np.abs(w - rw) <= 11.1 * 2.0 ** -24 * rw + 2.0 ** -150).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,kept,k", [(28, 4, 3, 1), (64, 8, 3, 6), (48, 8, 1, 2), (1008, 63, 7, 10), (256, 8, 7, 16)])
+def test_gate_group_marks_beyond_fp32(gpu, E, groups, kept, k, score, dtype):
+    """Groups whose two best sum below FP32's lowest value, next to groups without candidates, which come first."""
+    print(f"gate E={E} groups={groups} kept={kept} {score} {dtype}", flush=True)
+    n = E // groups
+    l = normal(40, E, 75, gpu, dtype)
+    for t in range(40):                                # from no empty group to all but one
+        l[t, :n * (t % groups)] = -INF
+    g = torch.Generator().manual_seed(76)
+    for low, high in ((-3.4e38, -3.0e38), (-3.0e38, -3.0e38), (-1.8e38, -1.6e38)):
+        bias = (torch.rand(E, generator=g) * (high - low) + low).to(gpu)
+        check(l, k, bias=bias, score=score, num_groups=groups, topk_groups=kept, group_score="top2")
+        bias[n // 2::n + 1] = 0.25                     # a few groups with one usual expert
+        check(l, k, bias=bias, score=score, num_groups=groups, topk_groups=kept, group_score="top2")
