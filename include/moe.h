@@ -400,11 +400,12 @@ enum moe_dtype {
  *            of the block is 0), x_sf = s + 127, x_q = E4M3(v / 2^s).
  * The norm and both outputs come from h before its rounding to
  * residual_type.  The mean is that of x + residual in 64 bits, v is computed
- * in 32 (an h below 2^-126 of its row's rms may lose low bits, or all of
- * them), and the scale is the one of the formula in 64 bits also where an h
- * or max|v| rounds across 448 * 2^s in 32.  A NaN in a row makes the row's v
- * NaN (E4M3 code 0x7F or 0xFF); an infinite h becomes NaN and the others of
- * its row 0; a row of zeros with eps = 0 is NaN.
+ * in 32, and the scale is the one of the formula in 64 bits also where an h
+ * or max|v| rounds across 448 * 2^s in 32.  (An h below
+ * 2^-126 * sqrt(mean(h^2) + eps) may lose low bits, or all of them, before the
+ * weight is multiplied in.)  A NaN in a row makes the row's v NaN (E4M3 code
+ * 0x7F or 0xFF); an infinite h becomes NaN and the others of its row 0; a row
+ * of zeros with eps = 0 is NaN.
  * Limits (else MOE_ERR_SHAPE, or MOE_ERR_ALIGN for the divisibility rules):
  *   num_tokens 0 .. 2^28 - 1; hidden 32 .. 2^20, a multiple of 32; eps finite,
  *   >= 0;
