@@ -377,7 +377,8 @@ MOE_API int moe_forward_noalloc(const moe_shape* shape,
  *   moe_router_logits  logits = y W^T
  *   moe_gate           logits -> topk_idx, topk_w (moe_plan's and
  *                      moe_forward's inputs)
- * The library is a forward with FP4 experts, so none of them has a backward.
+ * The experts' FP4 weights are not trained; the gate's gradient, for training
+ * the router in front of them, is moe_gate_grad below.
  * The conventions at the top of this file hold (validation order: NULL
  * shape, shape limits and divisibility, NULL pointers, alignment, workspace
  * size, architecture), except that rows of the inputs may be strided: a
@@ -540,6 +541,176 @@ MOE_API int moe_gate(const moe_gate_shape* shape, const void* logits, const floa
  * lanes that share a row, the experts that a lane holds (0: every row is
  * selected in 64 bits) and the keys that it keeps sorted.  For inspection. */
 MOE_API int moe_gate_lanes(const moe_gate_shape* shape, int32_t* lanes, int32_t* values, int32_t* keys);
+
+/* ---- microscaled quantisation, and the dense product in 4 bits -----------------
+ * What the layer's other matrices need beside the experts: the same formats
+ * (E2M1 weights, E2M1 or E4M3 activations, a UE8M0 scale per 32 columns) for
+ * a plain product y = x W^T.
+ *   moe_mx_quant           x -> codes and scales, and the values they stand for
+ *   moe_mx_linear_prepare  one-time re-layout of W
+ *   moe_mx_linear          y = x W^T
+ * moe_mx_quant's E2M1 output of a weight matrix is also what
+ * moe_prepare_weights reads, and its E4M3 output is moe_forward's x and x_sf.
+ * The conventions of the section above hold. */
+enum moe_mx_format {
+    MOE_E2M1 = 0,   /* 4 bits: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives */
+    MOE_E4M3 = 1    /* 8 bits, up to 448 */
+};
+
+/* Quantisation of each 32 neighbouring columns of a row:
+ *   2^s    the smallest power of two with max|x| / 2^s <= 6 (E2M1) or 448
+ *          (E4M3), s in [-127, 127]; -127 where all of the block is 0
+ *   x_sf   = s + 127
+ *   x_q    = x / 2^s rounded to the format's nearest value, ties to the even
+ *          code; two E2M1 codes to a byte, the even column low
+ *   x_dq   = x_q * 2^s rounded to BF16
+ * A block that holds a NaN or an infinity has x_sf 255, which stands for NaN,
+ * codes 0 and x_dq NaN throughout.  Where the rounding of x_dq passes BF16's
+ * range (|x| of almost 2^128) it is infinite.
+ * Limits (else MOE_ERR_SHAPE, or MOE_ERR_ALIGN for the divisibility rules):
+ *   num_rows 0 .. 2^28 - 1; num_cols 32 .. 2^20, a multiple of 32; x_stride >=
+ *   num_cols and a multiple of 8. */
+typedef struct moe_mx_quant_shape {
+    int64_t x_stride;
+    int32_t num_rows;
+    int32_t num_cols;
+    int32_t x_type;         /* MOE_BF16 or MOE_F32 */
+    int32_t format;         /* moe_mx_format */
+} moe_mx_quant_shape;
+/*   x     [R, C] x_type, rows x_stride apart
+ *   x_q   uint8 [R, C / 2] (E2M1) or [R, C] (E4M3), and
+ *   x_sf  uint8 [R, C / 32], or both NULL
+ *   x_dq  BF16 [R, C], or NULL
+ * At least one of x_q and x_dq must be given; x, x_q and x_dq 16-byte aligned;
+ * outputs must not overlap x. */
+MOE_API int moe_mx_quant(const moe_mx_quant_shape* shape, const void* x, uint8_t* x_q, uint8_t* x_sf,
+                uint16_t* x_dq, void* stream);
+
+/* Dense product: y[t, n] = sum over k of x[t, k] * w[n, k], x and w the values
+ * that their codes and scales stand for, summed in FP32 by the scaled matrix
+ * instructions and rounded to BF16.  (With E2M1 activations their sums of 64
+ * products are exact to FP32; with E4M3 they may be off by 2^-13 of the sum
+ * of magnitudes where scales are far apart.)  A scale of 255 or an E4M3 NaN
+ * makes y NaN wherever it is part of the sum.
+ * Limits: num_tokens 0 .. 2^28 - 1; in_features 32 .. 2^20, a multiple of 32;
+ * out_features 1 .. 2^20; y_stride >= out_features. */
+typedef struct moe_mx_linear_shape {
+    int64_t y_stride;
+    int32_t num_tokens;
+    int32_t in_features;
+    int32_t out_features;
+    int32_t x_format;       /* moe_mx_format */
+} moe_mx_linear_shape;
+
+/* One-time re-layout of the weights (num_tokens, x_format and y_stride are
+ * ignored): w uint8 [N, K / 2] E2M1, w_sf uint8 [N, K / 32], 16-byte aligned
+ * (w_sf any), into w_tiled of moe_mx_linear_weight_bytes, 16-byte aligned:
+ *   codes   [B][KT][128 slots of 16 B], B = 2 * ceil(N / 64), KT =
+ *           ceil(K / 128); slot p of (b, kt) holds the 32 columns from
+ *           128 kt + 32 ((p & 3) ^ ((c >> 1) & 3)) of weight row
+ *           64 (b / 2) + 2 c + b % 2, c = p >> 2;
+ *   scales  behind them, [B][KT][32 c][4 B];
+ * zeros where there is no such row or column. */
+MOE_API int moe_mx_linear_weight_bytes(const moe_mx_linear_shape* shape, size_t* bytes);
+MOE_API int moe_mx_linear_prepare(const moe_mx_linear_shape* shape, const uint8_t* w, const uint8_t* w_sf,
+                uint8_t* w_tiled, void* stream);
+
+/* Bytes of moe_mx_linear's workspace for this shape; may be 0, and then ws may
+ * be NULL.  More tokens may need LESS; moe_mx_linear_max_workspace_bytes is
+ * enough for every num_tokens from 0 to shape->num_tokens. */
+MOE_API int moe_mx_linear_workspace_bytes(const moe_mx_linear_shape* shape, size_t* bytes);
+MOE_API int moe_mx_linear_max_workspace_bytes(const moe_mx_linear_shape* shape, size_t* bytes);
+
+/* How moe_mx_linear takes a shape: the tokens and outputs of a tile, and the
+ * parts that a tile's columns are split into.  For inspection. */
+MOE_API int moe_mx_linear_tile(const moe_mx_linear_shape* shape, int32_t* tokens, int32_t* outputs, int32_t* splits);
+
+/*   x        uint8 [T, K / 2] (E2M1) or [T, K] (E4M3), 16-byte aligned
+ *   x_sf     uint8 [T, K / 32], 4-byte aligned
+ *   w_tiled  from moe_mx_linear_prepare for the same in_features and
+ *            out_features
+ *   y        BF16 [T, N], rows y_stride apart, 4-byte aligned
+ *   ws       any initial contents, 256-byte aligned */
+MOE_API int moe_mx_linear(const moe_mx_linear_shape* shape, const uint8_t* x, const uint8_t* x_sf,
+                const uint8_t* w_tiled, uint16_t* y, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- balance of the experts' load, and the gate's gradient ---------------------
+ * For training the router in front of experts that stay as they are: what
+ * moe_gate chose is counted and weighed against its scores, and the gradient
+ * of that loss and of the gate's weights goes back to the logits.
+ * Rows belong to sequences: with seq_offsets (int64 [S + 1], not falling)
+ * sequence s is the rows seq_offsets[s] .. seq_offsets[s + 1] - 1; offsets
+ * below 0 count as 0, those above T as T, and where one lies below the one
+ * before it the sequence is empty.  Rows in no sequence take no part; without
+ * seq_offsets S is 1 and all rows are its.  Of sequence s:
+ *   p[t, e]      row t's scores over their sum: softmax(l), or sigmoid(l) /
+ *                sum of sigmoid(l); 0 for a row whose logits are all
+ *                -infinity (padding)
+ *   rows[s]      rows that are not padding
+ *   counts[s, e] entries of topk_idx that are e; ids outside 0 .. E - 1 are
+ *                not counted
+ *   share[s, e]  sum over t of p[t, e], over rows[s]
+ *   loss[s]      E * sum over e of counts[s, e] * share[s, e], over the sum of
+ *                counts[s, e]: 1 where the load is even
+ *   z[s]         sum over t of (log sum over e of exp(l[t, e]))^2, over
+ *                rows[s]; softmax alone
+ * each 0 where its divisor is 0.  The gradient takes counts and rows as
+ * constants; counts may be summed over ranks first.  Sums hold in FP32 in an
+ * order that depends on the shape alone: the same inputs give the same bits.
+ * A NaN or +infinity among a row's logits makes the p of that row NaN (with
+ * sigmoid scores an infinity stands for 1).
+ * Limits: num_tokens 0 .. 2^28 - 1, T * topk < 2^30; num_experts 1 .. 1024;
+ * topk 1 .. min(64, num_experts); num_seqs 1 .. 2^20, 1 without seq_offsets,
+ * S * E < 2^30; scale finite; logits_stride >= num_experts. */
+typedef struct moe_balance_shape {
+    int64_t logits_stride;
+    int32_t num_tokens;
+    int32_t num_experts;    /* all ranks' experts */
+    int32_t topk;
+    int32_t num_seqs;       /* S */
+    int32_t score;          /* moe_score */
+    int32_t renormalize;    /* of moe_gate; moe_gate_grad alone */
+    float scale;            /* of moe_gate; moe_gate_grad alone */
+    int32_t logits_type;    /* MOE_BF16 or MOE_F32 */
+} moe_balance_shape;
+
+MOE_API int moe_balance_workspace_bytes(const moe_balance_shape* shape, size_t* bytes);
+
+/*   logits       [T, E] logits_type, aligned to its element; NULL where only
+ *                counts is asked for
+ *   topk_idx     int64 [T, k]
+ *   seq_offsets  int64 [S + 1], or NULL
+ *   counts       int32 [S, E], or NULL
+ *   rows         int32 [S], or NULL
+ *   share        float [S, E], or NULL
+ *   loss         float [S], or NULL
+ *   z            float [S], or NULL; NULL with sigmoid scores (else
+ *                MOE_ERR_SHAPE)
+ *   ws           any initial contents, 256-byte aligned
+ * At least one output must be given.  With num_tokens = 0 they are all 0. */
+MOE_API int moe_balance(const moe_balance_shape* shape, const void* logits, const int64_t* topk_idx,
+                const int64_t* seq_offsets, int32_t* counts, int32_t* rows, float* share, float* loss, float* z,
+                void* ws, size_t ws_bytes, void* stream);
+
+/* d_logits = the gradient, with respect to the logits, of
+ *     sum over s of d_loss[s] * loss[s] + d_z[s] * z[s]
+ *   + sum over t, j of d_topk_w[t, j] * topk_w[t, j]
+ * with topk_w as moe_gate forms it (scores of topk_idx, over their sum where
+ * renormalize is set, times scale; an entry whose id is outside 0 .. E - 1 has
+ * weight 0; an id that occurs twice in a row counts twice).  0 where a logit
+ * is -infinity.  Rows in no sequence are left as they were.
+ *   logits, topk_idx, seq_offsets   as for moe_balance
+ *   counts, rows   int32 [S, E] and [S], from moe_balance; counts with d_loss,
+ *                  rows with d_loss or d_z
+ *   d_loss         float [S], or NULL
+ *   d_z            float [S], or NULL; NULL with sigmoid scores
+ *   d_topk_w       float [T, k], or NULL
+ *   d_logits       [T, E] logits_type, contiguous, aligned to its element; may
+ *                  be logits itself where its rows are contiguous
+ * At least one of d_loss, d_z and d_topk_w must be given. */
+MOE_API int moe_gate_grad(const moe_balance_shape* shape, const void* logits, const int64_t* topk_idx,
+                const int64_t* seq_offsets, const int32_t* counts, const int32_t* rows, const float* d_loss,
+                const float* d_z, const float* d_topk_w, void* d_logits, void* stream);
 
 /* MOE_OK if `device` is a gfx950 GPU, MOE_ERR_ARCH if not, MOE_ERR_HIP if
  * the runtime cannot be queried. */

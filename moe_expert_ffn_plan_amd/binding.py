@@ -22,6 +22,7 @@ WEIGHTS_PLAIN, WEIGHTS_TILED = 0, 1   # moe_shape.weight_layout
 DTYPES = {torch.bfloat16: 0, torch.float32: 1}   # moe_dtype
 SCORES = {"softmax": 0, "sigmoid": 1}            # moe_score
 GROUP_SCORES = {"max": 0, "top2": 1}             # moe_group_score
+FORMATS = {"e2m1": 0, "e4m3": 1}                 # moe_mx_format
 
 
 class MoeError(RuntimeError):
@@ -55,6 +56,22 @@ class GateShape(ctypes.Structure):
                [("scale", ctypes.c_float), ("logits_type", ctypes.c_int32)]
 
 
+class MxQuantShape(ctypes.Structure):
+    _fields_ = [("x_stride", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("num_rows", "num_cols", "x_type", "format")]
+
+
+class MxLinearShape(ctypes.Structure):
+    _fields_ = [("y_stride", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("num_tokens", "in_features", "out_features", "x_format")]
+
+
+class BalanceShape(ctypes.Structure):
+    _fields_ = [("logits_stride", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("num_tokens", "num_experts", "topk", "num_seqs", "score", "renormalize")] + \
+               [("scale", ctypes.c_float), ("logits_type", ctypes.c_int32)]
+
+
 class PlanView(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("scalars", "counts", "offsets", "slot", "row_token", "row_topk",
                                                "block_expert", "slack", "pull_order")] + \
@@ -74,6 +91,9 @@ EXPORTS = ["moe_capacity_rows", "moe_suggest_block_m", "moe_gemm_launches", "moe
            "moe_norm_quant", "moe_router_weight_bytes", "moe_router_prepare", "moe_router_workspace_bytes",
            "moe_router_max_workspace_bytes", "moe_router_tile", "moe_router_logits", "moe_gate",
            "moe_gate_lanes",
+           "moe_mx_quant", "moe_mx_linear_weight_bytes", "moe_mx_linear_prepare", "moe_mx_linear_workspace_bytes",
+           "moe_mx_linear_max_workspace_bytes", "moe_mx_linear_tile", "moe_mx_linear",
+           "moe_balance_workspace_bytes", "moe_balance", "moe_gate_grad",
            "moe_forward_view_get", "moe_device_supported", "moe_status_str"]
 
 
@@ -111,6 +131,17 @@ def lib() -> ctypes.CDLL:
         L.moe_router_logits.argtypes = [R, VP, VP, VP, VP, SZ, VP]
         L.moe_gate_lanes.argtypes = [G, P(ctypes.c_int32), P(ctypes.c_int32), P(ctypes.c_int32)]
         L.moe_gate.argtypes = [G, VP, VP, VP, VP, VP]
+        Q, X, A = P(MxQuantShape), P(MxLinearShape), P(BalanceShape)
+        L.moe_mx_quant.argtypes = [Q, VP, VP, VP, VP, VP]
+        L.moe_mx_linear_weight_bytes.argtypes = [X, P(SZ)]
+        L.moe_mx_linear_prepare.argtypes = [X, VP, VP, VP, VP]
+        L.moe_mx_linear_workspace_bytes.argtypes = [X, P(SZ)]
+        L.moe_mx_linear_max_workspace_bytes.argtypes = [X, P(SZ)]
+        L.moe_mx_linear_tile.argtypes = [X, P(ctypes.c_int32), P(ctypes.c_int32), P(ctypes.c_int32)]
+        L.moe_mx_linear.argtypes = [X, VP, VP, VP, VP, VP, SZ, VP]
+        L.moe_balance_workspace_bytes.argtypes = [A, P(SZ)]
+        L.moe_balance.argtypes = [A, VP, VP, VP, VP, VP, VP, VP, VP, VP, SZ, VP]
+        L.moe_gate_grad.argtypes = [A, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP]
         L.moe_device_supported.argtypes = [ctypes.c_int]
         L.moe_status_str.argtypes = [ctypes.c_int]
         L.moe_status_str.restype = ctypes.c_char_p
@@ -543,3 +574,116 @@ def gate(shape: GateShape, logits, topk_idx, topk_w, bias=None, stream=None, bin
             _ptr(bias, torch.float32, "bias", dev, E), _ptr(topk_idx, torch.int64, "topk_idx", dev, T * k),
             _ptr(topk_w, torch.float32, "topk_w", dev, T * k)]
     return _call("moe_gate", shape, args, (logits, bias, topk_idx, topk_w), stream, bind)
+
+
+# ---- microscaled quantisation, and the dense product in 4 bits
+
+def make_mx_quant(num_rows, num_cols, format="e2m1", x_dtype=torch.bfloat16, x_stride=0) -> MxQuantShape:
+    """A moe_mx_quant_shape; x_stride: elements from one row of x to the next, 0 for contiguous rows."""
+    return MxQuantShape(x_stride, num_rows, num_cols, DTYPES[x_dtype], FORMATS[format])
+
+
+def make_mx_linear(num_tokens, in_features, out_features, x_format="e2m1", y_stride=0) -> MxLinearShape:
+    """A moe_mx_linear_shape; y_stride: elements from one row of y to the next, 0 for contiguous rows."""
+    return MxLinearShape(y_stride, num_tokens, in_features, out_features, FORMATS[x_format])
+
+
+def mx_quant(shape: MxQuantShape, x, x_q=None, x_sf=None, x_dq=None, stream=None, bind=False):
+    """moe_mx_quant: codes x_q and scales x_sf of x per 32 columns, and in x_dq (BF16) the values they stand for;
+    bind=True: return the call as a Bound."""
+    R, C, u8 = shape.num_rows, shape.num_cols, torch.uint8
+    dev = _here(x, "x")
+    args = [_rows(x, _dtype(shape.x_type), "x", dev, R, C, shape.x_stride),
+            _ptr(x_q, u8, "x_q", dev, R * C // (2 if shape.format == FORMATS["e2m1"] else 1)),
+            _ptr(x_sf, u8, "x_sf", dev, R * C // 32), _bf16(x_dq, "x_dq", dev, R * C)]
+    return _call("moe_mx_quant", shape, args, (x, x_q, x_sf, x_dq), stream, bind)
+
+
+def _bytes(name, shape) -> int:
+    v = ctypes.c_size_t()
+    _check(name, getattr(lib(), name)(ctypes.byref(shape), ctypes.byref(v)))
+    return v.value
+
+
+def mx_linear_weight_bytes(shape: MxLinearShape) -> int:
+    return _bytes("moe_mx_linear_weight_bytes", shape)
+
+
+def mx_linear_workspace_bytes(shape: MxLinearShape) -> int:
+    return _bytes("moe_mx_linear_workspace_bytes", shape)
+
+
+def mx_linear_max_workspace_bytes(shape: MxLinearShape) -> int:
+    """moe_mx_linear_max_workspace_bytes: enough for every number of tokens up to shape.num_tokens."""
+    return _bytes("moe_mx_linear_max_workspace_bytes", shape)
+
+
+def mx_linear_tile(shape: MxLinearShape) -> tuple[int, int, int]:
+    """moe_mx_linear_tile: (tokens of a tile, outputs of a tile, splits of its columns) of moe_mx_linear."""
+    v = [ctypes.c_int32() for _ in range(3)]
+    _check("moe_mx_linear_tile", lib().moe_mx_linear_tile(ctypes.byref(shape), *(ctypes.byref(i) for i in v)))
+    return tuple(i.value for i in v)
+
+
+def mx_linear_prepare(shape: MxLinearShape, w, w_sf, stream=None) -> torch.Tensor:
+    """moe_mx_linear_prepare: tiled copy (a new tensor) of E2M1 weights w [out_features, in_features / 2] and their
+    scales w_sf [out_features, in_features / 32]."""
+    dev, u8, n = _here(w, "w"), torch.uint8, shape.in_features * shape.out_features
+    out = _new(mx_linear_weight_bytes(shape), dev, stream)
+    _check("moe_mx_linear_prepare",
+           lib().moe_mx_linear_prepare(ctypes.byref(shape), _ptr(w, u8, "w", dev, n // 2), _ptr(w_sf, u8, "w_sf", dev, n // 32),
+                                       _ptr(out, u8, "w_tiled"), _stream(stream)))
+    return out
+
+
+def mx_linear(shape: MxLinearShape, x, x_sf, w_tiled, y, ws=None, stream=None, bind=False):
+    """moe_mx_linear: y = x W^T in BF16, x as codes and scales, W prepared by mx_linear_prepare; bind=True: return the
+    call as a Bound.  ws may be None where mx_linear_workspace_bytes is 0."""
+    T, K, N, u8 = shape.num_tokens, shape.in_features, shape.out_features, torch.uint8
+    dev = _here(x, "x")
+    args = [_ptr(x, u8, "x", dev, T * K // (2 if shape.x_format == FORMATS["e2m1"] else 1)),
+            _ptr(x_sf, u8, "x_sf", dev, T * K // 32), _ptr(w_tiled, u8, "w_tiled", dev, mx_linear_weight_bytes(shape)),
+            _rows(y, torch.bfloat16, "y", dev, T, N, shape.y_stride), _ptr(ws, u8, "ws", dev), 0 if ws is None else ws.numel()]
+    return _call("moe_mx_linear", shape, args, (x, x_sf, w_tiled, y, ws), stream, bind)
+
+
+# ---- balance of the experts' load, and the gate's gradient
+
+def make_balance(num_tokens, num_experts, topk, num_seqs=1, score="softmax", logits_dtype=torch.float32, logits_stride=0,
+                 renormalize=True, scale=1.0) -> BalanceShape:
+    """A moe_balance_shape; score, renormalize and scale as of the gate whose choice is weighed."""
+    return BalanceShape(logits_stride, num_tokens, num_experts, topk, num_seqs, SCORES[score], int(bool(renormalize)),
+                        float(scale), DTYPES[logits_dtype])
+
+
+def balance_workspace_bytes(shape: BalanceShape) -> int:
+    return _bytes("moe_balance_workspace_bytes", shape)
+
+
+def balance(shape: BalanceShape, logits, topk_idx, ws, seq_offsets=None, counts=None, rows=None, share=None, loss=None,
+            z=None, stream=None, bind=False):
+    """moe_balance: per sequence the experts' counts and shares of the scores, the loss of their product and the mean of
+    the squared log-sum-exp; logits may be None where only counts is asked for; bind=True: return the call as a Bound."""
+    T, E, k, S = shape.num_tokens, shape.num_experts, shape.topk, shape.num_seqs
+    i32, i64, f32 = torch.int32, torch.int64, torch.float32
+    dev = _here(topk_idx, "topk_idx")
+    args = [_rows(logits, _dtype(shape.logits_type), "logits", dev, T, E, shape.logits_stride),
+            _ptr(topk_idx, i64, "topk_idx", dev, T * k), _ptr(seq_offsets, i64, "seq_offsets", dev, S + 1),
+            _ptr(counts, i32, "counts", dev, S * E), _ptr(rows, i32, "rows", dev, S), _ptr(share, f32, "share", dev, S * E),
+            _ptr(loss, f32, "loss", dev, S), _ptr(z, f32, "z", dev, S), _ptr(ws, torch.uint8, "ws", dev), ws.numel()]
+    return _call("moe_balance", shape, args, (logits, topk_idx, seq_offsets, counts, rows, share, loss, z, ws), stream, bind)
+
+
+def gate_grad(shape: BalanceShape, logits, topk_idx, d_logits, seq_offsets=None, counts=None, rows=None, d_loss=None,
+              d_z=None, d_topk_w=None, stream=None, bind=False):
+    """moe_gate_grad: the logits' gradient from those of balance's loss and z and of the gate's weights; bind=True:
+    return the call as a Bound."""
+    T, E, k, S = shape.num_tokens, shape.num_experts, shape.topk, shape.num_seqs
+    i32, i64, f32 = torch.int32, torch.int64, torch.float32
+    dev, lt = _here(logits, "logits"), _dtype(shape.logits_type)
+    args = [_rows(logits, lt, "logits", dev, T, E, shape.logits_stride), _ptr(topk_idx, i64, "topk_idx", dev, T * k),
+            _ptr(seq_offsets, i64, "seq_offsets", dev, S + 1), _ptr(counts, i32, "counts", dev, S * E),
+            _ptr(rows, i32, "rows", dev, S), _ptr(d_loss, f32, "d_loss", dev, S), _ptr(d_z, f32, "d_z", dev, S),
+            _ptr(d_topk_w, f32, "d_topk_w", dev, T * k), _rows(d_logits, lt, "d_logits", dev, T, E, 0)]
+    return _call("moe_gate_grad", shape, args, (logits, topk_idx, seq_offsets, counts, rows, d_loss, d_z, d_topk_w, d_logits),
+                 stream, bind)

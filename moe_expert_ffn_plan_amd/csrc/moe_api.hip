@@ -568,3 +568,190 @@ int moe_gate_lanes(const moe_gate_shape* shape, int32_t* lanes, int32_t* values,
 }
 
 }  // extern "C"
+
+// ---- microscaled quantisation and the dense product
+namespace {
+
+bool format_ok(int f) { return f == MOE_E2M1 || f == MOE_E4M3; }
+
+int check_mx_quant(const moe_mx_quant_shape* s) {
+    if (!s) return MOE_ERR_NULL;
+    if (!tokens_ok(s->num_rows) || !type_ok(s->x_type) || !format_ok(s->format)) return MOE_ERR_SHAPE;
+    const int st = check_hidden(s->num_cols);
+    return st != MOE_OK ? st : check_stride(s->x_stride, s->num_cols);
+}
+
+int check_mx_linear(const moe_mx_linear_shape* s) {
+    if (!s) return MOE_ERR_NULL;
+    if (!tokens_ok(s->num_tokens) || !format_ok(s->x_format)) return MOE_ERR_SHAPE;
+    if (s->out_features < 1 || s->out_features > kMaxHidden) return MOE_ERR_SHAPE;
+    if (s->y_stride != 0 && (s->y_stride < s->out_features || s->y_stride > (1ll << 40))) return MOE_ERR_SHAPE;
+    return check_hidden(s->in_features);
+}
+
+MxLinearChoice choice_of(const moe_mx_linear_shape* s) {
+    return choose_mx_linear(s->num_tokens, s->out_features, s->in_features, s->x_format);
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_mx_quant(const moe_mx_quant_shape* shape, const void* x, uint8_t* x_q, uint8_t* x_sf, uint16_t* x_dq,
+                 void* stream) {
+    int st = check_mx_quant(shape);
+    if (st != MOE_OK) return st;
+    if (shape->num_rows == 0) return MOE_OK;
+    if (!x || (!x_q && !x_dq) || (x_q == nullptr) != (x_sf == nullptr)) return MOE_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(x_q, 16) || !aligned(x_dq, 16)) return MOE_ERR_ALIGN;
+    if ((st = check_arch_current()) != MOE_OK) return st;
+    const MxQuantArgs a{x, x_q, x_sf, x_dq, shape->num_rows, shape->num_cols, stride_or(shape->x_stride, shape->num_cols)};
+    const hipError_t e = launch_mx_quant(a, shape->x_type, shape->format, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_mx_linear_weight_bytes(const moe_mx_linear_shape* shape, size_t* bytes) {
+    if (!bytes) return MOE_ERR_NULL;
+    const int st = check_mx_linear(shape);
+    if (st != MOE_OK) return st;
+    *bytes = (size_t)(mx_column_blocks(shape->out_features) * mx_steps(shape->in_features) * kMxBlockBytes);
+    return MOE_OK;
+}
+
+int moe_mx_linear_prepare(const moe_mx_linear_shape* shape, const uint8_t* w, const uint8_t* w_sf, uint8_t* w_tiled,
+                          void* stream) {
+    int st = check_mx_linear(shape);
+    if (st != MOE_OK) return st;
+    if (!w || !w_sf || !w_tiled) return MOE_ERR_NULL;
+    if (!aligned(w, 16) || !aligned(w_tiled, 16)) return MOE_ERR_ALIGN;
+    if ((st = check_arch_current()) != MOE_OK) return st;
+    const hipError_t e = launch_mx_linear_prepare(shape->out_features, shape->in_features, w, w_sf, w_tiled,
+                                                  static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_mx_linear_workspace_bytes(const moe_mx_linear_shape* shape, size_t* bytes) {
+    if (!bytes) return MOE_ERR_NULL;
+    const int st = check_mx_linear(shape);
+    if (st != MOE_OK) return st;
+    *bytes = shape->num_tokens ? choice_of(shape).workspace_bytes() : 0;
+    return MOE_OK;
+}
+
+int moe_mx_linear_max_workspace_bytes(const moe_mx_linear_shape* shape, size_t* bytes) {
+    if (!bytes) return MOE_ERR_NULL;
+    const int st = check_mx_linear(shape);
+    if (st != MOE_OK) return st;
+    *bytes = most_mx_linear_workspace(shape->num_tokens, shape->out_features, shape->in_features, shape->x_format);
+    return MOE_OK;
+}
+
+int moe_mx_linear_tile(const moe_mx_linear_shape* shape, int32_t* tokens, int32_t* outputs, int32_t* splits) {
+    if (!tokens || !outputs || !splits) return MOE_ERR_NULL;
+    const int st = check_mx_linear(shape);
+    if (st != MOE_OK) return st;
+    const MxLinearChoice c = choice_of(shape);
+    *tokens = c.tokens;
+    *outputs = c.columns;
+    *splits = c.splits;
+    return MOE_OK;
+}
+
+int moe_mx_linear(const moe_mx_linear_shape* shape, const uint8_t* x, const uint8_t* x_sf, const uint8_t* w_tiled,
+                  uint16_t* y, void* ws, size_t ws_bytes, void* stream) {
+    int st = check_mx_linear(shape);
+    if (st != MOE_OK) return st;
+    if (shape->num_tokens == 0) return MOE_OK;
+    const MxLinearChoice choice = choice_of(shape);
+    const size_t need = choice.workspace_bytes();
+    if (!x || !x_sf || !w_tiled || !y || (need > 0 && !ws)) return MOE_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(x_sf, 4) || !aligned(w_tiled, 16) || !aligned(y, 4) ||
+        (need > 0 && !aligned(ws, kAlign)))
+        return MOE_ERR_ALIGN;
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+    if ((st = check_arch_current()) != MOE_OK) return st;
+    const MxLinearArgs a{x, x_sf, w_tiled, y, static_cast<uint8_t*>(ws), stride_or(shape->y_stride, shape->out_features),
+                         shape->num_tokens, shape->out_features, shape->in_features, shape->x_format};
+    return launch_mx_linear(a, choice, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+}  // extern "C"
+
+// ---- balance of the load, and the gate's gradient
+namespace {
+
+constexpr int kMaxSeqs = 1 << 20;
+
+int check_balance(const moe_balance_shape* s) {
+    if (!s) return MOE_ERR_NULL;
+    if (!tokens_ok(s->num_tokens) || s->num_experts < 1 || s->num_experts > kMaxGateExperts) return MOE_ERR_SHAPE;
+    if (s->topk < 1 || s->topk > kMaxTopk || s->topk > s->num_experts) return MOE_ERR_SHAPE;
+    if ((int64_t)s->num_tokens * s->topk >= (1ll << 30)) return MOE_ERR_SHAPE;
+    if (s->num_seqs < 1 || s->num_seqs > kMaxSeqs || (int64_t)s->num_seqs * s->num_experts >= (1ll << 30))
+        return MOE_ERR_SHAPE;
+    if (!flag_ok(s->score) || !flag_ok(s->renormalize) || !type_ok(s->logits_type)) return MOE_ERR_SHAPE;
+    if (!(s->scale >= -FLT_MAX && s->scale <= FLT_MAX)) return MOE_ERR_SHAPE;  // also rejects NaN
+    if (s->logits_stride != 0 && (s->logits_stride < s->num_experts || s->logits_stride > (1ll << 40)))
+        return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_balance_workspace_bytes(const moe_balance_shape* shape, size_t* bytes) {
+    if (!bytes) return MOE_ERR_NULL;
+    const int st = check_balance(shape);
+    if (st != MOE_OK) return st;
+    *bytes = balance_workspace(shape->num_tokens, shape->num_experts, shape->num_seqs);
+    return MOE_OK;
+}
+
+int moe_balance(const moe_balance_shape* shape, const void* logits, const int64_t* topk_idx, const int64_t* seq_offsets,
+                int32_t* counts, int32_t* rows, float* share, float* loss, float* z, void* ws, size_t ws_bytes,
+                void* stream) {
+    int st = check_balance(shape);
+    if (st != MOE_OK) return st;
+    if (!seq_offsets && shape->num_seqs != 1) return MOE_ERR_SHAPE;
+    if (z && shape->score != MOE_SCORE_SOFTMAX) return MOE_ERR_SHAPE;
+    const bool scores = rows || share || loss || z;
+    if (!counts && !scores) return MOE_ERR_NULL;
+    if (!ws || (shape->num_tokens > 0 && (!topk_idx || (scores && !logits)))) return MOE_ERR_NULL;
+    if (!aligned(logits, shape->logits_type == MOE_F32 ? 4 : 2) || !aligned(topk_idx, 8) || !aligned(seq_offsets, 8) ||
+        !aligned(counts, 4) || !aligned(rows, 4) || !aligned(share, 4) || !aligned(loss, 4) || !aligned(z, 4) ||
+        !aligned(ws, kAlign))
+        return MOE_ERR_ALIGN;
+    if (ws_bytes < balance_workspace(shape->num_tokens, shape->num_experts, shape->num_seqs)) return MOE_ERR_WORKSPACE;
+    if ((st = check_arch_current()) != MOE_OK) return st;
+    const BalanceArgs a{scores ? logits : nullptr, topk_idx, seq_offsets, stride_or(shape->logits_stride, shape->num_experts),
+                        shape->num_tokens, shape->num_experts, shape->topk, shape->num_seqs, shape->score,
+                        shape->logits_type, counts, rows, share, loss, z};
+    return launch_balance(a, ws, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int moe_gate_grad(const moe_balance_shape* shape, const void* logits, const int64_t* topk_idx,
+                  const int64_t* seq_offsets, const int32_t* counts, const int32_t* rows, const float* d_loss,
+                  const float* d_z, const float* d_topk_w, void* d_logits, void* stream) {
+    int st = check_balance(shape);
+    if (st != MOE_OK) return st;
+    if (!seq_offsets && shape->num_seqs != 1) return MOE_ERR_SHAPE;
+    if (d_z && shape->score != MOE_SCORE_SOFTMAX) return MOE_ERR_SHAPE;
+    const int64_t stride = stride_or(shape->logits_stride, shape->num_experts);
+    if (d_logits && d_logits == logits && shape->num_tokens > 1 && stride != shape->num_experts) return MOE_ERR_SHAPE;
+    if (!d_loss && !d_z && !d_topk_w) return MOE_ERR_NULL;
+    if (shape->num_tokens == 0) return MOE_OK;
+    if (!logits || !d_logits || (d_topk_w && !topk_idx) || (d_loss && !counts) || ((d_loss || d_z) && !rows))
+        return MOE_ERR_NULL;
+    const int size = shape->logits_type == MOE_F32 ? 4 : 2;
+    if (!aligned(logits, size) || !aligned(d_logits, size) || !aligned(topk_idx, 8) || !aligned(seq_offsets, 8) ||
+        !aligned(counts, 4) || !aligned(rows, 4) || !aligned(d_loss, 4) || !aligned(d_z, 4) || !aligned(d_topk_w, 4))
+        return MOE_ERR_ALIGN;
+    if ((st = check_arch_current()) != MOE_OK) return st;
+    const GateGradArgs a{logits, topk_idx, seq_offsets, counts, rows, d_loss, d_z, d_topk_w, d_logits, stride,
+                         shape->num_tokens, shape->num_experts, shape->topk, shape->num_seqs, shape->score,
+                         shape->renormalize, shape->logits_type, shape->scale};
+    return launch_gate_grad(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+}  // extern "C"

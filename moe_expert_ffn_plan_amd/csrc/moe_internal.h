@@ -258,4 +258,71 @@ struct GateChoice {
 GateChoice choose_gate(const GateArgs& a);
 hipError_t launch_gate(const GateArgs& a, hipStream_t stream);
 
+// ---- microscaled quantisation and the dense product in 4 bits
+struct MxQuantArgs {
+    const void* x;
+    uint8_t* x_q;    // or null, with x_sf
+    uint8_t* x_sf;
+    uint16_t* x_dq;  // or null
+    int64_t rows, cols, stride;
+};
+hipError_t launch_mx_quant(const MxQuantArgs& a, int x_type, int format, hipStream_t stream);
+
+inline int mx_steps(int K) { return (K + 127) / 128; }                                // K-steps of 128 columns
+inline int64_t mx_column_blocks(int N) { return ((int64_t)N + 63) / 64 * 2; }          // blocks of 32 outputs, in pairs
+constexpr int64_t kMxBlockBytes = 32 * 64 + 32 * 4;                                    // codes and scales of a block's K-step
+hipError_t launch_mx_linear_prepare(int N, int K, const uint8_t* w, const uint8_t* w_sf, uint8_t* w_tiled,
+                                    hipStream_t stream);
+
+struct MxLinearArgs {
+    const uint8_t* x;
+    const uint8_t* x_sf;
+    const uint8_t* w;      // codes [N/32][KT][32][64 B], behind them scales [N/32][KT][32][4 B]
+    uint16_t* y;
+    uint8_t* ws;
+    int64_t y_stride;
+    int M, N, K, format;
+};
+struct MxLinearChoice {
+    int kernel, tokens, columns, splits;  // kernel: moe_linear.hip's own numbers; a tile's rows and columns
+    bool pad_scales;                      // x_sf is copied to rows of whole words first
+    size_t scale_bytes, partial_bytes;    // of the workspace, in this order
+    size_t workspace_bytes() const { return scale_bytes + partial_bytes; }
+};
+MxLinearChoice choose_mx_linear(int M, int N, int K, int format);
+size_t most_mx_linear_workspace(int M, int N, int K, int format);  // at least that of any choice for 0 .. M tokens
+hipError_t launch_mx_linear(const MxLinearArgs& a, const MxLinearChoice& c, hipStream_t stream);
+
+// ---- balance of the load, and the gate's gradient
+struct BalanceArgs {
+    const void* logits;          // or null: counts alone
+    const int64_t* topk_idx;
+    const int64_t* seq_offsets;  // or null: one sequence of all rows
+    int64_t stride;
+    int T, E, k, S, score, logits_type;
+    int32_t* counts;             // or null, as all that follow
+    int32_t* rows;
+    float* share;
+    float* loss;
+    float* z;
+};
+size_t balance_workspace(int T, int E, int S);
+hipError_t launch_balance(const BalanceArgs& a, void* ws, hipStream_t stream);
+
+struct GateGradArgs {
+    const void* logits;
+    const int64_t* topk_idx;
+    const int64_t* seq_offsets;  // or null
+    const int32_t* counts;       // with rows and d_loss, or null
+    const int32_t* rows;
+    const float* d_loss;
+    const float* d_z;            // or null; needs rows
+    const float* d_topk_w;       // or null
+    void* d_logits;
+    int64_t stride;
+    int T, E, k, S, score, renorm, logits_type;
+    float scale;
+};
+hipError_t launch_gate_grad(const GateGradArgs& a, hipStream_t stream);
+
 }  // namespace moe

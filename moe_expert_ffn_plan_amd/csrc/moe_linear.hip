@@ -1,0 +1,391 @@
+// Dense product y = x W^T on the scaled matrix instructions: x E2M1 or E4M3, W E2M1, a UE8M0 scale per 32 columns.
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kStep = 128;       // columns of a K-step
+constexpr int kBlockCodes = 2048, kBlockScales = 128;  // bytes of 32 weight rows in a K-step
+constexpr int kNumXcd = 8;
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+__device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return reinterpret_cast<const uint8_t*>(((uint64_t)hi << 32) | lo);
+}
+
+// LDS DMA: lane l reads 16 (4) bytes at the wave-uniform base plus its own offset and writes them at LDS address
+// lds + 16 l (4 l).  Issued from asm so that no wait for it is put in front of every LDS read.
+__device__ __forceinline__ void dma16(uint32_t voff, const uint8_t* base, uint32_t lds) {
+    asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void dma4(uint32_t voff, const uint8_t* base, uint32_t lds) {
+    asm volatile("global_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)p);
+}
+// At most N of this wave's DMA instructions stay in flight and its LDS reads are done; then all waves meet.
+template <int N>
+__device__ __forceinline__ void wait_and_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+template <int D>
+__device__ __forceinline__ void wait_stages_and_barrier(int later) {  // later: stages of D that may stay in flight
+    if (later >= 3) wait_and_barrier<3 * D>();
+    else if (later == 2) wait_and_barrier<2 * D>();
+    else if (later == 1) wait_and_barrier<D>();
+    else wait_and_barrier<0>();
+}
+
+struct Args {
+    const uint8_t* x;
+    const uint8_t* sf;
+    const uint8_t* w;
+    const uint8_t* w_sf;
+    uint16_t* y;
+    float* partial;       // [splits][M][columns] where splits > 1
+    int64_t y_stride;
+    int64_t x_row;        // bytes of a row of codes
+    int sf_row;           // bytes from one row of scales to the next, whole words
+    int M, N, KT, tail;   // tail: bytes of a row's last K-step
+    int blocks;           // blocks of 32 weight rows
+    int splits, per;      // K-steps of a split
+    int mt, nt;           // tiles
+};
+
+__device__ __forceinline__ int64_t partial_columns(const Args& a) { return (int64_t)a.blocks * 32; }
+
+// Two neighbouring outputs of a row.
+__device__ __forceinline__ void store2(const Args& a, int row, int col, float v0, float v1) {
+    uint16_t* out = a.y + (int64_t)row * a.y_stride + col;
+    const uint32_t both = pack_bf16(v0, v1);
+    if ((a.y_stride & 1) == 0 && col + 1 < a.N) {
+        *reinterpret_cast<uint32_t*>(out) = both;
+    } else {
+        if (col < a.N) out[0] = (uint16_t)both;
+        if (col + 1 < a.N) out[1] = (uint16_t)(both >> 16);
+    }
+}
+
+// One tile of BM x BN outputs per workgroup, WM x WN waves.
+//
+// A K-step of 128 columns is a stage of a ring of NS in LDS, filled by DMA.  It is multiplied in two halves by
+// V_MFMA_SCALE_F32_32X32X64: the hardware's two blocks of 32 columns are, in half s, the K-step's blocks s and 2 + s,
+// so that lane l (row l % 32, q = l / 32) finds its two scales, of blocks 2q and 2q + 1, side by side in its row's word.
+// An E2M1 lane holds the 32 columns of block 2q + s; an E4M3 lane 16 columns of each of the two blocks.  Rows of codes
+// are 64 or 128 bytes with their 16-byte chunks permuted by the row (chunk ^ (row / 2) % 4, or % 8): the lanes that
+// LDS serves together then read distinct banks.
+//
+// Half 1 of a stage is read while half 0 is multiplied, and half 0 of the next stage while half 1 is; the barrier that
+// hands over a stage's buffer stands between the two.
+template <int FMT, int BM, int BN, int WM, int WN, int NS_>
+struct Tile {
+    static constexpr int W = WM * WN, THREADS = 64 * W, NS = NS_;
+    static constexpr int RB = FMT == MOE_E2M1 ? 64 : 128;  // bytes of a row in a stage
+    static constexpr int CHUNKS = RB / 16;
+    static constexpr int MI = BM / WM / 32, NI = BN / WN / 32;
+    static constexpr int A = 0, B = BM * RB, S = B + BN * 64, STAGE = S + (BM + BN) * 4;
+    static constexpr int A_I = BM * RB / 1024, B_I = BN * 64 / 1024, S_I = (BM + BN) / 64;  // DMA instructions
+    static constexpr int A_PW = (A_I + W - 1) / W, B_PW = (B_I + W - 1) / W, S_PW = (S_I + W - 1) / W;
+    static constexpr int D = A_PW + B_PW + S_PW;
+    static_assert(BM % 64 == 0 && BN % 64 == 0 && NI % 2 == 0 && NS >= 2 && NS <= 4 && (NS - 1) * D < 63, "tile");
+    static_assert(W * 64 / CHUNKS % 16 == 0 && A_I % W == 0, "rows of a wave's instructions");
+};
+
+template <int FMT>
+struct Frag {
+    typedef v4i type;
+};
+template <>
+struct Frag<MOE_E4M3> {
+    typedef v8i type;
+};
+
+template <int FMT, int H>
+__device__ __forceinline__ v16f mfma(const typename Frag<FMT>::type& a, const v4i& b, const v16f& c, int sa, int sb) {
+    const v8i b8 = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
+    if constexpr (FMT == MOE_E2M1) {
+        const v8i a8 = {a[0], a[1], a[2], a[3], 0, 0, 0, 0};
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, H, sa, H, sb);
+    } else {
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b8, c, 0, 4, H, sa, H, sb);
+    }
+}
+
+template <int FMT, int BM, int BN, int WM, int WN, int NS, int OCC>
+__global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
+    using T = Tile<FMT, BM, BN, WM, WN, NS>;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * T::STAGE];
+
+    // every XCD takes a contiguous run of tiles, in columns of 8 tile rows, so that what runs together shares
+    // its rows of x and its weights in the XCD's L2
+    const int per_split = g.mt * g.nt, tiles = per_split * g.splits;
+    const int share = (tiles + kNumXcd - 1) / kNumXcd;
+    const int id = (blockIdx.x % kNumXcd) * share + blockIdx.x / kNumXcd;
+    if ((int)(blockIdx.x / kNumXcd) >= share || id >= tiles) return;
+    const int z = id / per_split, in = id % per_split;
+    const int band = in / (8 * g.nt), rows = min(8, g.mt - band * 8), at = in - band * 8 * g.nt;
+    const int m0 = (band * 8 + at % rows) * BM, n0 = at / rows * BN;
+    const int k0 = z * g.per, n = min(g.per, g.KT - k0);
+
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    // ---- DMA sources
+    const uint8_t* x = uniform_ptr(g.x + (int64_t)m0 * g.x_row);
+    const int swz = T::CHUNKS == 4 ? 3 : 7;
+    // the rows of a wave's instructions lie W * 64 / CHUNKS apart, a multiple of the permutation's 16
+    const uint32_t chunk = ((lane % T::CHUNKS) ^ (((w * (64 / T::CHUNKS) + lane / T::CHUNKS) >> 1) & swz)) * 16;
+    uint32_t a_row[T::A_PW];
+#pragma unroll
+    for (int i = 0; i < T::A_PW; ++i) {
+        const int row = (i * T::W + w) % T::A_I * (64 / T::CHUNKS) + lane / T::CHUNKS;
+        a_row[i] = (uint32_t)min(row, g.M - 1 - m0) * (uint32_t)g.x_row;
+    }
+    const int nb0 = n0 / 32;
+    const uint8_t* b_src[T::B_PW];
+#pragma unroll
+    for (int i = 0; i < T::B_PW; ++i) {
+        const int blk = (i * T::W + w) % T::B_I;
+        b_src[i] = uniform_ptr(g.w + (int64_t)min(nb0 + blk / 2, g.blocks - 1) * g.KT * kBlockCodes + (blk & 1) * 1024);
+    }
+    uint32_t s_off[T::S_PW], s_step[T::S_PW];
+    const uint8_t* s_src[T::S_PW];
+#pragma unroll
+    for (int i = 0; i < T::S_PW; ++i) {
+        const int idx = (i * T::W + w) % T::S_I;
+        if (idx < BM / 64) {  // 64 rows of x
+            s_src[i] = uniform_ptr(g.sf + (int64_t)m0 * g.sf_row);
+            s_step[i] = 4;
+            s_off[i] = (uint32_t)min(idx * 64 + lane, g.M - 1 - m0) * (uint32_t)g.sf_row;
+        } else {  // a pair of blocks of weight rows
+            const int pair = min(nb0 + (idx - BM / 64) * 2, g.blocks - 2);
+            s_src[i] = uniform_ptr(g.w_sf + (int64_t)pair * g.KT * kBlockScales);
+            s_step[i] = kBlockScales;
+            s_off[i] = (uint32_t)(lane % 32) * 4 + (uint32_t)(lane / 32) * (uint32_t)g.KT * kBlockScales;
+        }
+    }
+    auto issue = [&](int t) {
+        uint8_t* st = smem + t % NS * T::STAGE;
+        const int kt = k0 + t;
+        // columns past the last are those of the row's last chunk: the weights there are 0
+        const uint32_t c = kt == g.KT - 1 ? min(chunk, (uint32_t)g.tail - 16) : chunk;
+#pragma unroll
+        for (int i = 0; i < T::A_PW; ++i)
+            dma16(a_row[i] + c, x + (int64_t)kt * T::RB, lds_addr(st + T::A + (i * T::W + w) % T::A_I * 1024));
+#pragma unroll
+        for (int i = 0; i < T::B_PW; ++i)
+            dma16((uint32_t)lane * 16, b_src[i] + (int64_t)kt * kBlockCodes, lds_addr(st + T::B + (i * T::W + w) % T::B_I * 1024));
+#pragma unroll
+        for (int i = 0; i < T::S_PW; ++i)
+            dma4(s_off[i], s_src[i] + (int64_t)kt * s_step[i], lds_addr(st + T::S + (i * T::W + w) % T::S_I * 256));
+    };
+
+    // ---- fragments
+    const int r = lane & 31, q = lane >> 5, rsw = (r >> 1) & swz, bsw = (r >> 1) & 3;
+    const int wm0 = w / WN * (BM / WM), wn0 = w % WN * (BN / WN);
+    typedef typename Frag<FMT>::type fa;
+    auto read_a = [&](fa (&f)[T::MI], const uint8_t* st, int h) {
+#pragma unroll
+        for (int i = 0; i < T::MI; ++i) {
+            const uint8_t* row = st + T::A + (wm0 + i * 32 + r) * T::RB;
+            if constexpr (FMT == MOE_E2M1) {
+                f[i] = *reinterpret_cast<const v4i*>(row + (((2 * q + h) ^ rsw) << 4));
+            } else {
+                const v4i lo = *reinterpret_cast<const v4i*>(row + (((2 * h + q) ^ rsw) << 4));
+                const v4i hi = *reinterpret_cast<const v4i*>(row + (((4 + 2 * h + q) ^ rsw) << 4));
+                f[i] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            }
+        }
+    };
+    auto read_b = [&](v4i (&f)[T::NI], const uint8_t* st, int h) {
+#pragma unroll
+        for (int i = 0; i < T::NI; ++i)
+            f[i] = *reinterpret_cast<const v4i*>(st + T::B + (wn0 + i * 32 + r) * 64 + (((2 * q + h) ^ bsw) << 4));
+    };
+    auto read_s = [&](int (&sa)[T::MI], int (&sb)[T::NI], const uint8_t* st) {
+        const uint32_t* s = reinterpret_cast<const uint32_t*>(st + T::S);
+#pragma unroll
+        for (int i = 0; i < T::MI; ++i) sa[i] = (int)(s[wm0 + i * 32 + r] >> (16 * q));
+#pragma unroll
+        for (int i = 0; i < T::NI; ++i) sb[i] = (int)(s[BM + wn0 + i * 32 + r] >> (16 * q));
+    };
+
+    v16f acc[T::MI][T::NI];
+#pragma unroll
+    for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+        for (int j = 0; j < T::NI; ++j) acc[i][j] = v16f{};
+#pragma unroll
+    for (int t = 0; t < NS; ++t)
+        if (t < n) issue(t);
+    fa a0[T::MI], a1[T::MI];
+    v4i b0[T::NI], b1[T::NI];
+    int sa[T::MI], sb[T::NI];
+    wait_stages_and_barrier<T::D>(min(NS, n) - 1);
+    read_a(a0, smem, 0);
+    read_b(b0, smem, 0);
+    read_s(sa, sb, smem);
+    for (int t = 0; t < n; ++t) {
+        const uint8_t* st = smem + t % NS * T::STAGE;
+        read_a(a1, st, 1);
+        read_b(b1, st, 1);
+#pragma unroll
+        for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+            for (int j = 0; j < T::NI; ++j) acc[i][j] = mfma<FMT, 0>(a0[i], b0[j], acc[i][j], sa[i], sb[j]);
+        int ta[T::MI], tb[T::NI];
+#pragma unroll
+        for (int i = 0; i < T::MI; ++i) ta[i] = sa[i];
+#pragma unroll
+        for (int j = 0; j < T::NI; ++j) tb[j] = sb[j];
+        if (t + 1 < n) {
+            wait_stages_and_barrier<T::D>(min(NS - 2, n - 2 - t));  // stage t + 1 is there, stage t read
+            if (t + NS < n) issue(t + NS);
+            const uint8_t* next = smem + (t + 1) % NS * T::STAGE;
+            read_a(a0, next, 0);
+            read_b(b0, next, 0);
+            read_s(sa, sb, next);
+        }
+#pragma unroll
+        for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+            for (int j = 0; j < T::NI; ++j) acc[i][j] = mfma<FMT, 1>(a1[i], b1[j], acc[i][j], ta[i], tb[j]);
+    }
+
+    // ---- outputs: weight rows are laid so that lane r of blocks 2b and 2b + 1 holds outputs 2r and 2r + 1 of their 64
+    float* part = g.partial + (int64_t)z * g.M * partial_columns(g);
+#pragma unroll
+    for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int row = m0 + wm0 + i * 32 + 8 * (e / 4) + 4 * q + e % 4;
+            if (row >= g.M) continue;
+#pragma unroll
+            for (int j = 0; j < T::NI; j += 2) {
+                const int col = n0 + wn0 + j * 32 + 2 * r;
+                if (g.splits > 1) {
+                    if (col < partial_columns(g))
+                        *reinterpret_cast<f32x2*>(part + (int64_t)row * partial_columns(g) + col) =
+                            f32x2{acc[i][j][e], acc[i][j + 1][e]};
+                } else {
+                    store2(g, row, col, acc[i][j][e], acc[i][j + 1][e]);
+                }
+            }
+        }
+}
+
+constexpr int kThreads = 256;
+
+// The splits' sums, in their order.
+__global__ __launch_bounds__(kThreads) void join_kernel(Args g) {
+    const int64_t columns = partial_columns(g), at = (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x) * 4;
+    if (at >= (int64_t)g.M * columns) return;
+    v4f v = {0.f, 0.f, 0.f, 0.f};
+    for (int z = 0; z < g.splits; ++z) v += *reinterpret_cast<const v4f*>(g.partial + (int64_t)z * g.M * columns + at);
+    const int row = (int)(at / columns), col = (int)(at % columns);
+    store2(g, row, col, v[0], v[1]);
+    store2(g, row, col + 2, v[2], v[3]);
+}
+
+// Rows of scales as whole words, zeros behind the last column.
+__global__ __launch_bounds__(kThreads) void pad_scales_kernel(const uint8_t* sf, int M, int blocks, int KT, uint32_t* out) {
+    const int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
+    if (i >= (int64_t)M * KT) return;
+    const int64_t row = i / KT, kt = i % KT;
+    uint32_t v = 0;
+    for (int b = 0; b < 4; ++b)
+        if (kt * 4 + b < blocks) v |= (uint32_t)sf[row * blocks + kt * 4 + b] << (8 * b);
+    out[i] = v;
+}
+
+template <int FMT, int BM, int BN, int WM, int WN, int NS, int OCC>
+void go(const Args& g, hipStream_t stream) {
+    const int tiles = g.mt * g.nt * g.splits, share = (tiles + kNumXcd - 1) / kNumXcd;
+    hipLaunchKernelGGL((tile_kernel<FMT, BM, BN, WM, WN, NS, OCC>), dim3((unsigned)(share * kNumXcd)), dim3(64 * WM * WN), 0,
+                       stream, g);
+}
+
+}  // namespace
+
+constexpr int kFillTiles = 256;  // a workgroup for every compute unit
+
+MxLinearChoice choose_mx_linear(int M, int N, int K, int format) {
+    MxLinearChoice c{};
+    const int KT = mx_steps(K);
+    const int64_t big = (((int64_t)M + 255) / 256) * (((int64_t)N + 255) / 256);
+    c.kernel = big >= kFillTiles ? 0 : 1;
+    c.tokens = c.columns = c.kernel == 0 ? 256 : 128;
+    const int64_t tiles = (((int64_t)M + c.tokens - 1) / c.tokens) * (((int64_t)N + c.columns - 1) / c.columns);
+    c.splits = 1;
+    while (tiles * c.splits < kFillTiles && KT / (c.splits * 2) >= 4 && c.splits < 16) c.splits *= 2;
+    c.pad_scales = K % 128 != 0;
+    c.scale_bytes = c.pad_scales ? align_up((size_t)M * KT * 4, kAlign) : 0;
+    c.partial_bytes = c.splits > 1 ? (size_t)c.splits * M * mx_column_blocks(N) * 32 * 4 : 0;
+    return c;
+}
+
+size_t most_mx_linear_workspace(int M, int N, int K, int format) {
+    // More tokens in as many tiles need more, and from kFillTiles tile rows on nothing is split: the most is that of M,
+    // or of the last number of tokens of some smaller number of tile rows.
+    size_t most = M > 0 ? choose_mx_linear(M, N, K, format).workspace_bytes() : 0;
+    for (int m = std::min(M / 16, kFillTiles * 8) * 16; m > 0; m -= 16)
+        most = std::max(most, choose_mx_linear(m, N, K, format).workspace_bytes());
+    return most;
+}
+
+hipError_t launch_mx_linear(const MxLinearArgs& a, const MxLinearChoice& c, hipStream_t stream) {
+    Args g{};
+    g.x = a.x;
+    g.w = a.w;
+    g.y = a.y;
+    g.y_stride = a.y_stride;
+    g.M = a.M;
+    g.N = a.N;
+    g.KT = mx_steps(a.K);
+    g.blocks = (int)mx_column_blocks(a.N);
+    g.w_sf = a.w + (int64_t)g.blocks * g.KT * kBlockCodes;
+    const int per16 = a.format == MOE_E2M1 ? 2 : 1;  // codes of a byte
+    g.x_row = a.K / per16;
+    g.tail = (a.K - (g.KT - 1) * kStep) / per16;
+    g.sf = a.x_sf;
+    g.sf_row = a.K / 32;
+    g.partial = reinterpret_cast<float*>(a.ws + c.scale_bytes);
+    if (c.pad_scales) {
+        g.sf = a.ws;
+        g.sf_row = g.KT * 4;
+        hipLaunchKernelGGL(pad_scales_kernel, wide_grid(((int64_t)a.M * g.KT + kThreads - 1) / kThreads), dim3(kThreads), 0,
+                           stream, a.x_sf, a.M, a.K / 32, g.KT, reinterpret_cast<uint32_t*>(a.ws));
+    }
+    g.splits = c.splits;
+    g.per = (g.KT + c.splits - 1) / c.splits;
+    g.splits = (g.KT + g.per - 1) / g.per;  // none without a K-step
+    g.mt = (a.M + c.tokens - 1) / c.tokens;
+    g.nt = (a.N + c.columns - 1) / c.columns;
+    if (c.kernel == 0) {
+        if (a.format == MOE_E2M1) go<MOE_E2M1, 256, 256, 2, 2, 4, 1>(g, stream);
+        else go<MOE_E4M3, 256, 256, 2, 2, 3, 1>(g, stream);
+    } else {
+        if (a.format == MOE_E2M1) go<MOE_E2M1, 128, 128, 2, 2, 4, 2>(g, stream);
+        else go<MOE_E4M3, 128, 128, 2, 2, 3, 2>(g, stream);
+    }
+    if (g.splits > 1)
+        hipLaunchKernelGGL(join_kernel, wide_grid(((int64_t)a.M * (g.blocks * 32) / 4 + kThreads - 1) / kThreads),
+                           dim3(kThreads), 0, stream, g);
+    return hipGetLastError();
+}
+
+}  // namespace moe
