@@ -607,7 +607,7 @@ typedef struct moe_mx_linear_shape {
  * (w_sf any), into w_tiled of moe_mx_linear_weight_bytes, 16-byte aligned:
  *   codes   [B][KT][128 slots of 16 B], B = 2 * ceil(N / 64), KT =
  *           ceil(K / 128); slot p of (b, kt) holds the 32 columns from
- *           128 kt + 32 ((p & 3) ^ ((c >> 1) & 3)) of weight row
+ *           128 kt + 32 ((p & 3) ^ ((c >> 2) & 3)) of weight row
  *           64 (b / 2) + 2 c + b % 2, c = p >> 2;
  *   scales  behind them, [B][KT][32 c][4 B];
  * zeros where there is no such row or column. */

@@ -285,7 +285,7 @@ struct MxLinearArgs {
 };
 struct MxLinearChoice {
     int kernel, tokens, columns, splits;  // kernel: moe_linear.hip's own numbers; a tile's rows and columns
-    bool pad_scales;                      // x_sf is copied to rows of whole words first
+    bool tile_scales;                     // x_sf is laid out by K-step first
     size_t scale_bytes, partial_bytes;    // of the workspace, in this order
     size_t workspace_bytes() const { return scale_bytes + partial_bytes; }
 };

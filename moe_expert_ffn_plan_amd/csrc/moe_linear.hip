@@ -1,6 +1,8 @@
 // Dense product y = x W^T on the scaled matrix instructions: x E2M1 or E4M3, W E2M1, a UE8M0 scale per 32 columns.
 #include "moe_internal.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -43,14 +45,6 @@ __device__ __forceinline__ void wait_and_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
     __builtin_amdgcn_sched_barrier(0);
 }
-template <int D>
-__device__ __forceinline__ void wait_stages_and_barrier(int later) {  // later: stages of D that may stay in flight
-    if (later >= 3) wait_and_barrier<3 * D>();
-    else if (later == 2) wait_and_barrier<2 * D>();
-    else if (later == 1) wait_and_barrier<D>();
-    else wait_and_barrier<0>();
-}
-
 struct Args {
     const uint8_t* x;
     const uint8_t* sf;
@@ -60,7 +54,9 @@ struct Args {
     float* partial;       // [splits][M][columns] where splits > 1
     int64_t y_stride;
     int64_t x_row;        // bytes of a row of codes
-    int sf_row;           // bytes from one row of scales to the next, whole words
+    // scales of x as words: row m of K-step kt at (m / 64) * sf_band + (m % 64) * sf_row + kt * sf_step
+    int64_t sf_band;
+    int sf_row, sf_step;
     int M, N, KT, tail;   // tail: bytes of a row's last K-step
     int blocks;           // blocks of 32 weight rows
     int splits, per;      // K-steps of a split
@@ -87,8 +83,8 @@ __device__ __forceinline__ void store2(const Args& a, int row, int col, float v0
 // V_MFMA_SCALE_F32_32X32X64: the hardware's two blocks of 32 columns are, in half s, the K-step's blocks s and 2 + s,
 // so that lane l (row l % 32, q = l / 32) finds its two scales, of blocks 2q and 2q + 1, side by side in its row's word.
 // An E2M1 lane holds the 32 columns of block 2q + s; an E4M3 lane 16 columns of each of the two blocks.  Rows of codes
-// are 64 or 128 bytes with their 16-byte chunks permuted by the row (chunk ^ (row / 2) % 4, or % 8): the lanes that
-// LDS serves together then read distinct banks.
+// are 64 or 128 bytes with their 16-byte chunks permuted by the row (chunk ^ (row / 4) % 4, or ^ (row / 2) % 8): the 16
+// lanes that LDS serves together (0-3, 12-15, 20-27 and so on) then read distinct banks of its 64.
 //
 // Half 1 of a stage is read while half 0 is multiplied, and half 0 of the next stage while half 1 is; the barrier that
 // hands over a stage's buffer stands between the two.
@@ -102,6 +98,7 @@ struct Tile {
     static constexpr int A_I = BM * RB / 1024, B_I = BN * 64 / 1024, S_I = (BM + BN) / 64;  // DMA instructions
     static constexpr int A_PW = (A_I + W - 1) / W, B_PW = (B_I + W - 1) / W, S_PW = (S_I + W - 1) / W;
     static constexpr int D = A_PW + B_PW + S_PW;
+    static __device__ __forceinline__ int permuted(int row) { return FMT == MOE_E2M1 ? (row >> 2) & 3 : (row >> 1) & 7; }
     static_assert(BM % 64 == 0 && BN % 64 == 0 && NI % 2 == 0 && NS >= 2 && NS <= 4 && (NS - 1) * D < 63, "tile");
     static_assert(W * 64 / CHUNKS % 16 == 0 && A_I % W == 0, "rows of a wave's instructions");
 };
@@ -146,9 +143,8 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
 
     // ---- DMA sources
     const uint8_t* x = uniform_ptr(g.x + (int64_t)m0 * g.x_row);
-    const int swz = T::CHUNKS == 4 ? 3 : 7;
     // the rows of a wave's instructions lie W * 64 / CHUNKS apart, a multiple of the permutation's 16
-    const uint32_t chunk = ((lane % T::CHUNKS) ^ (((w * (64 / T::CHUNKS) + lane / T::CHUNKS) >> 1) & swz)) * 16;
+    const uint32_t chunk = ((lane % T::CHUNKS) ^ T::permuted(w * (64 / T::CHUNKS) + lane / T::CHUNKS)) * 16;
     uint32_t a_row[T::A_PW];
 #pragma unroll
     for (int i = 0; i < T::A_PW; ++i) {
@@ -162,66 +158,80 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
         const int blk = (i * T::W + w) % T::B_I;
         b_src[i] = uniform_ptr(g.w + (int64_t)min(nb0 + blk / 2, g.blocks - 1) * g.KT * kBlockCodes + (blk & 1) * 1024);
     }
+    // a wave's scales of row r of its blocks of 32 lie side by side: word (part * 32 + r) * blocks + i is that of row
+    // part * 32 * blocks + 32 i + r
     uint32_t s_off[T::S_PW], s_step[T::S_PW];
     const uint8_t* s_src[T::S_PW];
 #pragma unroll
     for (int i = 0; i < T::S_PW; ++i) {
         const int idx = (i * T::W + w) % T::S_I;
-        if (idx < BM / 64) {  // 64 rows of x
-            s_src[i] = uniform_ptr(g.sf + (int64_t)m0 * g.sf_row);
-            s_step[i] = 4;
-            s_off[i] = (uint32_t)min(idx * 64 + lane, g.M - 1 - m0) * (uint32_t)g.sf_row;
-        } else {  // a pair of blocks of weight rows
-            const int pair = min(nb0 + (idx - BM / 64) * 2, g.blocks - 2);
-            s_src[i] = uniform_ptr(g.w_sf + (int64_t)pair * g.KT * kBlockScales);
+        if (idx < BM / 64) {  // rows of x
+            const int word = idx * 64 + lane, at = word / T::MI;
+            const int row = at / 32 * (32 * T::MI) + word % T::MI * 32 + at % 32;
+            const int m = min(row, g.M - 1 - m0);
+            s_src[i] = uniform_ptr(g.sf + m0 / 64 * g.sf_band);
+            s_step[i] = g.sf_step;
+            s_off[i] = (uint32_t)(m / 64) * (uint32_t)g.sf_band + (uint32_t)(m % 64) * (uint32_t)g.sf_row;
+        } else {  // weight rows
+            const int word = (idx - BM / 64) * 64 + lane, at = word / T::NI;
+            const int blk = at / 32 * T::NI + word % T::NI;
+            s_src[i] = uniform_ptr(g.w_sf + (int64_t)nb0 * g.KT * kBlockScales);
             s_step[i] = kBlockScales;
-            s_off[i] = (uint32_t)(lane % 32) * 4 + (uint32_t)(lane / 32) * (uint32_t)g.KT * kBlockScales;
+            s_off[i] = (uint32_t)min(blk, g.blocks - 1 - nb0) * (uint32_t)g.KT * kBlockScales + (uint32_t)(at % 32) * 4;
         }
     }
-    auto issue = [&](int t) {
-        uint8_t* st = smem + t % NS * T::STAGE;
-        const int kt = k0 + t;
-        // columns past the last are those of the row's last chunk: the weights there are 0
-        const uint32_t c = kt == g.KT - 1 ? min(chunk, (uint32_t)g.tail - 16) : chunk;
-#pragma unroll
-        for (int i = 0; i < T::A_PW; ++i)
+    // DMA instruction i of K-step k0 + t
+    auto issue1 = [&](int i, uint8_t* st, int kt) {
+        if (i < T::A_PW) {
+            // columns past the last are those of the row's last chunk: the weights there are 0
+            const uint32_t c = kt == g.KT - 1 ? min(chunk, (uint32_t)g.tail - 16) : chunk;
             dma16(a_row[i] + c, x + (int64_t)kt * T::RB, lds_addr(st + T::A + (i * T::W + w) % T::A_I * 1024));
-#pragma unroll
-        for (int i = 0; i < T::B_PW; ++i)
+        } else if (i < T::A_PW + T::B_PW) {
+            i -= T::A_PW;
             dma16((uint32_t)lane * 16, b_src[i] + (int64_t)kt * kBlockCodes, lds_addr(st + T::B + (i * T::W + w) % T::B_I * 1024));
-#pragma unroll
-        for (int i = 0; i < T::S_PW; ++i)
+        } else {
+            i -= T::A_PW + T::B_PW;
             dma4(s_off[i], s_src[i] + (int64_t)kt * s_step[i], lds_addr(st + T::S + (i * T::W + w) % T::S_I * 256));
+        }
     };
 
     // ---- fragments
-    const int r = lane & 31, q = lane >> 5, rsw = (r >> 1) & swz, bsw = (r >> 1) & 3;
-    const int wm0 = w / WN * (BM / WM), wn0 = w % WN * (BN / WN);
+    const int r = lane & 31, q = lane >> 5, rsw = T::permuted(r), bsw = (r >> 2) & 3;
+    const int wm = w / WN, wn = w % WN, wm0 = wm * (BM / WM), wn0 = wn * (BN / WN);
     typedef typename Frag<FMT>::type fa;
-    auto read_a = [&](fa (&f)[T::MI], const uint8_t* st, int h) {
-#pragma unroll
-        for (int i = 0; i < T::MI; ++i) {
+    struct Half {
+        fa a[T::MI];
+        v4i b[T::NI];
+    };
+    // fragment i of half h of a stage, in the order in which they are multiplied
+    auto read1 = [&](int i, Half& f, const uint8_t* st, int h) {
+        if (i == 0 || i > T::NI) {
+            i = i == 0 ? 0 : i - T::NI;
             const uint8_t* row = st + T::A + (wm0 + i * 32 + r) * T::RB;
             if constexpr (FMT == MOE_E2M1) {
-                f[i] = *reinterpret_cast<const v4i*>(row + (((2 * q + h) ^ rsw) << 4));
+                f.a[i] = *reinterpret_cast<const v4i*>(row + (((2 * q + h) ^ rsw) << 4));
             } else {
                 const v4i lo = *reinterpret_cast<const v4i*>(row + (((2 * h + q) ^ rsw) << 4));
                 const v4i hi = *reinterpret_cast<const v4i*>(row + (((4 + 2 * h + q) ^ rsw) << 4));
-                f[i] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                f.a[i] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
             }
+        } else {
+            i -= 1;
+            f.b[i] = *reinterpret_cast<const v4i*>(st + T::B + (wn0 + i * 32 + r) * 64 + (((2 * q + h) ^ bsw) << 4));
         }
     };
-    auto read_b = [&](v4i (&f)[T::NI], const uint8_t* st, int h) {
-#pragma unroll
-        for (int i = 0; i < T::NI; ++i)
-            f[i] = *reinterpret_cast<const v4i*>(st + T::B + (wn0 + i * 32 + r) * 64 + (((2 * q + h) ^ bsw) << 4));
+    struct Scales {
+        int a[T::MI], b[T::NI];
     };
-    auto read_s = [&](int (&sa)[T::MI], int (&sb)[T::NI], const uint8_t* st) {
-        const uint32_t* s = reinterpret_cast<const uint32_t*>(st + T::S);
+    auto read_scales = [&](Scales& f, const uint8_t* st) {
+        typedef uint32_t va __attribute__((ext_vector_type(T::MI)));
+        typedef uint32_t vb __attribute__((ext_vector_type(T::NI)));
+        const va sa = *reinterpret_cast<const va*>(st + T::S + (wm * 32 + r) * T::MI * 4);
+        const vb sb = *reinterpret_cast<const vb*>(st + T::S + BM * 4 + (wn * 32 + r) * T::NI * 4);
 #pragma unroll
-        for (int i = 0; i < T::MI; ++i) sa[i] = (int)(s[wm0 + i * 32 + r] >> (16 * q));
+        for (int i = 0; i < T::MI; ++i) f.a[i] = (int)(sa[i] >> (16 * q));
 #pragma unroll
-        for (int i = 0; i < T::NI; ++i) sb[i] = (int)(s[BM + wn0 + i * 32 + r] >> (16 * q));
+        for (int i = 0; i < T::NI; ++i) f.b[i] = (int)(sb[i] >> (16 * q));
     };
 
     v16f acc[T::MI][T::NI];
@@ -229,42 +239,69 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
     for (int i = 0; i < T::MI; ++i)
 #pragma unroll
         for (int j = 0; j < T::NI; ++j) acc[i][j] = v16f{};
+    constexpr int FRAGS = T::MI + T::NI, SLOTS = T::MI * T::NI, PER = (FRAGS + SLOTS - 1) / SLOTS;
+    Half f0, f1;
+    Scales sc, sn;
+    // K-step t.  The DMA of stage t + NS begins behind the barrier that frees its buffer (parts 0 .. D1 - 1, if `begin`)
+    // and goes on in front of the next (`finish`, of stage t + NS - 1): in one burst the waves wait for each other's
+    // requests.  later: stages behind t + 1 that are in flight at the barrier.  The order is pinned: reads and DMA stand
+    // between the products, so that the matrix core always has the next one.
+    constexpr int D1 = T::D / 2;
+    auto dma_slot = [](int i, int count) { return (2 * i + 1) * SLOTS / (2 * count); };
+    auto step = [&](int t, auto finish, auto begin, auto later) {
+        uint8_t* st = smem + t % NS * T::STAGE;
+        const uint8_t* next = smem + (t + 1) % NS * T::STAGE;
+        uint8_t* last = smem + (t + NS - 1) % NS * T::STAGE;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int k = 0; k < SLOTS; ++k) {
+            const int i = k / T::NI, j = k % T::NI;
+            acc[i][j] = mfma<FMT, 0>(f0.a[i], f0.b[j], acc[i][j], sc.a[i], sc.b[j]);
+#pragma unroll
+            for (int h = k * PER; h < min((k + 1) * PER, FRAGS); ++h) read1(h, f1, st, 1);
+            if constexpr (decltype(finish)::value) {
+#pragma unroll
+                for (int h = D1; h < T::D; ++h)
+                    if (dma_slot(h - D1, T::D - D1) == k) issue1(h, last, k0 + min(t + NS - 1, n - 1));
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        wait_and_barrier<decltype(later)::value * T::D>();  // stage t + 1 is there, stage t read
+#pragma unroll
+        for (int k = 0; k < SLOTS; ++k) {
+            const int i = k / T::NI, j = k % T::NI;
+            acc[i][j] = mfma<FMT, 1>(f1.a[i], f1.b[j], acc[i][j], sc.a[i], sc.b[j]);
+#pragma unroll
+            for (int h = k * PER; h < min((k + 1) * PER, FRAGS); ++h) read1(h, f0, next, 0);
+            if (k == SLOTS / 2) read_scales(sn, next);
+            if constexpr (decltype(begin)::value) {
+#pragma unroll
+                for (int h = 0; h < D1; ++h)
+                    if (dma_slot(h, D1) == k) issue1(h, st, k0 + t + NS);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        sc = sn;
+    };
+    // a split of fewer than NS K-steps fills the ring with its last one
 #pragma unroll
     for (int t = 0; t < NS; ++t)
-        if (t < n) issue(t);
-    fa a0[T::MI], a1[T::MI];
-    v4i b0[T::NI], b1[T::NI];
-    int sa[T::MI], sb[T::NI];
-    wait_stages_and_barrier<T::D>(min(NS, n) - 1);
-    read_a(a0, smem, 0);
-    read_b(b0, smem, 0);
-    read_s(sa, sb, smem);
-    for (int t = 0; t < n; ++t) {
-        const uint8_t* st = smem + t % NS * T::STAGE;
-        read_a(a1, st, 1);
-        read_b(b1, st, 1);
 #pragma unroll
-        for (int i = 0; i < T::MI; ++i)
+        for (int i = 0; i < (t < NS - 1 ? T::D : D1); ++i) issue1(i, smem + t * T::STAGE, k0 + min(t, n - 1));
+    wait_and_barrier<(NS - 2) * T::D + D1>();
 #pragma unroll
-            for (int j = 0; j < T::NI; ++j) acc[i][j] = mfma<FMT, 0>(a0[i], b0[j], acc[i][j], sa[i], sb[j]);
-        int ta[T::MI], tb[T::NI];
-#pragma unroll
-        for (int i = 0; i < T::MI; ++i) ta[i] = sa[i];
-#pragma unroll
-        for (int j = 0; j < T::NI; ++j) tb[j] = sb[j];
-        if (t + 1 < n) {
-            wait_stages_and_barrier<T::D>(min(NS - 2, n - 2 - t));  // stage t + 1 is there, stage t read
-            if (t + NS < n) issue(t + NS);
-            const uint8_t* next = smem + (t + 1) % NS * T::STAGE;
-            read_a(a0, next, 0);
-            read_b(b0, next, 0);
-            read_s(sa, sb, next);
-        }
-#pragma unroll
-        for (int i = 0; i < T::MI; ++i)
-#pragma unroll
-            for (int j = 0; j < T::NI; ++j) acc[i][j] = mfma<FMT, 1>(a1[i], b1[j], acc[i][j], ta[i], tb[j]);
-    }
+    for (int i = 0; i < FRAGS; ++i) read1(i, f0, smem, 0);
+    read_scales(sc, smem);
+    int t = 0;
+    for (; t < n - NS; ++t) step(t, std::true_type{}, std::true_type{}, std::integral_constant<int, NS - 2>{});
+    step(t++, std::true_type{}, std::false_type{}, std::integral_constant<int, NS - 2>{});
+    auto tail = [&](auto i) {
+        constexpr int later = NS - 2 - decltype(i)::value;
+        if (t < n) step(t++, std::false_type{}, std::false_type{}, std::integral_constant<int, (later > 0 ? later : 0)>{});
+    };
+    tail(std::integral_constant<int, 1>{});
+    if constexpr (NS > 2) tail(std::integral_constant<int, 2>{});
+    if constexpr (NS > 3) tail(std::integral_constant<int, 3>{});
 
     // ---- outputs: weight rows are laid so that lane r of blocks 2b and 2b + 1 holds outputs 2r and 2r + 1 of their 64
     float* part = g.partial + (int64_t)z * g.M * partial_columns(g);
@@ -301,11 +338,14 @@ __global__ __launch_bounds__(kThreads) void join_kernel(Args g) {
     store2(g, row, col + 2, v[2], v[3]);
 }
 
-// Rows of scales as whole words, zeros behind the last column.
-__global__ __launch_bounds__(kThreads) void pad_scales_kernel(const uint8_t* sf, int M, int blocks, int KT, uint32_t* out) {
+// Scales of x by K-step, [M/64][KT][64 rows][4 B], zeros behind the last column: what a tile loads of a K-step is then
+// whole lines.
+__global__ __launch_bounds__(kThreads) void tile_scales_kernel(const uint8_t* sf, int M, int blocks, int KT, uint32_t* out) {
     const int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
-    if (i >= (int64_t)M * KT) return;
-    const int64_t row = i / KT, kt = i % KT;
+    const int64_t band = i / (64 * KT);
+    const int kt = (int)(i % (64 * KT) / 64);
+    const int64_t row = band * 64 + i % 64;
+    if (row >= M) return;
     uint32_t v = 0;
     for (int b = 0; b < 4; ++b)
         if (kt * 4 + b < blocks) v |= (uint32_t)sf[row * blocks + kt * 4 + b] << (8 * b);
@@ -332,8 +372,8 @@ MxLinearChoice choose_mx_linear(int M, int N, int K, int format) {
     const int64_t tiles = (((int64_t)M + c.tokens - 1) / c.tokens) * (((int64_t)N + c.columns - 1) / c.columns);
     c.splits = 1;
     while (tiles * c.splits < kFillTiles && KT / (c.splits * 2) >= 4 && c.splits < 16) c.splits *= 2;
-    c.pad_scales = K % 128 != 0;
-    c.scale_bytes = c.pad_scales ? align_up((size_t)M * KT * 4, kAlign) : 0;
+    c.tile_scales = K % kStep != 0 || c.kernel == 0;
+    c.scale_bytes = c.tile_scales ? ((size_t)M + 63) / 64 * KT * 256 : 0;
     c.partial_bytes = c.splits > 1 ? (size_t)c.splits * M * mx_column_blocks(N) * 32 * 4 : 0;
     return c;
 }
@@ -362,13 +402,18 @@ hipError_t launch_mx_linear(const MxLinearArgs& a, const MxLinearChoice& c, hipS
     g.x_row = a.K / per16;
     g.tail = (a.K - (g.KT - 1) * kStep) / per16;
     g.sf = a.x_sf;
+    g.sf_band = (int64_t)a.K / 32 * 64;
     g.sf_row = a.K / 32;
+    g.sf_step = 4;
     g.partial = reinterpret_cast<float*>(a.ws + c.scale_bytes);
-    if (c.pad_scales) {
+    if (c.tile_scales) {
         g.sf = a.ws;
-        g.sf_row = g.KT * 4;
-        hipLaunchKernelGGL(pad_scales_kernel, wide_grid(((int64_t)a.M * g.KT + kThreads - 1) / kThreads), dim3(kThreads), 0,
-                           stream, a.x_sf, a.M, a.K / 32, g.KT, reinterpret_cast<uint32_t*>(a.ws));
+        g.sf_band = (int64_t)g.KT * 256;
+        g.sf_row = 4;
+        g.sf_step = 256;
+        const int64_t words = ((int64_t)a.M + 63) / 64 * 64 * g.KT;
+        hipLaunchKernelGGL(tile_scales_kernel, wide_grid((words + kThreads - 1) / kThreads), dim3(kThreads), 0, stream, a.x_sf,
+                           a.M, a.K / 32, g.KT, reinterpret_cast<uint32_t*>(a.ws));
     }
     g.splits = c.splits;
     g.per = (g.KT + c.splits - 1) / c.splits;
@@ -376,8 +421,8 @@ hipError_t launch_mx_linear(const MxLinearArgs& a, const MxLinearChoice& c, hipS
     g.mt = (a.M + c.tokens - 1) / c.tokens;
     g.nt = (a.N + c.columns - 1) / c.columns;
     if (c.kernel == 0) {
-        if (a.format == MOE_E2M1) go<MOE_E2M1, 256, 256, 2, 2, 4, 1>(g, stream);
-        else go<MOE_E4M3, 256, 256, 2, 2, 3, 1>(g, stream);
+        if (a.format == MOE_E2M1) go<MOE_E2M1, 256, 256, 2, 4, 4, 2>(g, stream);
+        else go<MOE_E4M3, 256, 256, 2, 4, 3, 2>(g, stream);
     } else {
         if (a.format == MOE_E2M1) go<MOE_E2M1, 128, 128, 2, 2, 4, 2>(g, stream);
         else go<MOE_E4M3, 128, 128, 2, 2, 3, 2>(g, stream);

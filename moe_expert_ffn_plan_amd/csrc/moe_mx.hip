@@ -163,7 +163,7 @@ __global__ __launch_bounds__(kThreads) void tile_codes_kernel(const uint8_t* w, 
                                                               uint8_t* out) {
     const int64_t s = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
     if (s >= slots) return;
-    const int p = (int)(s & 127), c = p >> 2, chunk = (p & 3) ^ ((c >> 1) & 3);
+    const int p = (int)(s & 127), c = p >> 2, chunk = (p & 3) ^ ((c >> 2) & 3);
     const int64_t blk = s >> 7;
     const int kt = (int)(blk % KT);
     const int64_t nb = blk / KT;

@@ -228,7 +228,7 @@ def test_prepared_layout(gpu):
     codes, scales = t[:blocks * KT * 2048].view(blocks, KT, 128, 16), t[blocks * KT * 2048:].view(blocks, KT, 32, 4)
     for b, kt, p in itertools.product(range(blocks), range(KT), range(128)):
         c = p >> 2
-        n, k = 64 * (b // 2) + 2 * c + b % 2, 128 * kt + 32 * ((p & 3) ^ ((c >> 1) & 3))
+        n, k = 64 * (b // 2) + 2 * c + b % 2, 128 * kt + 32 * ((p & 3) ^ ((c >> 2) & 3))
         want = w[n, k // 2:k // 2 + 16] if n < N and k < K else torch.zeros(16, dtype=torch.uint8)
         assert torch.equal(codes[b, kt, p], want)
     for b, kt, c, j in itertools.product(range(blocks), range(KT), range(32), range(4)):
