@@ -15,7 +15,6 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
@@ -25,8 +24,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 struct Sum {
     static __device__ __forceinline__ float of(float a, float b) { return a + b; }
 };
+struct IntSum {  // of ints in their bits
+    static __device__ __forceinline__ float of(float a, float b) { return __int_as_float(__float_as_int(a) + __float_as_int(b)); }
+};
 struct Max {
-    static __device__ __forceinline__ float of(float a, float b) { return fmaxf(a, b); }
+    static __device__ __forceinline__ float of(float a, float b);
 };
 template <class Op, int CTRL>
 __device__ __forceinline__ float with_dpp(float v) {
@@ -47,6 +49,26 @@ __device__ __forceinline__ float over_lanes(float v) {
         v = Op::of(__uint_as_float(r[0]), __uint_as_float(r[1]));
     }
     return v;
+}
+
+template <int L>
+__device__ __forceinline__ int sum_over_lanes(int v) {
+    return __float_as_int(over_lanes<IntSum, L>(__int_as_float(v)));
+}
+
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+
+// Maxima that pass over NaN; fmaxf quiets its operands first, an instruction more for each.
+__device__ __forceinline__ float max2(float a, float b) {
+    float r;
+    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ float Max::of(float a, float b) { return max2(a, b); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
 }
 
 // ---- a row
@@ -87,54 +109,68 @@ __device__ __forceinline__ void load_row(float (&l)[V], const void* base, int64_
 }
 template <int L, int V, bool VEC>
 __device__ __forceinline__ void mask_row(float (&l)[V], int E, int lane) {
+    if (E == L * V) return;
 #pragma unroll
     for (int i = 0; i < V; ++i)
         if (expert_of<L, V, VEC>(lane, i) >= E) l[i] = -INFINITY;
 }
 
-// Scores of a row as shares of their sum.  `top` is the largest logit, +infinity where there is a NaN and -infinity
-// in a padding row, whose shares are 0.  lse: the logarithm of the sum of exponentials (softmax).
-//   softmax: e = exp(l - top)
-//   sigmoid: with a = exp(-|l|), 1 / (1 + a) or a / (1 + a); where all logits are negative both sides of the division
-//            are formed over exp(top), so that shares of tiny scores keep their bits
+// Scores of a row as shares of their sum.  `top` is the largest logit, NaN aside; a padding row has none and shares of 0.
+//   softmax: exp(l - top) as 2^(l log2 e - top log2 e), the difference rounded once: off by 2^-24 |l - top| (1 + 0.2),
+//            for the rounding and for log2 e's; what the rounding of top log2 e does is the same for the whole row
+//   sigmoid: 1 / (1 + 2^(-l log2 e)); where all logits are below -60, exp(l - top) / (1 + exp(l)), which keeps the bits
+//            of the shares of tiny scores
+// A NaN or, with softmax, an infinity makes the sum NaN.  Exponentials below 2^-126 of the largest may be 0.
 struct RowSum {
-    float top, lse, inv;  // inv: 1 over the sum, formed over exp(top)
+    float top, by, sum, inv;  // by: top log2 e, or 0; inv: 1 over the sum
     bool alive;
+    __device__ __forceinline__ float lse() const {  // softmax alone
+        const float v = fabsf(top) < 0x1p100f ? (by + __builtin_amdgcn_logf(sum)) * kLn2 : top;
+        return alive ? v : 0.0f;
+    }
 };
+__device__ __forceinline__ float sigmoid(float l) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * l));
+}
+__device__ __forceinline__ float exp_over(float l, float top) { return __builtin_amdgcn_exp2f((l - top) * kLog2e); }
+
 template <int SCORE, int L, int V>
 __device__ __forceinline__ RowSum shares(const float (&l)[V], float (&p)[V]) {
     RowSum r;
-    float top = -INFINITY;
+    float top = max2(l[0], l[1]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) top = fmaxf(top, l[i] == l[i] ? l[i] : INFINITY);
+    for (int i = 2; i < V; i += 2) top = max3(top, l[i], l[i + 1]);
     r.top = over_lanes<Max, L>(top);
     r.alive = r.top > -INFINITY;
-    float sum = 0.0f;
-    if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
-        const float by = r.alive ? r.top : 0.0f;
+    if (!r.alive) {  // padding, or NaN beside it
+        bool nan = false;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            p[i] = expf(l[i] - by);
-            sum += p[i];
+        for (int i = 0; i < V; ++i) nan |= l[i] != l[i];
+        r.alive = over_lanes<Max, L>(nan ? 1.0f : 0.0f) > 0.0f;
+    }
+    r.by = r.alive ? r.top * kLog2e : 0.0f;
+    if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
+        if (fabsf(r.top) < 0x1p100f || !r.alive) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(l[i], kLog2e, -r.by));
+        } else {  // top log2 e may be beyond FP32
+#pragma unroll
+            for (int i = 0; i < V; ++i) p[i] = exp_over(l[i], r.top);
         }
     } else {
+        if (r.top > -60.0f || !r.alive) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float a = expf(-fabsf(l[i]));
-            p[i] = (l[i] >= 0.0f ? 1.0f : a) / (1.0f + a);
+            for (int i = 0; i < V; ++i) p[i] = sigmoid(l[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) p[i] = exp_over(l[i], r.top) * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[i] * kLog2e));
         }
-        if (r.top < 0.0f && r.alive) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) p[i] = expf(l[i] - r.top) / (1.0f + expf(l[i]));
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) sum += p[i];
     }
-    sum = over_lanes<Sum, L>(sum);
-    r.lse = SCORE == MOE_SCORE_SOFTMAX && r.alive ? r.top + logf(sum) : 0.0f;
-    r.inv = r.alive ? 1.0f / sum : 0.0f;
+    float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) p[i] *= r.inv;
+    for (int i = 0; i < V; ++i) sum += p[i];
+    r.sum = over_lanes<Sum, L>(sum);
+    r.inv = r.alive ? __builtin_amdgcn_rcpf(r.sum) : 0.0f;
     return r;
 }
 
@@ -166,18 +202,109 @@ struct Slot {  // floats and ints of one part: shares [E], counts [E], then rows
     static __host__ __device__ __forceinline__ int64_t words(int E) { return 2 * (int64_t)E + 2; }
 };
 
+//
+// Few rows are one launch: a workgroup takes a sequence whole and writes its results.
+
+// Waves of a workgroup of the first kernel; their sums, one per expert, stand side by side in LDS.
+template <int V>
+constexpr int kWaves = V > 8 ? 8 : 16;
+
+template <int V>
+struct RowSums {  // in LDS
+    float* share;  // [kWaves][E]
+    int* count;    // [E]
+    int* rows;     // [kWaves]
+    float* z;      // [kWaves]
+    __device__ __forceinline__ RowSums(float* smem, int E)
+        : share(smem), count(reinterpret_cast<int*>(smem + kWaves<V> * E)), rows(count + E),
+          z(reinterpret_cast<float*>(rows + kWaves<V>)) {}
+    static size_t bytes(int E) { return ((size_t)(kWaves<V> + 1) * E + 2 * kWaves<V>) * 4; }
+    __device__ __forceinline__ float share_of(int e, int E) const {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves<V>; ++w) v += share[w * E + e];
+        return v;
+    }
+    __device__ __forceinline__ void row_totals(int& n, float& zz) const {
+        n = 0;
+        zz = 0.0f;
+        for (int w = 0; w < kWaves<V>; ++w) n += rows[w], zz += z[w];
+    }
+};
+
+// Sums of rows [row, end), of the whole workgroup; the caller's next barrier is behind the last read of them.
 template <int TYPE, int SCORE, int L, int V, bool VEC>
-__global__ __launch_bounds__(kThreads) void balance_parts_kernel(BalanceArgs a, int tile, float* parts, uint32_t* tickets) {
-    constexpr int GROUPS = kThreads / L;
-    extern __shared__ float smem[];  // [kWaves][E] shares, [E] counts, [kWaves] rows, [kWaves] z
-    float* wave_share = smem;
-    int* count = reinterpret_cast<int*>(smem + kWaves * a.E);
-    int* wave_rows = count + a.E;
-    float* wave_z = reinterpret_cast<float*>(wave_rows + kWaves);
+__device__ __forceinline__ void sum_rows(const BalanceArgs& a, int row, int end, const RowSums<V>& out) {
+    constexpr int THREADS = kWaves<V> * 64, GROUPS = THREADS / L;
+    constexpr int U = V > 8 ? 1 : 2;  // rows of a group that are loaded together
     const int tid = threadIdx.x, lane = tid % L, group = tid / L, wave = tid / 64;
-    const int b = blockIdx.x;
+    for (int e = tid; e < a.E; e += THREADS) out.count[e] = 0;
+    const int64_t id0 = (int64_t)row * a.k, ids = (int64_t)(end - row) * a.k;
+    const int64_t first_id = tid < ids ? a.topk_idx[id0 + tid] : -1;
+    float acc[V], z = 0.0f;
+    int rows = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+    if (a.logits) {
+        for (int t = row + group; t < end; t += U * GROUPS) {
+            float l[U][V];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                load_row<TYPE, L, V, VEC>(l[u], a.logits, (int64_t)min(t + u * GROUPS, end - 1) * a.stride, a.E, lane);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float p[V];
+                mask_row<L, V, VEC>(l[u], t + u * GROUPS < end ? a.E : 0, lane);
+                const RowSum r = shares<SCORE, L, V>(l[u], p);
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] = fmaf(p[i], r.inv, acc[i]);
+                rows += r.alive;
+                if (SCORE == MOE_SCORE_SOFTMAX && a.z) {
+                    const float lse = r.lse();
+                    z = fmaf(lse, lse, z);
+                }
+            }
+        }
+    }
+    // the groups of a wave, then the waves
+    if constexpr (L < 64) {
+#pragma unroll
+        for (int d = L; d < 64; d *= 2) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] += __shfl_xor(acc[i], d);
+            rows += __shfl_xor(rows, d);
+            z += __shfl_xor(z, d);
+        }
+    }
+    if (tid % 64 < L) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = expert_of<L, V, VEC>(lane, i);
+            if (e < a.E) out.share[wave * a.E + e] = acc[i];
+        }
+        if (lane == 0) {
+            out.rows[wave] = rows;
+            out.z[wave] = z;
+        }
+    }
+    __syncthreads();
+    if (first_id >= 0 && first_id < a.E) atomicAdd(&out.count[first_id], 1);
+    for (int64_t i = tid + THREADS; i < ids; i += THREADS) {
+        const int64_t e = a.topk_idx[id0 + i];
+        if (e >= 0 && e < a.E) atomicAdd(&out.count[e], 1);
+    }
+    __syncthreads();
+}
+
+template <int TYPE, int SCORE, int L, int V, bool VEC>
+__global__ __launch_bounds__(kWaves<V> * 64) void balance_parts_kernel(BalanceArgs a, int tile, float* parts,
+                                                                       uint32_t* tickets) {
+    extern __shared__ float smem[];
+    const RowSums<V> sums(smem, a.E);
+    constexpr int THREADS = kWaves<V> * 64;
+    const int tid = threadIdx.x, b = blockIdx.x;
     if (b == 0)
-        for (int s = tid; s < a.S; s += kThreads) tickets[s] = 0;
+        for (int s = tid; s < a.S; s += THREADS) tickets[s] = 0;
     int row = (int)min((int64_t)b * tile, (int64_t)a.T);
     const int last = min(row + tile, a.T);
     int s = sequence_of(a.seq_offsets, row, a.S, a.T);
@@ -192,65 +319,18 @@ __global__ __launch_bounds__(kThreads) void balance_parts_kernel(BalanceArgs a, 
             ++s;
             continue;
         }
-        for (int e = tid; e < a.E; e += kThreads) count[e] = 0;
-        float acc[V], z = 0.0f;
-        int rows = 0;
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-        if (a.logits) {
-            for (int t = row + group; t < end; t += GROUPS) {
-                float l[V], p[V];
-                load_row<TYPE, L, V, VEC>(l, a.logits, (int64_t)t * a.stride, a.E, lane);
-                mask_row<L, V, VEC>(l, a.E, lane);
-                const RowSum r = shares<SCORE, L, V>(l, p);
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] += p[i];
-                rows += r.alive;
-                z += r.lse * r.lse;
-            }
-        }
-        // the groups of a wave, then the waves
-        if constexpr (L < 64) {
-#pragma unroll
-            for (int d = L; d < 64; d *= 2) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] += __shfl_xor(acc[i], d);
-                rows += __shfl_xor(rows, d);
-                z += __shfl_xor(z, d);
-            }
-        }
-        if (tid % 64 < L) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = expert_of<L, V, VEC>(lane, i);
-                if (e < a.E) wave_share[wave * a.E + e] = acc[i];
-            }
-            if (lane == 0) {
-                wave_rows[wave] = rows;
-                wave_z[wave] = z;
-            }
-        }
-        __syncthreads();
-        const int64_t id0 = (int64_t)row * a.k, ids = (int64_t)(end - row) * a.k;
-        for (int64_t i = tid; i < ids; i += kThreads) {
-            const int64_t e = a.topk_idx[id0 + i];
-            if (e >= 0 && e < a.E) atomicAdd(&count[e], 1);
-        }
-        __syncthreads();
+        sum_rows<TYPE, SCORE, L, V, VEC>(a, row, end, sums);
         float* out = parts + (int64_t)(b + s) * Slot::words(a.E);
-        for (int e = tid; e < a.E; e += kThreads) {
-            float v = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) v += wave_share[w * a.E + e];
-            out[e] = v;
-            reinterpret_cast<int*>(out)[a.E + e] = count[e];
+        for (int e = tid; e < a.E; e += THREADS) {
+            out[e] = sums.share_of(e, a.E);
+            reinterpret_cast<int*>(out)[a.E + e] = sums.count[e];
         }
         if (tid == 0) {
-            int n = 0;
-            float v = 0.0f;
-            for (int w = 0; w < kWaves; ++w) n += wave_rows[w], v += wave_z[w];
+            int n;
+            float z;
+            sums.row_totals(n, z);
             reinterpret_cast<int*>(out)[2 * a.E] = n;
-            out[2 * a.E + 1] = v;
+            out[2 * a.E + 1] = z;
         }
         __syncthreads();
         row = end;
@@ -258,15 +338,58 @@ __global__ __launch_bounds__(kThreads) void balance_parts_kernel(BalanceArgs a, 
     }
 }
 
+// A sequence whole.
+template <int TYPE, int SCORE, int L, int V, bool VEC>
+__global__ __launch_bounds__(kWaves<V> * 64) void balance_whole_kernel(BalanceArgs a) {
+    extern __shared__ float smem[];
+    __shared__ float cross_part[kWaves<V>];
+    __shared__ int count_part[kWaves<V>];
+    const RowSums<V> sums(smem, a.E);
+    constexpr int THREADS = kWaves<V> * 64;
+    const int tid = threadIdx.x;
+    const int64_t s = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (s >= a.S) return;
+    const int from = offset_at(a.seq_offsets, (int)s, a.T), to = max(from, offset_at(a.seq_offsets, (int)s + 1, a.T));
+    sum_rows<TYPE, SCORE, L, V, VEC>(a, from, to, sums);
+    int n;
+    float z;
+    sums.row_totals(n, z);
+    float cross = 0.0f;
+    int total = 0;
+    for (int e = tid; e < a.E; e += THREADS) {
+        const int count = sums.count[e];
+        const float share = n > 0 ? sums.share_of(e, a.E) / (float)n : 0.0f;
+        if (a.counts) a.counts[s * a.E + e] = count;
+        if (a.share) a.share[s * a.E + e] = share;
+        if (count > 0) cross += (float)count * share;
+        total += count;
+    }
+    if (tid == 0) {
+        if (a.rows) a.rows[s] = n;
+        if (a.z) a.z[s] = n > 0 ? z / (float)n : 0.0f;
+    }
+    if (!a.loss) return;
+    cross = over_lanes<Sum, 64>(cross);
+    total = sum_over_lanes<64>(total);
+    if (tid % 64 == 0) {
+        cross_part[tid / 64] = cross;
+        count_part[tid / 64] = total;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 1; w < kWaves<V>; ++w) cross += cross_part[w], total += count_part[w];
+        a.loss[s] = total > 0 ? (float)a.E * cross / (float)total : 0.0f;
+    }
+}
+
 // One workgroup per sequence and kColumns experts; the last of a sequence to arrive adds up the loss.
-constexpr int kColumns = 32;
-__global__ __launch_bounds__(kThreads) void balance_join_kernel(BalanceArgs a, int tile, const float* parts,
-                                                                uint32_t* tickets, float* sums) {
-    constexpr int LANES = kThreads / kColumns;
-    __shared__ float share_part[LANES][kColumns], z_part[LANES];
-    __shared__ int count_part[LANES][kColumns];
-    __shared__ int rows_part[LANES];
-    __shared__ bool is_last;
+constexpr int kColumns = 32, kJoinThreads = 1024;
+static_assert(kMaxGateExperts / kColumns <= 64, "a lane for each of a sequence's workgroups");
+__global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs a, int tile, const float* parts,
+                                                                    uint32_t* tickets, float* sums) {
+    __shared__ float share_part[kJoinThreads / kColumns][kColumns], z_part[kJoinThreads / kColumns];
+    __shared__ int count_part[kJoinThreads / kColumns][kColumns], rows_part[kJoinThreads / kColumns];
+    const int LANES = blockDim.x / kColumns;
     const int chunks = (a.E + kColumns - 1) / kColumns;
     const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     if (block >= (int64_t)chunks * a.S) return;
@@ -278,14 +401,16 @@ __global__ __launch_bounds__(kThreads) void balance_join_kernel(BalanceArgs a, i
     int count = 0, rows = 0;
     if (to > from) {
         const int first = from / tile, end = (to - 1) / tile + 1;
+        const int at = min(e, a.E - 1);
+#pragma unroll 4
         for (int b = first + part; b < end; b += LANES) {
             const float* in = parts + (int64_t)(b + s) * words;
-            if (e < a.E) {
-                share += in[e];
-                count += reinterpret_cast<const int*>(in)[a.E + e];
+            share += in[at];
+            count += reinterpret_cast<const int*>(in)[a.E + at];
+            if (col == 0) {
+                rows += reinterpret_cast<const int*>(in)[2 * a.E];
+                z += in[2 * a.E + 1];
             }
-            rows += reinterpret_cast<const int*>(in)[2 * a.E];
-            z += in[2 * a.E + 1];
         }
     }
     share_part[part][col] = share;
@@ -295,58 +420,59 @@ __global__ __launch_bounds__(kThreads) void balance_join_kernel(BalanceArgs a, i
         z_part[part] = z;
     }
     __syncthreads();
-    float cross = 0.0f;  // counts times shares, and counts, of this workgroup's experts
-    int total = 0;
-    if (threadIdx.x < 64) {  // one wave, whose lanes past the columns add nothing
-        share = z = 0.0f;
-        count = rows = 0;
-        for (int q = 0; q < LANES; ++q) {
-            if (threadIdx.x < kColumns) {
-                share += share_part[q][col];
-                count += count_part[q][col];
-            }
-            rows += rows_part[q];
-            z += z_part[q];
-        }
-        share = rows > 0 ? share / (float)rows : 0.0f;
-        if (threadIdx.x < kColumns && e < a.E) {
-            if (a.counts) a.counts[(int64_t)s * a.E + e] = count;
-            if (a.share) a.share[(int64_t)s * a.E + e] = share;
-        }
-        if (chunk == 0 && threadIdx.x == 0) {
-            if (a.rows) a.rows[s] = rows;
-            if (a.z) a.z[s] = rows > 0 ? z / (float)rows : 0.0f;
-        }
-        cross = over_lanes<Sum, 64>(count > 0 ? (float)count * share : 0.0f);
-        total = count;
-        for (int d = 1; d < 64; d *= 2) total += __shfl_xor(total, d);
+    if (threadIdx.x >= 64) return;
+    // one wave: its halves add the even and the odd parts of the columns
+    rows = (int)threadIdx.x < LANES ? rows_part[threadIdx.x] : 0;
+    z = (int)threadIdx.x < LANES ? z_part[threadIdx.x] : 0.0f;
+    rows = sum_over_lanes<64>(rows);
+    z = over_lanes<Sum, 64>(z);
+    share = 0.0f;
+    count = 0;
+#pragma unroll 4
+    for (int q = part; q < LANES; q += 2) {
+        share += share_part[q][col];
+        count += count_part[q][col];
+    }
+    share += __shfl_xor(share, kColumns);
+    count += __shfl_xor(count, kColumns);
+    share = rows > 0 ? share / (float)rows : 0.0f;
+    const bool mine = threadIdx.x < kColumns && e < a.E;
+    if (mine) {
+        if (a.counts) a.counts[(int64_t)s * a.E + e] = count;
+        if (a.share) a.share[(int64_t)s * a.E + e] = share;
+    }
+    if (chunk == 0 && threadIdx.x == 0) {
+        if (a.rows) a.rows[s] = rows;
+        if (a.z) a.z[s] = rows > 0 ? z / (float)rows : 0.0f;
     }
     if (!a.loss) return;
-    float* mine = sums + ((int64_t)s * chunks + chunk) * 2;
+    const float cross = over_lanes<Sum, 64>(mine && count > 0 ? (float)count * share : 0.0f);
+    const int total = sum_over_lanes<64>(mine ? count : 0);
+    float* out = sums + ((int64_t)s * chunks + chunk) * 2;
+    uint32_t before = 0;
     if (threadIdx.x == 0) {
-        __hip_atomic_store(mine, cross, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __hip_atomic_store(mine + 1, __int_as_float(total), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        is_last = __hip_atomic_fetch_add(&tickets[s], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-                  (uint32_t)chunks - 1;
-        if (is_last) {
-            const float* all = sums + (int64_t)s * chunks * 2;
-            float v = 0.0f;
-            int64_t n = 0;
-            for (int c = 0; c < chunks; ++c) {
-                v += __hip_atomic_load(all + 2 * c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                n += __float_as_int(__hip_atomic_load(all + 2 * c + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-            }
-            a.loss[s] = n > 0 ? (float)a.E * v / (float)n : 0.0f;
-        }
+        __hip_atomic_store(out, cross, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(out + 1, __int_as_float(total), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        before = __hip_atomic_fetch_add(&tickets[s], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
     }
+    if (__builtin_amdgcn_readfirstlane(before) != (uint32_t)chunks - 1) return;
+    const float* all = sums + ((int64_t)s * chunks + min((int)threadIdx.x, chunks - 1)) * 2;
+    const float part_cross = __hip_atomic_load(all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int part_total = __float_as_int(__hip_atomic_load(all + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    const bool has = (int)threadIdx.x < chunks;
+    const float v = over_lanes<Sum, 64>(has ? part_cross : 0.0f);
+    const int n = sum_over_lanes<64>(has ? part_total : 0);
+    if (threadIdx.x == 0) a.loss[s] = n > 0 ? (float)a.E * v / (float)n : 0.0f;
 }
 
-// Rows of a tile: enough tiles to fill the GPU, and no more parts than the second kernel can add quickly.
+// Rows of a tile: a tile for every compute unit, and no more parts than the second kernel can add quickly.
 int tile_rows(int T) {
     int tile = 16;
-    while (tile < 1024 && (int64_t)tile * 512 < T) tile *= 2;
+    while (tile < 1024 && (int64_t)tile * 256 < T) tile *= 2;
     return tile;
 }
+// Few enough rows for one launch: no sequence has more.
+constexpr int kWholeRows = 512;
 
 struct BalanceLayout {
     int tile, tiles;
@@ -355,7 +481,7 @@ struct BalanceLayout {
 BalanceLayout balance_layout(int T, int E, int S) {
     BalanceLayout l;
     l.tile = tile_rows(T);
-    l.tiles = T > 0 ? (T + l.tile - 1) / l.tile : 1;  // the first one clears the tickets
+    l.tiles = (T + l.tile - 1) / l.tile;
     size_t o = 0;
     auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, kAlign); return at; };
     l.parts = take((size_t)((int64_t)l.tiles + S) * Slot::words(E) * 4);
@@ -374,18 +500,22 @@ BalanceLayout balance_layout(int T, int E, int S) {
 // z adds p * 2 lse d_z / rows.  The weights w = scale * r, r = s over the sum of the chosen (or s), add at the chosen
 //   renormalised:  softmax  scale r (d - m),  sigmoid  scale r (1 - s) (d - m),  m = sum of r d
 //   else:          softmax  scale p d, and -p * (sum of scale p d) at every expert;  sigmoid  scale s (1 - s) d
-constexpr int kRowsPerGroup = 4;
-
 template <int TYPE, int SCORE, int L, int V, bool VEC, int KV>
-__global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a) {
+__global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int rows_per_group) {
     constexpr int GROUPS = kThreads / L;
+    // what a group's row adds at the experts it chose, by expert; zeros between rows.  A group's lanes are of one wave,
+    // whose LDS instructions are done in their order, and an instruction's additions to one place in the lanes' order.
+    __shared__ __attribute__((aligned(16))) float chosen_sums[GROUPS][L * V];
+    float* own = chosen_sums[threadIdx.x / L];
     const int lane = threadIdx.x % L;
-    const int64_t first = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * GROUPS * kRowsPerGroup + threadIdx.x / L;
+#pragma unroll
+    for (int i = 0; i < V; ++i) own[lane + L * i] = 0.0f;
+    const int64_t first = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * GROUPS * rows_per_group + threadIdx.x / L;
     int s = -2, begin = 0, end = 0;  // the sequence of the last row, and its rows
     float pull[V], zpull = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) pull[i] = 0.0f;
-    for (int step = 0; step < kRowsPerGroup; ++step) {
+    for (int step = 0; step < rows_per_group; ++step) {
         const int64_t t = first + (int64_t)step * GROUPS;
         if (t >= a.T) break;
         if (s == -2 || t < begin || t >= end) {
@@ -395,15 +525,15 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a) {
             if (s < 0 || s >= a.S) continue;
             const float n = a.rows ? (float)a.rows[s] : 0.0f;
             if (a.d_loss) {
-                int64_t total = 0;
-                int c[V];
+                int c[V], low = 0, high = 0;  // halves of the sum, which may pass 32 bits
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const int e = expert_of<L, V, VEC>(lane, i);
                     c[i] = e < a.E ? a.counts[(int64_t)s * a.E + e] : 0;
-                    total += c[i];
+                    low += c[i] & 0xFFFF;
+                    high += c[i] >> 16;
                 }
-                for (int d = 1; d < L; d *= 2) total += __shfl_xor(total, d);
+                const int64_t total = ((int64_t)sum_over_lanes<L>(high) << 16) + sum_over_lanes<L>(low);
                 const float by = n > 0.0f && total != 0 ? a.d_loss[s] / n / (float)total : 0.0f;
 #pragma unroll
                 for (int i = 0; i < V; ++i) pull[i] = by * (float)((int64_t)c[i] * a.E - total);
@@ -428,79 +558,75 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a) {
         }
         mask_row<L, V, VEC>(l, a.E, lane);
         const RowSum r = shares<SCORE, L, V>(l, p);
-        float mean = 0.0f;
+        float common = 0.0f;  // what falls on every expert by its share
+        if (a.d_loss) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) mean += p[i] * pull[i];
-        mean = over_lanes<Sum, L>(mean);
-        float g[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            g[i] = p[i] * (pull[i] - mean + (SCORE == MOE_SCORE_SOFTMAX ? zpull * r.lse : 0.0f));
-            if constexpr (SCORE == MOE_SCORE_SIGMOID) {
-                const float x = expf(-fabsf(l[i]));
-                g[i] *= (l[i] >= 0.0f ? x : 1.0f) / (1.0f + x);
-            }
+            for (int i = 0; i < V; ++i) common = fmaf(p[i], pull[i], common);
+            common = -over_lanes<Sum, L>(common) * r.inv;
         }
+        if (SCORE == MOE_SCORE_SOFTMAX && a.d_z) common = fmaf(zpull, r.lse(), common);
+        bool chosen = false;
         if (a.d_topk_w) {
             float w[KV], rest[KV];  // r and, of sigmoid scores, 1 - s
             float top = -INFINITY;
+            if (a.renorm) {
 #pragma unroll
-            for (int q = 0; q < KV; ++q) top = fmaxf(top, lk[q] == lk[q] ? lk[q] : INFINITY);
-            if (a.renorm) top = over_lanes<Max, L>(top);
-            const float by = SCORE == MOE_SCORE_SIGMOID ? (a.renorm ? fminf(top, 0.0f) : 0.0f) : a.renorm ? top : r.top;
+                for (int q = 0; q < KV; ++q) top = max2(top, lk[q]);
+                top = over_lanes<Max, L>(top);
+            }
             float sum = 0.0f;
 #pragma unroll
             for (int q = 0; q < KV; ++q) {
-                const bool ok = id[q] >= 0 && lk[q] != -INFINITY;
                 if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
-                    w[q] = ok ? expf(lk[q] - by) : 0.0f;
+                    w[q] = exp_over(lk[q], a.renorm ? top : r.top);
                     rest[q] = 1.0f;
                 } else {
-                    const float x = expf(-fabsf(lk[q]));
-                    w[q] = ok ? (lk[q] >= 0.0f ? 1.0f : expf(lk[q] - by)) / (1.0f + x) : 0.0f;
-                    rest[q] = (lk[q] >= 0.0f ? x : 1.0f) / (1.0f + x);
+                    // over exp(top) where all are small, as in shares()
+                    w[q] = a.renorm && top < -60.0f ? exp_over(lk[q], top) : sigmoid(lk[q]);
+                    rest[q] = sigmoid(-lk[q]);
                 }
+                if (lk[q] == -INFINITY) w[q] = 0.0f;  // none, or masked
                 sum += w[q];
             }
+            float m = 0.0f;
             if (a.renorm) {
                 sum = over_lanes<Sum, L>(sum);
-                const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-                float m = 0.0f;
+                const float inv = sum != 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
 #pragma unroll
                 for (int q = 0; q < KV; ++q) {
                     w[q] *= inv;
-                    m += w[q] * dw[q];
+                    m = fmaf(w[q], dw[q], m);
                 }
                 m = over_lanes<Sum, L>(m);
-#pragma unroll
-                for (int q = 0; q < KV; ++q) w[q] *= (dw[q] - m) * rest[q];
             } else if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
-                float m = 0.0f;
+                float all = 0.0f;
 #pragma unroll
                 for (int q = 0; q < KV; ++q) {
-                    w[q] *= r.inv * dw[q];
-                    m += w[q];
+                    w[q] *= r.inv;
+                    all = fmaf(w[q], dw[q], all);
                 }
-                m = over_lanes<Sum, L>(m);
-#pragma unroll
-                for (int i = 0; i < V; ++i) g[i] -= p[i] * m;
-            } else {
-#pragma unroll
-                for (int q = 0; q < KV; ++q) w[q] *= dw[q] * rest[q];
+                common -= over_lanes<Sum, L>(all);
             }
-            for (int j = 0; j < a.k; ++j) {  // in the order of j: an id that occurs twice adds twice
-                int e = 0;
-                float v = 0.0f;
+            chosen = true;
 #pragma unroll
-                for (int q = 0; q < KV; ++q)
-                    if (j / L == q) {
-                        e = __shfl(id[q], j % L, L);
-                        v = __shfl(w[q], j % L, L);
-                    }
+            for (int q = 0; q < KV; ++q)
+                if (id[q] >= 0) atomicAdd(&own[id[q]], w[q] * (dw[q] - m) * rest[q]);
+        }
+        float g[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (expert_of<L, V, VEC>(lane, i) == e) g[i] += v;
+        for (int i = 0; i < V; ++i) {
+            g[i] = p[i] * r.inv * (pull[i] + common);
+            if constexpr (SCORE == MOE_SCORE_SIGMOID) g[i] *= sigmoid(-l[i]);
+        }
+        if (chosen) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = expert_of<L, V, VEC>(lane, i);
+                if (VEC || e < a.E) g[i] += own[e];
             }
+#pragma unroll
+            for (int q = 0; q < KV; ++q)
+                if (id[q] >= 0) own[id[q]] = 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -540,15 +666,22 @@ bool vector_rows(const void* base, int64_t stride, int E, int type) {
 
 template <int TYPE, int SCORE, int L, int V, bool VEC>
 void parts_go(const BalanceArgs& a, const BalanceLayout& l, char* ws, hipStream_t stream) {
-    const size_t lds = ((size_t)(kWaves + 1) * a.E + 2 * kWaves) * 4;
-    hipLaunchKernelGGL((balance_parts_kernel<TYPE, SCORE, L, V, VEC>), dim3((unsigned)l.tiles), dim3(kThreads), lds, stream,
-                       a, l.tile, reinterpret_cast<float*>(ws + l.parts), reinterpret_cast<uint32_t*>(ws + l.tickets));
+    const size_t lds = RowSums<V>::bytes(a.E);
+    if (a.T <= kWholeRows)
+        hipLaunchKernelGGL((balance_whole_kernel<TYPE, SCORE, L, V, VEC>), wide_grid(a.S), dim3(kWaves<V> * 64), lds, stream, a);
+    else
+        hipLaunchKernelGGL((balance_parts_kernel<TYPE, SCORE, L, V, VEC>), dim3((unsigned)l.tiles), dim3(kWaves<V> * 64), lds,
+                           stream, a, l.tile, reinterpret_cast<float*>(ws + l.parts),
+                           reinterpret_cast<uint32_t*>(ws + l.tickets));
 }
 template <int TYPE, int SCORE, int L, int V, bool VEC, int KV>
 void grad_go(const GateGradArgs& a, hipStream_t stream) {
-    const int rows = kThreads / L * kRowsPerGroup;
+    // rows side by side while there are workgroups to have, then several to a group, which load a sequence's counts once
+    int per = 1;
+    while (per < 8 && (int64_t)kThreads / L * per * 4096 < a.T) per *= 2;
+    const int rows = kThreads / L * per;
     hipLaunchKernelGGL((gate_grad_kernel<TYPE, SCORE, L, V, VEC, KV>), wide_grid(((int64_t)a.T + rows - 1) / rows),
-                       dim3(kThreads), 0, stream, a);
+                       dim3(kThreads), 0, stream, a, per);
 }
 
 // f(type, score, lanes, values, vector loads, chosen ids per lane) as compile-time constants
@@ -557,9 +690,10 @@ using Int = std::integral_constant<int, N>;
 template <class F>
 void with_lanes(int E, F f) {
     if (E <= 32) f(Int<8>{}, Int<4>{}, Int<4>{});
-    else if (E <= 64) f(Int<16>{}, Int<4>{}, Int<4>{});
-    else if (E <= 128) f(Int<32>{}, Int<4>{}, Int<2>{});
-    else if (E <= 256) f(Int<64>{}, Int<4>{}, Int<1>{});
+    else if (E <= 64) f(Int<8>{}, Int<8>{}, Int<8>{});
+    else if (E <= 128) f(Int<16>{}, Int<8>{}, Int<4>{});
+    else if (E <= 256) f(Int<32>{}, Int<8>{}, Int<2>{});
+    else if (E <= 384) f(Int<32>{}, Int<12>{}, Int<2>{});
     else if (E <= 512) f(Int<64>{}, Int<8>{}, Int<1>{});
     else f(Int<64>{}, Int<16>{}, Int<1>{});
 }
@@ -592,8 +726,11 @@ hipError_t launch_balance(const BalanceArgs& a, void* ws, hipStream_t stream) {
              });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    if (a.T <= kWholeRows) return hipSuccess;
     const int chunks = (a.E + kColumns - 1) / kColumns;
-    hipLaunchKernelGGL(balance_join_kernel, wide_grid((int64_t)chunks * a.S), dim3(kThreads), 0, stream, a, l.tile,
+    // lanes for the parts that a sequence has if all are as long
+    const int threads = l.tiles / a.S >= 16 ? kJoinThreads : kThreads;
+    hipLaunchKernelGGL(balance_join_kernel, wide_grid((int64_t)chunks * a.S), dim3((unsigned)threads), 0, stream, a, l.tile,
                        reinterpret_cast<const float*>(base + l.parts), reinterpret_cast<uint32_t*>(base + l.tickets),
                        reinterpret_cast<float*>(base + l.sums));
     return hipGetLastError();
