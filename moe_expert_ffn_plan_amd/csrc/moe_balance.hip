@@ -72,31 +72,29 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // ---- a row
-template <int TYPE>
-__device__ __forceinline__ float load1(const void* base, int64_t i) {
-    if constexpr (TYPE == MOE_F32) return static_cast<const float*>(base)[i];
-    else return __uint_as_float((uint32_t)static_cast<const uint16_t*>(base)[i] << 16);
-}
-
 template <int L, int V, bool VEC>
 __device__ __forceinline__ int expert_of(int lane, int i) {
     return VEC ? 4 * (lane + L * (i / 4)) + i % 4 : lane + L * i;
 }
 
-// The logits of one row; -infinity past the last expert.
+// The logits of the row at `row`; -infinity past the last expert, or everywhere where the row is not to be had.
 template <int TYPE, int L, int V, bool VEC>
-__device__ __forceinline__ void load_row(float (&l)[V], const void* base, int64_t at, int E, int lane) {
+__device__ __forceinline__ void load_row(float (&l)[V], const char* row, int E, int lane, bool valid = true) {
+    constexpr int SIZE = TYPE == MOE_F32 ? 4 : 2;
+    row += (VEC ? 4 : 1) * lane * SIZE;
     if constexpr (VEC) {
 #pragma unroll
         for (int i = 0; i < V; i += 4) {
-            const int e = 4 * (lane + L * (i / 4));
-            const int64_t from = at + (e < E ? e : 0);
+            const char* at = row + L * i * SIZE;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) l[i + j] = -INFINITY;
+            if (!valid || expert_of<L, V, VEC>(lane, i) >= E) continue;
             if constexpr (TYPE == MOE_F32) {
-                const v4f v = *reinterpret_cast<const v4f*>(static_cast<const float*>(base) + from);
+                const v4f v = *reinterpret_cast<const v4f*>(at);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) l[i + j] = v[j];
             } else {
-                const v2i v = *reinterpret_cast<const v2i*>(static_cast<const uint16_t*>(base) + from);
+                const v2i v = *reinterpret_cast<const v2i*>(at);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     l[i + j] = __uint_as_float(j & 1 ? (uint32_t)v[j / 2] & 0xFFFF0000u : (uint32_t)v[j / 2] << 16);
@@ -104,15 +102,15 @@ __device__ __forceinline__ void load_row(float (&l)[V], const void* base, int64_
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) l[i] = load1<TYPE>(base, at + min(lane + L * i, E - 1));
+        for (int i = 0; i < V; ++i) {
+            l[i] = -INFINITY;
+            if (valid && expert_of<L, V, VEC>(lane, i) < E) {
+                const char* at = row + L * i * SIZE;
+                if constexpr (TYPE == MOE_F32) l[i] = *reinterpret_cast<const float*>(at);
+                else l[i] = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(at) << 16);
+            }
+        }
     }
-}
-template <int L, int V, bool VEC>
-__device__ __forceinline__ void mask_row(float (&l)[V], int E, int lane) {
-    if (E == L * V) return;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (expert_of<L, V, VEC>(lane, i) >= E) l[i] = -INFINITY;
 }
 
 // Scores of a row as shares of their sum.  `top` is the largest logit, NaN aside; a padding row has none and shares of 0.
@@ -192,6 +190,30 @@ __device__ __forceinline__ int sequence_of(const int64_t* off, int row, int S, i
     return lo - 1;
 }
 
+// The same of one row for a whole wave, which compares 64 offsets at a time.
+__device__ __forceinline__ int sequence_of_wave(const int64_t* off, int row, int S, int T) {
+    if (!off) return 0;
+    const int lane = threadIdx.x % 64;
+    int lo = 0, n = S + 1;  // the offsets in question
+    while (n > 0) {
+        const int step = (n + 63) / 64, at = lane * step;
+        const bool before = at < n && offset_at(off, lo + at, T) <= row;
+        const int c = __popcll(__ballot(before));
+        if (c == 0) break;
+        lo += (c - 1) * step + 1;
+        n = min(step - 1, n - (c - 1) * step - 1);
+    }
+    return lo - 1;
+}
+// The sequence of a row at or behind sequence s's first: often s or the next one.
+__device__ __forceinline__ int sequence_from(const int64_t* off, int s, int row, int S, int T) {
+    for (int i = 0; i < 3; ++i) {
+        if (s >= S || row < offset_at(off, s + 1, T)) return s;
+        ++s;
+    }
+    return sequence_of(off, row, S, T);
+}
+
 // ---- forward: sums of a tile's rows, then sums of the tiles
 //
 // Tiles of `tile` rows, whatever the sequences.  The part of sequence s in tile b goes to slot b + s: from one part to
@@ -246,15 +268,16 @@ __device__ __forceinline__ void sum_rows(const BalanceArgs& a, int row, int end,
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
     if (a.logits) {
+        const char* base = static_cast<const char*>(a.logits);
+        const int64_t pitch = a.stride * (TYPE == MOE_F32 ? 4 : 2);
         for (int t = row + group; t < end; t += U * GROUPS) {
             float l[U][V];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                load_row<TYPE, L, V, VEC>(l[u], a.logits, (int64_t)min(t + u * GROUPS, end - 1) * a.stride, a.E, lane);
+                load_row<TYPE, L, V, VEC>(l[u], base + (int64_t)(t + u * GROUPS) * pitch, a.E, lane, t + u * GROUPS < end);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 float p[V];
-                mask_row<L, V, VEC>(l[u], t + u * GROUPS < end ? a.E : 0, lane);
                 const RowSum r = shares<SCORE, L, V>(l[u], p);
 #pragma unroll
                 for (int i = 0; i < V; ++i) acc[i] = fmaf(p[i], r.inv, acc[i]);
@@ -307,7 +330,7 @@ __global__ __launch_bounds__(kWaves<V> * 64) void balance_parts_kernel(BalanceAr
         for (int s = tid; s < a.S; s += THREADS) tickets[s] = 0;
     int row = (int)min((int64_t)b * tile, (int64_t)a.T);
     const int last = min(row + tile, a.T);
-    int s = sequence_of(a.seq_offsets, row, a.S, a.T);
+    int s = sequence_of_wave(a.seq_offsets, row, a.S, a.T);
     while (row < last && s < a.S) {
         if (s < 0) {  // rows in front of the first sequence
             row = max(row, offset_at(a.seq_offsets, 0, a.T));
@@ -402,7 +425,7 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs 
     if (to > from) {
         const int first = from / tile, end = (to - 1) / tile + 1;
         const int at = min(e, a.E - 1);
-#pragma unroll 4
+#pragma unroll 8
         for (int b = first + part; b < end; b += LANES) {
             const float* in = parts + (int64_t)(b + s) * words;
             share += in[at];
@@ -502,25 +525,55 @@ BalanceLayout balance_layout(int T, int E, int S) {
 //   else:          softmax  scale p d, and -p * (sum of scale p d) at every expert;  sigmoid  scale s (1 - s) d
 template <int TYPE, int SCORE, int L, int V, bool VEC, int KV>
 __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int rows_per_group) {
-    constexpr int GROUPS = kThreads / L;
-    // what a group's row adds at the experts it chose, by expert; zeros between rows.  A group's lanes are of one wave,
-    // whose LDS instructions are done in their order, and an instruction's additions to one place in the lanes' order.
-    __shared__ __attribute__((aligned(16))) float chosen_sums[GROUPS][L * V];
-    float* own = chosen_sums[threadIdx.x / L];
-    const int lane = threadIdx.x % L;
+    constexpr int GROUPS = kThreads / L, SIZE = TYPE == MOE_F32 ? 4 : 2;
+    // What a group's row adds at the experts it chose, by expert (zeros between rows), and the row's scores (softmax) or
+    // logits for its chosen experts to be read from.  A group's lanes are of one wave, whose LDS instructions are done in
+    // their order, and an instruction's additions to one place in the lanes' order.
+    __shared__ __attribute__((aligned(16))) float sums_of_rows[GROUPS][L * V], row_of_group[GROUPS][L * V];
+    const int lane = threadIdx.x % L, group = threadIdx.x / L;
+    float* own = sums_of_rows[group];
+    float* values = row_of_group[group];
 #pragma unroll
     for (int i = 0; i < V; ++i) own[lane + L * i] = 0.0f;
-    const int64_t first = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * GROUPS * rows_per_group + threadIdx.x / L;
-    int s = -2, begin = 0, end = 0;  // the sequence of the last row, and its rows
+    const int64_t first = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * GROUPS * rows_per_group;
+    if (first >= a.T) return;
+    int64_t t = first + group;
+    const char* in = static_cast<const char*>(a.logits) + t * a.stride * SIZE;
+    char* out = static_cast<char*>(a.d_logits) + t * a.E * SIZE;
+    int64_t at_k = t * a.k + lane;
+    // the sequence of the last row, and its rows; before the first row none is known
+    int s = sequence_of_wave(a.seq_offsets, (int)min(first + threadIdx.x / 64 * (64 / L), (int64_t)a.T), a.S, a.T);
+    int begin = 0, end = 0;
     float pull[V], zpull = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) pull[i] = 0.0f;
-    for (int step = 0; step < rows_per_group; ++step) {
-        const int64_t t = first + (int64_t)step * GROUPS;
-        if (t >= a.T) break;
-        if (s == -2 || t < begin || t >= end) {
-            s = sequence_of(a.seq_offsets, (int)t, a.S, a.T);
-            begin = s >= 0 ? offset_at(a.seq_offsets, s, a.T) : 0;
+    for (int step = 0; step < rows_per_group && t < a.T; ++step, t += GROUPS, in += GROUPS * a.stride * SIZE,
+             out += (int64_t)GROUPS * a.E * SIZE, at_k += GROUPS * a.k) {
+        float l[V], p[V], dw[KV];
+        int id[KV];
+        load_row<TYPE, L, V, VEC>(l, in, a.E, lane);
+        if (a.d_topk_w) {
+#pragma unroll
+            for (int q = 0; q < KV; ++q) {
+                id[q] = -1;
+                dw[q] = 0.0f;
+                if (q > 0 && q * L >= a.k) break;
+                if (lane + q * L < a.k) {
+                    const int64_t e = a.topk_idx[at_k + q * L];
+                    id[q] = (uint64_t)e < (uint64_t)a.E ? (int)e : -1;
+                    dw[q] = a.scale * a.d_topk_w[at_k + q * L];
+                }
+            }
+        }
+        if (t < begin || t >= end) {
+            s = sequence_from(a.seq_offsets, max(s, 0), (int)t, a.S, a.T);
+            begin = offset_at(a.seq_offsets, min(s, a.S), a.T);
+            if (s == 0 && t < begin) {  // in front of the first sequence
+                s = -1;
+                end = begin;
+                begin = 0;
+                continue;
+            }
             end = s < a.S ? offset_at(a.seq_offsets, s + 1, a.T) : a.T;
             if (s < 0 || s >= a.S) continue;
             const float n = a.rows ? (float)a.rows[s] : 0.0f;
@@ -533,30 +586,15 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
                     low += c[i] & 0xFFFF;
                     high += c[i] >> 16;
                 }
-                const int64_t total = ((int64_t)sum_over_lanes<L>(high) << 16) + sum_over_lanes<L>(low);
-                const float by = n > 0.0f && total != 0 ? a.d_loss[s] / n / (float)total : 0.0f;
+                const double total = 65536.0 * sum_over_lanes<L>(high) + sum_over_lanes<L>(low);
+                const float by = n > 0.0f && total != 0.0 ? a.d_loss[s] / n / (float)total : 0.0f;
 #pragma unroll
-                for (int i = 0; i < V; ++i) pull[i] = by * (float)((int64_t)c[i] * a.E - total);
+                for (int i = 0; i < V; ++i) pull[i] = by * (float)fma((double)c[i], (double)a.E, -total);  // exact before it is rounded
             }
             zpull = a.d_z && n > 0.0f ? 2.0f * a.d_z[s] / n : 0.0f;
         }
         if (s < 0 || s >= a.S) continue;
 
-        float l[V], p[V];
-        load_row<TYPE, L, V, VEC>(l, a.logits, t * a.stride, a.E, lane);
-        int id[KV];
-        float lk[KV], dw[KV];
-        if (a.d_topk_w) {
-#pragma unroll
-            for (int q = 0; q < KV; ++q) {
-                const int j = lane + L * q;
-                const int64_t e = j < a.k ? a.topk_idx[t * a.k + j] : -1;
-                id[q] = e >= 0 && e < a.E ? (int)e : -1;
-                dw[q] = id[q] >= 0 ? a.scale * a.d_topk_w[t * a.k + j] : 0.0f;
-                lk[q] = id[q] >= 0 ? load1<TYPE>(a.logits, t * a.stride + id[q]) : -INFINITY;
-            }
-        }
-        mask_row<L, V, VEC>(l, a.E, lane);
         const RowSum r = shares<SCORE, L, V>(l, p);
         float common = 0.0f;  // what falls on every expert by its share
         if (a.d_loss) {
@@ -565,94 +603,107 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
             common = -over_lanes<Sum, L>(common) * r.inv;
         }
         if (SCORE == MOE_SCORE_SOFTMAX && a.d_z) common = fmaf(zpull, r.lse(), common);
-        bool chosen = false;
         if (a.d_topk_w) {
-            float w[KV], rest[KV];  // r and, of sigmoid scores, 1 - s
-            float top = -INFINITY;
-            if (a.renorm) {
 #pragma unroll
-                for (int q = 0; q < KV; ++q) top = max2(top, lk[q]);
-                top = over_lanes<Max, L>(top);
-            }
-            float sum = 0.0f;
+            for (int i = 0; i < V; ++i) values[expert_of<L, V, VEC>(lane, i)] = SCORE == MOE_SCORE_SOFTMAX ? p[i] : l[i];
+            float w[KV], rest[KV];  // the chosen's scores and, of sigmoid ones, what they lack to 1
+            float sum = 0.0f, m = 0.0f;
 #pragma unroll
             for (int q = 0; q < KV; ++q) {
-                if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
-                    w[q] = exp_over(lk[q], a.renorm ? top : r.top);
-                    rest[q] = 1.0f;
-                } else {
-                    // over exp(top) where all are small, as in shares()
-                    w[q] = a.renorm && top < -60.0f ? exp_over(lk[q], top) : sigmoid(lk[q]);
-                    rest[q] = sigmoid(-lk[q]);
+                w[q] = 0.0f;
+                rest[q] = 1.0f;
+                if (q > 0 && q * L >= a.k) break;
+                if (id[q] >= 0) {
+                    const float v = values[id[q]];
+                    if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
+                        w[q] = v;
+                    } else {
+                        w[q] = sigmoid(v);
+                        rest[q] = sigmoid(-v);
+                    }
                 }
-                if (lk[q] == -INFINITY) w[q] = 0.0f;  // none, or masked
                 sum += w[q];
+                m = fmaf(w[q], dw[q], m);
             }
-            float m = 0.0f;
+            sum = over_lanes<Sum, L>(sum);
+            m = over_lanes<Sum, L>(m);
             if (a.renorm) {
-                sum = over_lanes<Sum, L>(sum);
+                if (sum < 0x1p-80f) {  // far below the row's largest, or all tiny: formed over the largest of them
+                    float top = -INFINITY, lk[KV];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) values[expert_of<L, V, VEC>(lane, i)] = l[i];
+#pragma unroll
+                    for (int q = 0; q < KV; ++q) {
+                        lk[q] = id[q] >= 0 ? values[id[q]] : -INFINITY;
+                        top = max2(top, lk[q]);
+                    }
+                    top = over_lanes<Max, L>(top);
+                    sum = m = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < KV; ++q) {
+                        w[q] = lk[q] > -INFINITY ? exp_over(lk[q], top) : 0.0f;
+                        if constexpr (SCORE == MOE_SCORE_SIGMOID) w[q] *= rest[q];  // 1 / (1 + exp(l))
+                        sum += w[q];
+                        m = fmaf(w[q], dw[q], m);
+                    }
+                    sum = over_lanes<Sum, L>(sum);
+                    m = over_lanes<Sum, L>(m);
+                }
                 const float inv = sum != 0.0f ? __builtin_amdgcn_rcpf(sum) : 0.0f;
+                m *= inv;
 #pragma unroll
-                for (int q = 0; q < KV; ++q) {
-                    w[q] *= inv;
-                    m = fmaf(w[q], dw[q], m);
-                }
-                m = over_lanes<Sum, L>(m);
-            } else if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
-                float all = 0.0f;
+                for (int q = 0; q < KV; ++q) w[q] *= inv;
+            } else {
+                if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
+                    common = fmaf(-m, r.inv, common);
 #pragma unroll
-                for (int q = 0; q < KV; ++q) {
-                    w[q] *= r.inv;
-                    all = fmaf(w[q], dw[q], all);
+                    for (int q = 0; q < KV; ++q) w[q] *= r.inv;
                 }
-                common -= over_lanes<Sum, L>(all);
+                m = 0.0f;
             }
-            chosen = true;
 #pragma unroll
-            for (int q = 0; q < KV; ++q)
+            for (int q = 0; q < KV; ++q) {
+                if (q > 0 && q * L >= a.k) break;
                 if (id[q] >= 0) atomicAdd(&own[id[q]], w[q] * (dw[q] - m) * rest[q]);
+            }
         }
         float g[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            g[i] = p[i] * r.inv * (pull[i] + common);
+            g[i] = p[i] * fmaf(pull[i], r.inv, common * r.inv);
             if constexpr (SCORE == MOE_SCORE_SIGMOID) g[i] *= sigmoid(-l[i]);
         }
-        if (chosen) {
+        if (a.d_topk_w) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = expert_of<L, V, VEC>(lane, i);
-                if (VEC || e < a.E) g[i] += own[e];
-            }
+            for (int i = 0; i < V; ++i) g[i] += own[expert_of<L, V, VEC>(lane, i)];
 #pragma unroll
-            for (int q = 0; q < KV; ++q)
+            for (int q = 0; q < KV; ++q) {
+                if (q > 0 && q * L >= a.k) break;
                 if (id[q] >= 0) own[id[q]] = 0.0f;
+            }
         }
+        if (!(fabsf(common * r.inv) < INFINITY)) {  // a masked expert has a gradient of 0 beside a NaN too
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (l[i] == -INFINITY) g[i] = 0.0f;
-        const int64_t at = t * a.E;
+            for (int i = 0; i < V; ++i)
+                if (l[i] == -INFINITY) g[i] = 0.0f;
+        }
+        char* at = out + (VEC ? 4 : 1) * lane * SIZE;
         if constexpr (VEC) {
 #pragma unroll
             for (int i = 0; i < V; i += 4) {
-                const int e = 4 * (lane + L * (i / 4));
-                if (e < a.E) {
-                    if constexpr (TYPE == MOE_F32)
-                        *reinterpret_cast<v4f*>(static_cast<float*>(a.d_logits) + at + e) =
-                            v4f{g[i], g[i + 1], g[i + 2], g[i + 3]};
-                    else
-                        *reinterpret_cast<v2i*>(static_cast<uint16_t*>(a.d_logits) + at + e) =
-                            v2i{(int)pack_bf16(g[i], g[i + 1]), (int)pack_bf16(g[i + 2], g[i + 3])};
-                }
+                if (expert_of<L, V, VEC>(lane, i) >= a.E) continue;
+                if constexpr (TYPE == MOE_F32)
+                    *reinterpret_cast<v4f*>(at + L * i * SIZE) = v4f{g[i], g[i + 1], g[i + 2], g[i + 3]};
+                else
+                    *reinterpret_cast<v2i*>(at + L * i * SIZE) =
+                        v2i{(int)pack_bf16(g[i], g[i + 1]), (int)pack_bf16(g[i + 2], g[i + 3])};
             }
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int e = lane + L * i;
-                if (e < a.E) {
-                    if constexpr (TYPE == MOE_F32) static_cast<float*>(a.d_logits)[at + e] = g[i];
-                    else static_cast<uint16_t*>(a.d_logits)[at + e] = (uint16_t)pack_bf16(g[i], g[i]);
-                }
+                if (expert_of<L, V, VEC>(lane, i) >= a.E) continue;
+                if constexpr (TYPE == MOE_F32) *reinterpret_cast<float*>(at + L * i * SIZE) = g[i];
+                else *reinterpret_cast<uint16_t*>(at + L * i * SIZE) = (uint16_t)pack_bf16(g[i], g[i]);
             }
         }
     }
