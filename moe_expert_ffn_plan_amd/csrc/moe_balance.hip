@@ -132,8 +132,9 @@ __device__ __forceinline__ float sigmoid(float l) {
 }
 __device__ __forceinline__ float exp_over(float l, float top) { return __builtin_amdgcn_exp2f((l - top) * kLog2e); }
 
-template <int SCORE, int L, int V>
-__device__ __forceinline__ RowSum shares(const float (&l)[V], float (&p)[V]) {
+// rest: of sigmoid scores, what they lack to 1 (REST alone)
+template <int SCORE, int L, int V, bool REST>
+__device__ __forceinline__ RowSum shares(const float (&l)[V], float (&p)[V], float (&rest)[V]) {
     RowSum r;
     float top = max2(l[0], l[1]);
 #pragma unroll
@@ -158,10 +159,19 @@ __device__ __forceinline__ RowSum shares(const float (&l)[V], float (&p)[V]) {
     } else {
         if (r.top > -60.0f || !r.alive) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) p[i] = sigmoid(l[i]);
+            for (int i = 0; i < V; ++i) {
+                const float e = __builtin_amdgcn_exp2f(-kLog2e * l[i]);
+                p[i] = __builtin_amdgcn_rcpf(1.0f + e);
+                if constexpr (REST) rest[i] = l[i] < -64.0f ? 1.0f : e * p[i];
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) p[i] = exp_over(l[i], r.top) * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[i] * kLog2e));
+            for (int i = 0; i < V; ++i) {
+                p[i] = exp_over(l[i], r.top);
+                const float less = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[i] * kLog2e));
+                p[i] *= less;
+                if constexpr (REST) rest[i] = less;
+            }
         }
     }
     float sum = 0.0f;
@@ -278,7 +288,7 @@ __device__ __forceinline__ void sum_rows(const BalanceArgs& a, int row, int end,
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 float p[V];
-                const RowSum r = shares<SCORE, L, V>(l[u], p);
+                const RowSum r = shares<SCORE, L, V, false>(l[u], p, p);
 #pragma unroll
                 for (int i = 0; i < V; ++i) acc[i] = fmaf(p[i], r.inv, acc[i]);
                 rows += r.alive;
@@ -595,7 +605,8 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
         }
         if (s < 0 || s >= a.S) continue;
 
-        const RowSum r = shares<SCORE, L, V>(l, p);
+        float less[V];  // of sigmoid scores
+        const RowSum r = shares<SCORE, L, V, SCORE == MOE_SCORE_SIGMOID>(l, p, less);
         float common = 0.0f;  // what falls on every expert by its share
         if (a.d_loss) {
 #pragma unroll
@@ -671,7 +682,7 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             g[i] = p[i] * fmaf(pull[i], r.inv, common * r.inv);
-            if constexpr (SCORE == MOE_SCORE_SIGMOID) g[i] *= sigmoid(-l[i]);
+            if constexpr (SCORE == MOE_SCORE_SIGMOID) g[i] *= less[i];
         }
         if (a.d_topk_w) {
 #pragma unroll
@@ -729,7 +740,7 @@ template <int TYPE, int SCORE, int L, int V, bool VEC, int KV>
 void grad_go(const GateGradArgs& a, hipStream_t stream) {
     // rows side by side while there are workgroups to have, then several to a group, which load a sequence's counts once
     int per = 1;
-    while (per < 8 && (int64_t)kThreads / L * per * 4096 < a.T) per *= 2;
+    while (per < 8 && (int64_t)kThreads / L * per * 1024 < a.T) per *= 2;
     const int rows = kThreads / L * per;
     hipLaunchKernelGGL((gate_grad_kernel<TYPE, SCORE, L, V, VEC, KV>), wide_grid(((int64_t)a.T + rows - 1) / rows),
                        dim3(kThreads), 0, stream, a, per);

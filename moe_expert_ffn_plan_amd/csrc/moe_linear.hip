@@ -325,6 +325,115 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
         }
 }
 
+// Few rows of x: what counts is how the weights stream in.  A workgroup takes a block of 32 weight rows over all columns,
+// its W waves U K-steps each in turn.  The weights go straight from memory to the matrix instructions' registers (no two
+// waves read the same ones, so LDS would only be a detour).  x goes through LDS, where each wave has a place of its own and
+// needs no barrier: lanes that load neighbouring chunks of few rows touch few lines, lanes that load what they multiply
+// touch one each.  The waves' sums are added through LDS, in the waves' order.
+template <int FMT, int ROWS, int W, int U>
+struct Few {
+    static constexpr int RB = FMT == MOE_E2M1 ? 64 : 128, BYTES = U * RB, CHUNKS = BYTES / 16;  // of a row in a turn
+    static constexpr int MI = (ROWS + 31) / 32, PER = 64 / CHUNKS;                              // rows of a DMA instruction
+    static constexpr int PLACE = ROWS * BYTES, SUMS = MI * 16 * 64 * 4;                         // of a wave
+    static constexpr int LDS = W * (PLACE > SUMS ? PLACE : SUMS);
+    static_assert(CHUNKS >= 16 && CHUNKS <= 64 && LDS <= 160 * 1024, "place of a wave");
+};
+
+template <int FMT, int ROWS, int W, int U>
+__global__ __launch_bounds__(64 * W) void few_kernel(Args g) {
+    using F = Few<FMT, ROWS, W, U>;
+    typedef typename Frag<FMT>::type fa;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[F::LDS];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 31, q = lane >> 5, b = blockIdx.x;
+    uint8_t* place = smem + w * F::PLACE;
+    const int row_bytes = (int)g.x_row, blocks = g.sf_row;  // of scales: bytes, one for 32 columns
+    const uint8_t* code = g.w + (int64_t)b * g.KT * kBlockCodes + r * 64;
+    const uint8_t* scale = g.w_sf + (int64_t)b * g.KT * kBlockScales + r * 4;
+    const int c0 = ((2 * q) ^ ((r >> 2) & 3)) * 16;  // of half 0; half 1 is its neighbour
+    v16f acc[F::MI];
+#pragma unroll
+    for (int i = 0; i < F::MI; ++i) acc[i] = v16f{};
+    for (int kt0 = w * U; kt0 < g.KT; kt0 += W * U) {
+        // columns past the last are those of the row's last chunk, and its last scale: the weights there are 0
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the last turn's reads are done
+#pragma unroll
+        for (int i = 0; i < ROWS / F::PER; ++i) {
+            if (i * F::PER >= g.M) break;
+            const int row = i * F::PER + lane / F::CHUNKS;
+            const int chunk = (lane % F::CHUNKS) ^ (row & 15);
+            const uint32_t at = (uint32_t)min(row, g.M - 1) * (uint32_t)row_bytes +
+                                (uint32_t)min(kt0 * F::RB + chunk * 16, row_bytes - 16);
+            dma16(at, g.x, lds_addr(place + i * 1024));
+        }
+        v4i wc[U][2];
+        uint32_t ws[U], xs[F::MI][U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int kt = min(kt0 + u, g.KT - 1);
+            const uint8_t* at = code + (int64_t)kt * kBlockCodes;
+            wc[u][0] = *reinterpret_cast<const v4i*>(at + c0);
+            wc[u][1] = *reinterpret_cast<const v4i*>(at + (c0 ^ 16));
+            ws[u] = *reinterpret_cast<const uint32_t*>(scale + (int64_t)kt * kBlockScales);
+        }
+#pragma unroll
+        for (int i = 0; i < F::MI; ++i) {  // a turn's scales of a row lie side by side
+            const uint8_t* sf = g.sf + (int64_t)min(i * 32 + r, g.M - 1) * blocks + kt0 * 4;
+            if ((kt0 + U) * 4 <= blocks) {
+                __builtin_memcpy(&xs[i][0], sf, U * 4);
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    xs[i][u] = 0;
+                    for (int k = 0; k < 4; ++k)
+                        if ((kt0 + u) * 4 + k < blocks) xs[i][u] |= (uint32_t)sf[u * 4 + k] << (8 * k);
+                }
+            }
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (kt0 + u >= g.KT) break;
+            const int sb = (int)(ws[u] >> (16 * q));
+#pragma unroll
+            for (int i = 0; i < F::MI; ++i) {
+                const uint8_t* row = place + (ROWS < 32 ? r % ROWS : i * 32 + r) * F::BYTES;
+                const int sa = (int)(xs[i][u] >> (16 * q));
+                auto chunk = [&](int c) { return *reinterpret_cast<const v4i*>(row + (((u * (F::RB / 16) + c) ^ (r & 15)) << 4)); };
+                fa a0, a1;
+                if constexpr (FMT == MOE_E2M1) {
+                    a0 = chunk(2 * q);
+                    a1 = chunk(2 * q + 1);
+                } else {
+                    const v4i c00 = chunk(q), c01 = chunk(4 + q), c10 = chunk(2 + q), c11 = chunk(6 + q);
+                    a0 = v8i{c00[0], c00[1], c00[2], c00[3], c01[0], c01[1], c01[2], c01[3]};
+                    a1 = v8i{c10[0], c10[1], c10[2], c10[3], c11[0], c11[1], c11[2], c11[3]};
+                }
+                acc[i] = mfma<FMT, 0>(a0, wc[u][0], acc[i], sa, sb);
+                acc[i] = mfma<FMT, 1>(a1, wc[u][1], acc[i], sa, sb);
+            }
+        }
+    }
+    __syncthreads();
+    float* sums = reinterpret_cast<float*>(smem);  // [W][MI * 16][64]
+#pragma unroll
+    for (int i = 0; i < F::MI; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (i * 32 + 8 * (e / 4) < g.M) sums[((w * F::MI + i) * 16 + e) * 64 + lane] = acc[i][e];
+    __syncthreads();
+    for (int o = threadIdx.x; o < F::MI * 1024; o += 64 * W) {
+        const int at = o & 63, e = o / 64 % 16, i = o / 1024;
+        const int row = i * 32 + 8 * (e / 4) + 4 * (at >> 5) + e % 4;
+        const int col = (b >> 1) * 64 + 2 * (at & 31) + (b & 1);
+        if (row >= g.M || col >= g.N) continue;
+        float v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) v += sums[((k * F::MI + i) * 16 + e) * 64 + at];
+        g.y[(int64_t)row * g.y_stride + col] = (uint16_t)pack_bf16(v, v);
+    }
+}
+
 constexpr int kThreads = 256;
 
 // The splits' sums, in their order.
@@ -359,13 +468,26 @@ void go(const Args& g, hipStream_t stream) {
                        stream, g);
 }
 
+template <int FMT, int ROWS, int W, int U>
+void few(const Args& g, hipStream_t stream) {
+    hipLaunchKernelGGL((few_kernel<FMT, ROWS, W, U>), dim3((unsigned)g.blocks), dim3(64 * W), 0, stream, g);
+}
+
 }  // namespace
 
+constexpr int kFewRows = 64;
 constexpr int kFillTiles = 256;  // a workgroup for every compute unit
 
 MxLinearChoice choose_mx_linear(int M, int N, int K, int format) {
     MxLinearChoice c{};
     const int KT = mx_steps(K);
+    if (M <= kFewRows) {
+        c.kernel = 2;
+        c.tokens = M <= 32 ? 32 : 64;
+        c.columns = 32;
+        c.splits = 1;
+        return c;
+    }
     const int64_t big = (((int64_t)M + 255) / 256) * (((int64_t)N + 255) / 256);
     c.kernel = big >= kFillTiles ? 0 : 1;
     c.tokens = c.columns = c.kernel == 0 ? 256 : 128;
@@ -420,7 +542,16 @@ hipError_t launch_mx_linear(const MxLinearArgs& a, const MxLinearChoice& c, hipS
     g.splits = (g.KT + g.per - 1) / g.per;  // none without a K-step
     g.mt = (a.M + c.tokens - 1) / c.tokens;
     g.nt = (a.N + c.columns - 1) / c.columns;
-    if (c.kernel == 0) {
+    if (c.kernel == 2) {
+        if (a.format == MOE_E2M1) {
+            if (a.M <= 32) few<MOE_E2M1, 32, 16, 4>(g, stream);
+            else few<MOE_E2M1, 64, 8, 4>(g, stream);
+        } else {
+            if (a.M <= 16) few<MOE_E4M3, 16, 16, 4>(g, stream);
+            else if (a.M <= 32) few<MOE_E4M3, 32, 16, 2>(g, stream);
+            else few<MOE_E4M3, 64, 8, 2>(g, stream);
+        }
+    } else if (c.kernel == 0) {
         if (a.format == MOE_E2M1) go<MOE_E2M1, 256, 256, 2, 4, 4, 2>(g, stream);
         else go<MOE_E4M3, 256, 256, 2, 4, 3, 2>(g, stream);
     } else {
