@@ -2,6 +2,7 @@
 #include "moe_internal.h"
 
 #include <type_traits>
+#include <utility>
 
 namespace moe {
 namespace {
@@ -99,7 +100,7 @@ struct Tile {
     static constexpr int A_PW = (A_I + W - 1) / W, B_PW = (B_I + W - 1) / W, S_PW = (S_I + W - 1) / W;
     static constexpr int D = A_PW + B_PW + S_PW;
     static __device__ __forceinline__ int permuted(int row) { return FMT == MOE_E2M1 ? (row >> 2) & 3 : (row >> 1) & 7; }
-    static_assert(BM % 64 == 0 && BN % 64 == 0 && NI % 2 == 0 && NS >= 2 && NS <= 4 && (NS - 1) * D < 63, "tile");
+    static_assert(BM % 64 == 0 && BN % 64 == 0 && NI % 2 == 0 && NS >= 2 && (NS - 1) * D < 63, "tile");
     static_assert(W * 64 / CHUNKS % 16 == 0 && A_I % W == 0, "rows of a wave's instructions");
 };
 
@@ -121,6 +122,11 @@ __device__ __forceinline__ v16f mfma(const typename Frag<FMT>::type& a, const v4
     } else {
         return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b8, c, 0, 4, H, sa, H, sb);
     }
+}
+
+template <class F, int... I>
+__device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
 }
 
 template <int FMT, int BM, int BN, int WM, int WN, int NS, int OCC>
@@ -299,9 +305,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
         constexpr int later = NS - 2 - decltype(i)::value;
         if (t < n) step(t++, std::false_type{}, std::false_type{}, std::integral_constant<int, (later > 0 ? later : 0)>{});
     };
-    tail(std::integral_constant<int, 1>{});
-    if constexpr (NS > 2) tail(std::integral_constant<int, 2>{});
-    if constexpr (NS > 3) tail(std::integral_constant<int, 3>{});
+    each_of([&](auto i) { tail(std::integral_constant<int, decltype(i)::value + 1>{}); }, std::make_integer_sequence<int, NS - 1>{});
 
     // ---- outputs: weight rows are laid so that lane r of blocks 2b and 2b + 1 holds outputs 2r and 2r + 1 of their 64
     float* part = g.partial + (int64_t)z * g.M * partial_columns(g);
@@ -346,6 +350,8 @@ __global__ __launch_bounds__(64 * W) void few_kernel(Args g) {
     __shared__ __attribute__((aligned(1024))) uint8_t smem[F::LDS];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 31, q = lane >> 5, b = blockIdx.x;
+    const int m0 = blockIdx.y * ROWS, rows = min(g.M - m0, ROWS);
+    const uint8_t* x = uniform_ptr(g.x + (int64_t)m0 * g.x_row);
     uint8_t* place = smem + w * F::PLACE;
     const int row_bytes = (int)g.x_row, blocks = g.sf_row;  // of scales: bytes, one for 32 columns
     const uint8_t* code = g.w + (int64_t)b * g.KT * kBlockCodes + r * 64;
@@ -359,12 +365,12 @@ __global__ __launch_bounds__(64 * W) void few_kernel(Args g) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the last turn's reads are done
 #pragma unroll
         for (int i = 0; i < ROWS / F::PER; ++i) {
-            if (i * F::PER >= g.M) break;
+            if (i * F::PER >= rows) break;
             const int row = i * F::PER + lane / F::CHUNKS;
             const int chunk = (lane % F::CHUNKS) ^ (row & 15);
-            const uint32_t at = (uint32_t)min(row, g.M - 1) * (uint32_t)row_bytes +
+            const uint32_t at = (uint32_t)min(row, rows - 1) * (uint32_t)row_bytes +
                                 (uint32_t)min(kt0 * F::RB + chunk * 16, row_bytes - 16);
-            dma16(at, g.x, lds_addr(place + i * 1024));
+            dma16(at, x, lds_addr(place + i * 1024));
         }
         v4i wc[U][2];
         uint32_t ws[U], xs[F::MI][U];
@@ -378,7 +384,7 @@ __global__ __launch_bounds__(64 * W) void few_kernel(Args g) {
         }
 #pragma unroll
         for (int i = 0; i < F::MI; ++i) {  // a turn's scales of a row lie side by side
-            const uint8_t* sf = g.sf + (int64_t)min(i * 32 + r, g.M - 1) * blocks + kt0 * 4;
+            const uint8_t* sf = g.sf + (int64_t)(m0 + min(i * 32 + r, rows - 1)) * blocks + kt0 * 4;
             if ((kt0 + U) * 4 <= blocks) {
                 __builtin_memcpy(&xs[i][0], sf, U * 4);
             } else {
@@ -420,17 +426,17 @@ __global__ __launch_bounds__(64 * W) void few_kernel(Args g) {
     for (int i = 0; i < F::MI; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-            if (i * 32 + 8 * (e / 4) < g.M) sums[((w * F::MI + i) * 16 + e) * 64 + lane] = acc[i][e];
+            if (i * 32 + 8 * (e / 4) < rows) sums[((w * F::MI + i) * 16 + e) * 64 + lane] = acc[i][e];
     __syncthreads();
     for (int o = threadIdx.x; o < F::MI * 1024; o += 64 * W) {
         const int at = o & 63, e = o / 64 % 16, i = o / 1024;
         const int row = i * 32 + 8 * (e / 4) + 4 * (at >> 5) + e % 4;
         const int col = (b >> 1) * 64 + 2 * (at & 31) + (b & 1);
-        if (row >= g.M || col >= g.N) continue;
+        if (row >= rows || col >= g.N) continue;
         float v = 0.0f;
 #pragma unroll
         for (int k = 0; k < W; ++k) v += sums[((k * F::MI + i) * 16 + e) * 64 + at];
-        g.y[(int64_t)row * g.y_stride + col] = (uint16_t)pack_bf16(v, v);
+        g.y[(int64_t)(m0 + row) * g.y_stride + col] = (uint16_t)pack_bf16(v, v);
     }
 }
 
@@ -470,12 +476,13 @@ void go(const Args& g, hipStream_t stream) {
 
 template <int FMT, int ROWS, int W, int U>
 void few(const Args& g, hipStream_t stream) {
-    hipLaunchKernelGGL((few_kernel<FMT, ROWS, W, U>), dim3((unsigned)g.blocks), dim3(64 * W), 0, stream, g);
+    hipLaunchKernelGGL((few_kernel<FMT, ROWS, W, U>), dim3((unsigned)g.blocks, (unsigned)((g.M + ROWS - 1) / ROWS)),
+                       dim3(64 * W), 0, stream, g);
 }
 
 }  // namespace
 
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 128;
 constexpr int kFillTiles = 256;  // a workgroup for every compute unit
 
 MxLinearChoice choose_mx_linear(int M, int N, int K, int format) {

@@ -211,10 +211,14 @@ def test_linear_nan(gpu, T, fmt):
 
 
 def test_linear_workspace_is_not_read(gpu):
-    x, w = operands(100, 4064, 200, "e4m3", 1, gpu)
-    a, s = product(x, w, "e4m3", ws_fill=0xFF)
-    b, _ = product(x, w, "e4m3", ws_fill=0)
-    assert B.mx_linear_workspace_bytes(s) > 0 and torch.equal(a, b)
+    used = 0
+    for T in (100, 300, 2047):
+        x, w = operands(T, 4064, 200, "e4m3", 1, gpu)
+        a, s = product(x, w, "e4m3", ws_fill=0xFF)
+        b, _ = product(x, w, "e4m3", ws_fill=0)
+        assert torch.equal(a, b)
+        used += B.mx_linear_workspace_bytes(s) > 0
+    assert used
 
 
 def test_prepared_layout(gpu):
