@@ -58,7 +58,7 @@ struct Args {
     // scales of x as words: row m of K-step kt at (m / 64) * sf_band + (m % 64) * sf_row + kt * sf_step
     int64_t sf_band;
     int sf_row, sf_step;
-    int M, N, KT, tail;   // tail: bytes of a row's last K-step
+    int M, N, KT;
     int blocks;           // blocks of 32 weight rows
     int splits, per;      // K-steps of a split
     int mt, nt;           // tiles
@@ -89,17 +89,23 @@ __device__ __forceinline__ void store2(const Args& a, int row, int col, float v0
 //
 // Half 1 of a stage is read while half 0 is multiplied, and half 0 of the next stage while half 1 is; the barrier that
 // hands over a stage's buffer stands between the two.
-template <int FMT, int BM, int BN, int WM, int WN, int NS_>
+//
+// AK = 2: the rows of x come two K-steps at a time, into a ring of their own of two units.  Rows of 64 bytes are half a
+// line each, and a request for half a line takes as long as one for a line.
+template <int FMT, int BM, int BN, int WM, int WN, int AK, int NS_>
 struct Tile {
     static constexpr int W = WM * WN, THREADS = 64 * W, NS = NS_;
-    static constexpr int RB = FMT == MOE_E2M1 ? 64 : 128;  // bytes of a row in a stage
+    static constexpr int KB = FMT == MOE_E2M1 ? 64 : 128;  // bytes of a row in a K-step
+    static constexpr int RB = AK * KB;                     // and in what a DMA instruction loads
     static constexpr int CHUNKS = RB / 16;
     static constexpr int MI = BM / WM / 32, NI = BN / WN / 32;
-    static constexpr int A = 0, B = BM * RB, S = B + BN * 64, STAGE = S + (BM + BN) * 4;
+    static constexpr int UNIT = BM * RB, UNITS = AK == 1 ? NS : 2;  // of x; behind them the stages of everything else
+    static constexpr int B = 0, S = B + BN * 64, STAGE = S + (BM + BN) * 4, LDS = UNITS * UNIT + NS * STAGE;
     static constexpr int A_I = BM * RB / 1024, B_I = BN * 64 / 1024, S_I = (BM + BN) / 64;  // DMA instructions
     static constexpr int A_PW = (A_I + W - 1) / W, B_PW = (B_I + W - 1) / W, S_PW = (S_I + W - 1) / W;
-    static constexpr int D = A_PW + B_PW + S_PW;
-    static __device__ __forceinline__ int permuted(int row) { return FMT == MOE_E2M1 ? (row >> 2) & 3 : (row >> 1) & 7; }
+    static constexpr int D = (AK == 1 ? A_PW : 0) + B_PW + S_PW;  // of a stage
+    static __device__ __forceinline__ int permuted(int row) { return CHUNKS == 4 ? (row >> 2) & 3 : (row >> 1) & 7; }
+    static_assert(CHUNKS == 4 || CHUNKS == 8, "rows of 64 or 128 bytes");
     static_assert(BM % 64 == 0 && BN % 64 == 0 && NI % 2 == 0 && NS >= 2 && (NS - 1) * D < 63, "tile");
     static_assert(W * 64 / CHUNKS % 16 == 0 && A_I % W == 0, "rows of a wave's instructions");
 };
@@ -129,10 +135,12 @@ __device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>) {
     (f(std::integral_constant<int, I>{}), ...);
 }
 
-template <int FMT, int BM, int BN, int WM, int WN, int NS, int OCC>
+template <int FMT, int BM, int BN, int WM, int WN, int AK, int NS, int OCC>
 __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
-    using T = Tile<FMT, BM, BN, WM, WN, NS>;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * T::STAGE];
+    using T = Tile<FMT, BM, BN, WM, WN, AK, NS>;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS];
+    auto unit_of = [&](int u) { return smem + u % T::UNITS * T::UNIT; };
+    auto stage_of = [&](int t) { return smem + T::UNITS * T::UNIT + t % NS * T::STAGE; };
 
     // every XCD takes a contiguous run of tiles, in columns of 8 tile rows, so that what runs together shares
     // its rows of x and its weights in the XCD's L2
@@ -186,17 +194,28 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
             s_off[i] = (uint32_t)min(blk, g.blocks - 1 - nb0) * (uint32_t)g.KT * kBlockScales + (uint32_t)(at % 32) * 4;
         }
     }
-    // DMA instruction i of K-step k0 + t
-    auto issue1 = [&](int i, uint8_t* st, int kt) {
-        if (i < T::A_PW) {
-            // columns past the last are those of the row's last chunk: the weights there are 0
-            const uint32_t c = kt == g.KT - 1 ? min(chunk, (uint32_t)g.tail - 16) : chunk;
-            dma16(a_row[i] + c, x + (int64_t)kt * T::RB, lds_addr(st + T::A + (i * T::W + w) % T::A_I * 1024));
-        } else if (i < T::A_PW + T::B_PW) {
+    // DMA instruction i of unit u of x: K-steps k0 + AK u and on.  Columns past the last are those of the row's last chunk:
+    // the weights there are 0.
+    auto issue_a = [&](int i, int u) {
+        const uint32_t at = (uint32_t)(k0 + u * AK) * T::KB + chunk;
+        dma16(a_row[i] + min(at, (uint32_t)g.x_row - 16), x, lds_addr(unit_of(u) + (i * T::W + w) % T::A_I * 1024));
+    };
+    // of stage t, in place of stage `to`
+    auto issue1 = [&](int i, int to, int t) {
+        uint8_t* st = stage_of(to);
+        const int kt = k0 + t;
+        if constexpr (AK == 1) {
+            if (i < T::A_PW) {
+                const uint32_t at = (uint32_t)kt * T::KB + chunk;
+                dma16(a_row[i] + min(at, (uint32_t)g.x_row - 16), x, lds_addr(unit_of(to) + (i * T::W + w) % T::A_I * 1024));
+                return;
+            }
             i -= T::A_PW;
+        }
+        if (i < T::B_PW) {
             dma16((uint32_t)lane * 16, b_src[i] + (int64_t)kt * kBlockCodes, lds_addr(st + T::B + (i * T::W + w) % T::B_I * 1024));
         } else {
-            i -= T::A_PW + T::B_PW;
+            i -= T::B_PW;
             dma4(s_off[i], s_src[i] + (int64_t)kt * s_step[i], lds_addr(st + T::S + (i * T::W + w) % T::S_I * 256));
         }
     };
@@ -209,13 +228,13 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
         fa a[T::MI];
         v4i b[T::NI];
     };
-    // fragment i of half h of a stage, in the order in which they are multiplied
-    auto read1 = [&](int i, Half& f, const uint8_t* st, int h) {
+    // fragment i of half h of K-step t, in the order in which they are multiplied
+    auto read1 = [&](int i, Half& f, int t, int h) {
         if (i == 0 || i > T::NI) {
             i = i == 0 ? 0 : i - T::NI;
-            const uint8_t* row = st + T::A + (wm0 + i * 32 + r) * T::RB;
+            const uint8_t* row = unit_of(t / AK) + (wm0 + i * 32 + r) * T::RB;
             if constexpr (FMT == MOE_E2M1) {
-                f.a[i] = *reinterpret_cast<const v4i*>(row + (((2 * q + h) ^ rsw) << 4));
+                f.a[i] = *reinterpret_cast<const v4i*>(row + (((t % AK * 4 + 2 * q + h) ^ rsw) << 4));
             } else {
                 const v4i lo = *reinterpret_cast<const v4i*>(row + (((2 * h + q) ^ rsw) << 4));
                 const v4i hi = *reinterpret_cast<const v4i*>(row + (((4 + 2 * h + q) ^ rsw) << 4));
@@ -223,13 +242,14 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
             }
         } else {
             i -= 1;
-            f.b[i] = *reinterpret_cast<const v4i*>(st + T::B + (wn0 + i * 32 + r) * 64 + (((2 * q + h) ^ bsw) << 4));
+            f.b[i] = *reinterpret_cast<const v4i*>(stage_of(t) + T::B + (wn0 + i * 32 + r) * 64 + (((2 * q + h) ^ bsw) << 4));
         }
     };
     struct Scales {
         int a[T::MI], b[T::NI];
     };
-    auto read_scales = [&](Scales& f, const uint8_t* st) {
+    auto read_scales = [&](Scales& f, int t) {
+        const uint8_t* st = stage_of(t);
         typedef uint32_t va __attribute__((ext_vector_type(T::MI)));
         typedef uint32_t vb __attribute__((ext_vector_type(T::NI)));
         const va sa = *reinterpret_cast<const va*>(st + T::S + (wm * 32 + r) * T::MI * 4);
@@ -250,62 +270,138 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
     Scales sc, sn;
     // K-step t.  The DMA of stage t + NS begins behind the barrier that frees its buffer (parts 0 .. D1 - 1, if `begin`)
     // and goes on in front of the next (`finish`, of stage t + NS - 1): in one burst the waves wait for each other's
-    // requests.  later: stages behind t + 1 that are in flight at the barrier.  The order is pinned: reads and DMA stand
-    // between the products, so that the matrix core always has the next one.
-    constexpr int D1 = T::D / 2;
+    // requests.  With AK = 2 that of a unit of x does so behind an odd K-step (`begin_a`, `finish_a`).  flight: this wave's
+    // DMA instructions behind those of K-step t + 1.  The order is pinned: reads and DMA stand between the products, so
+    // that the matrix core always has the next one.
+    constexpr int D1 = T::D / 2, A1 = T::A_PW / 2;
     auto dma_slot = [](int i, int count) { return (2 * i + 1) * SLOTS / (2 * count); };
-    auto step = [&](int t, auto finish, auto begin, auto later) {
-        uint8_t* st = smem + t % NS * T::STAGE;
-        const uint8_t* next = smem + (t + 1) % NS * T::STAGE;
-        uint8_t* last = smem + (t + NS - 1) % NS * T::STAGE;
+    auto step = [&](int t, auto finish, auto begin, auto finish_a, auto begin_a, auto flight) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int k = 0; k < SLOTS; ++k) {
             const int i = k / T::NI, j = k % T::NI;
             acc[i][j] = mfma<FMT, 0>(f0.a[i], f0.b[j], acc[i][j], sc.a[i], sc.b[j]);
 #pragma unroll
-            for (int h = k * PER; h < min((k + 1) * PER, FRAGS); ++h) read1(h, f1, st, 1);
-            if constexpr (decltype(finish)::value) {
+            for (int h = k * PER; h < min((k + 1) * PER, FRAGS); ++h) read1(h, f1, t, 1);
+            constexpr int MA = decltype(finish_a)::value ? T::A_PW - A1 : 0, MB = decltype(finish)::value ? T::D - D1 : 0;
 #pragma unroll
-                for (int h = D1; h < T::D; ++h)
-                    if (dma_slot(h - D1, T::D - D1) == k) issue1(h, last, k0 + min(t + NS - 1, n - 1));
-            }
+            for (int h = 0; h < MA + MB; ++h)
+                if (dma_slot(h, MA + MB) == k) {
+                    if (h < MA) issue_a(A1 + h, t / 2 + 1);
+                    else issue1(D1 + h - MA, t + NS - 1, min(t + NS - 1, n - 1));
+                }
             __builtin_amdgcn_sched_barrier(0);
         }
-        wait_and_barrier<decltype(later)::value * T::D>();  // stage t + 1 is there, stage t read
+        wait_and_barrier<decltype(flight)::value>();  // K-step t + 1 is there, K-step t read
 #pragma unroll
         for (int k = 0; k < SLOTS; ++k) {
             const int i = k / T::NI, j = k % T::NI;
             acc[i][j] = mfma<FMT, 1>(f1.a[i], f1.b[j], acc[i][j], sc.a[i], sc.b[j]);
 #pragma unroll
-            for (int h = k * PER; h < min((k + 1) * PER, FRAGS); ++h) read1(h, f0, next, 0);
-            if (k == SLOTS / 2) read_scales(sn, next);
-            if constexpr (decltype(begin)::value) {
+            for (int h = k * PER; h < min((k + 1) * PER, FRAGS); ++h) read1(h, f0, t + 1, 0);
+            if (k == SLOTS / 2) read_scales(sn, t + 1);
+            constexpr int MA = decltype(begin_a)::value ? A1 : 0, MB = decltype(begin)::value ? D1 : 0;
 #pragma unroll
-                for (int h = 0; h < D1; ++h)
-                    if (dma_slot(h, D1) == k) issue1(h, st, k0 + t + NS);
-            }
+            for (int h = 0; h < MA + MB; ++h)
+                if (dma_slot(h, MA + MB) == k) {
+                    if (h < MA) issue_a(h, (t + 3) / 2);
+                    else issue1(h - MA, t, t + NS);
+                }
             __builtin_amdgcn_sched_barrier(0);
         }
         sc = sn;
     };
-    // a split of fewer than NS K-steps fills the ring with its last one
-#pragma unroll
-    for (int t = 0; t < NS; ++t)
-#pragma unroll
-        for (int i = 0; i < (t < NS - 1 ? T::D : D1); ++i) issue1(i, smem + t * T::STAGE, k0 + min(t, n - 1));
-    wait_and_barrier<(NS - 2) * T::D + D1>();
-#pragma unroll
-    for (int i = 0; i < FRAGS; ++i) read1(i, f0, smem, 0);
-    read_scales(sc, smem);
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
     int t = 0;
-    for (; t < n - NS; ++t) step(t, std::true_type{}, std::true_type{}, std::integral_constant<int, NS - 2>{});
-    step(t++, std::true_type{}, std::false_type{}, std::integral_constant<int, NS - 2>{});
-    auto tail = [&](auto i) {
-        constexpr int later = NS - 2 - decltype(i)::value;
-        if (t < n) step(t++, std::false_type{}, std::false_type{}, std::integral_constant<int, (later > 0 ? later : 0)>{});
-    };
-    each_of([&](auto i) { tail(std::integral_constant<int, decltype(i)::value + 1>{}); }, std::make_integer_sequence<int, NS - 1>{});
+    if constexpr (AK == 1) {
+        // a split of fewer than NS K-steps fills the ring with its last one
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+            for (int i = 0; i < (u < NS - 1 ? T::D : D1); ++i) issue1(i, u, min(u, n - 1));
+        wait_and_barrier<(NS - 2) * T::D + D1>();
+    } else {  // in the order of the steps that would come before the first: of each stage, and of unit 0 with stage 1
+#pragma unroll
+        for (int i = 0; i < T::D; ++i) issue1(i, 0, 0);
+#pragma unroll
+        for (int i = 0; i < T::A_PW; ++i) issue_a(i, 0);
+#pragma unroll
+        for (int i = 0; i < T::D; ++i) issue1(i, 1, 1);
+#pragma unroll
+        for (int i = 0; i < T::D; ++i) issue1(i, 2, 2);
+#pragma unroll
+        for (int i = 0; i < A1; ++i) issue_a(i, 1);
+#pragma unroll
+        for (int i = 0; i < D1; ++i) issue1(i, 3, 3);
+        wait_and_barrier<2 * T::D + A1 + D1>();
+    }
+#pragma unroll
+    for (int i = 0; i < FRAGS; ++i) read1(i, f0, 0, 0);
+    read_scales(sc, 0);
+    if constexpr (AK == 1) {
+        for (; t < n - NS; ++t) step(t, yes, yes, no, no, std::integral_constant<int, (NS - 2) * T::D>{});
+        step(t++, yes, no, no, no, std::integral_constant<int, (NS - 2) * T::D>{});
+        auto tail = [&](auto i) {
+            constexpr int later = NS - 2 - decltype(i)::value;
+            if (t < n) step(t++, no, no, no, no, std::integral_constant<int, (later > 0 ? later : 0) * T::D>{});
+        };
+        each_of([&](auto i) { tail(std::integral_constant<int, decltype(i)::value + 1>{}); },
+                std::make_integer_sequence<int, NS - 1>{});
+    } else {
+        static_assert(AK == 1 || NS == 4, "what is in flight");
+        // At the barrier of an even step stages t + 2 and t + 3 are in flight and the unit that was begun behind t - 1; of an
+        // odd one, whose next step needs that unit, what followed it: the rest of stage t + 2, and stage t + 3.
+        constexpr int EVEN = 2 * T::D + T::A_PW, ODD = 2 * T::D - D1;
+        for (; t + 1 + NS < n;) {
+            step(t++, yes, yes, yes, no, std::integral_constant<int, EVEN>{});
+            step(t++, yes, yes, no, yes, std::integral_constant<int, ODD>{});
+        }
+        // the last NS or NS + 1, of which the one behind the NS has not been begun
+        const int rest = n - t;
+#pragma unroll
+        for (int i = A1; i < T::A_PW; ++i) issue_a(i, t / 2 + 1);
+#pragma unroll
+        for (int i = D1; i < T::D; ++i) issue1(i, t + NS - 1, t + NS - 1);
+        for (; t < n; ++t) {
+            const int left = n - t;
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int k = 0; k < SLOTS; ++k) {
+                const int i = k / T::NI, j = k % T::NI;
+                acc[i][j] = mfma<FMT, 0>(f0.a[i], f0.b[j], acc[i][j], sc.a[i], sc.b[j]);
+#pragma unroll
+                for (int h = k * PER; h < min((k + 1) * PER, FRAGS); ++h) read1(h, f1, t, 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (left == rest) wait_and_barrier<EVEN>();
+            else if (left == NS && rest == NS + 1) wait_and_barrier<ODD>();
+            else if (left == NS - 1 && rest == NS) wait_and_barrier<T::D - D1>();
+            else if (left == 3 && rest == NS + 1) wait_and_barrier<T::D + T::A_PW>();
+            else wait_and_barrier<0>();
+            if (left == NS + 1) {
+#pragma unroll
+                for (int i = 0; i < T::D; ++i) issue1(i, t, n - 1);
+            }
+            if (left == NS && rest == NS + 1) {
+#pragma unroll
+                for (int i = 0; i < T::A_PW; ++i) issue_a(i, (n - 1) / 2);
+            }
+#pragma unroll
+            for (int k = 0; k < SLOTS; ++k) {
+                const int i = k / T::NI, j = k % T::NI;
+                acc[i][j] = mfma<FMT, 1>(f1.a[i], f1.b[j], acc[i][j], sc.a[i], sc.b[j]);
+#pragma unroll
+                for (int h = k * PER; h < min((k + 1) * PER, FRAGS); ++h) read1(h, f0, t + 1, 0);
+                if (k == SLOTS / 2) read_scales(sn, t + 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            sc = sn;
+        }
+    }
+
+    // nothing is on its way to LDS when the workgroup ends: a split of fewer than NS K-steps filled the ring all the same
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
     // ---- outputs: weight rows are laid so that lane r of blocks 2b and 2b + 1 holds outputs 2r and 2r + 1 of their 64
     float* part = g.partial + (int64_t)z * g.M * partial_columns(g);
@@ -467,10 +563,10 @@ __global__ __launch_bounds__(kThreads) void tile_scales_kernel(const uint8_t* sf
     out[i] = v;
 }
 
-template <int FMT, int BM, int BN, int WM, int WN, int NS, int OCC>
+template <int FMT, int BM, int BN, int WM, int WN, int AK, int NS, int OCC>
 void go(const Args& g, hipStream_t stream) {
     const int tiles = g.mt * g.nt * g.splits, share = (tiles + kNumXcd - 1) / kNumXcd;
-    hipLaunchKernelGGL((tile_kernel<FMT, BM, BN, WM, WN, NS, OCC>), dim3((unsigned)(share * kNumXcd)), dim3(64 * WM * WN), 0,
+    hipLaunchKernelGGL((tile_kernel<FMT, BM, BN, WM, WN, AK, NS, OCC>), dim3((unsigned)(share * kNumXcd)), dim3(64 * WM * WN), 0,
                        stream, g);
 }
 
@@ -483,6 +579,7 @@ void few(const Args& g, hipStream_t stream) {
 }  // namespace
 
 constexpr int kFewRows = 128;
+constexpr int kLongSteps = 5;  // K-steps that the ring of two units of x needs
 constexpr int kFillTiles = 256;  // a workgroup for every compute unit
 
 MxLinearChoice choose_mx_linear(int M, int N, int K, int format) {
@@ -529,7 +626,6 @@ hipError_t launch_mx_linear(const MxLinearArgs& a, const MxLinearChoice& c, hipS
     g.w_sf = a.w + (int64_t)g.blocks * g.KT * kBlockCodes;
     const int per16 = a.format == MOE_E2M1 ? 2 : 1;  // codes of a byte
     g.x_row = a.K / per16;
-    g.tail = (a.K - (g.KT - 1) * kStep) / per16;
     g.sf = a.x_sf;
     g.sf_band = (int64_t)a.K / 32 * 64;
     g.sf_row = a.K / 32;
@@ -559,11 +655,12 @@ hipError_t launch_mx_linear(const MxLinearArgs& a, const MxLinearChoice& c, hipS
             else few<MOE_E4M3, 64, 8, 2>(g, stream);
         }
     } else if (c.kernel == 0) {
-        if (a.format == MOE_E2M1) go<MOE_E2M1, 256, 256, 2, 4, 4, 2>(g, stream);
-        else go<MOE_E4M3, 256, 256, 2, 4, 3, 2>(g, stream);
+        if (a.format == MOE_E4M3) go<MOE_E4M3, 256, 256, 2, 4, 1, 3, 2>(g, stream);
+        else if (g.KT >= kLongSteps) go<MOE_E2M1, 256, 256, 2, 4, 2, 4, 2>(g, stream);
+        else go<MOE_E2M1, 256, 256, 2, 4, 1, 4, 2>(g, stream);
     } else {
-        if (a.format == MOE_E2M1) go<MOE_E2M1, 128, 128, 2, 2, 4, 2>(g, stream);
-        else go<MOE_E4M3, 128, 128, 2, 2, 3, 2>(g, stream);
+        if (a.format == MOE_E2M1) go<MOE_E2M1, 128, 128, 2, 2, 1, 4, 2>(g, stream);
+        else go<MOE_E4M3, 128, 128, 2, 2, 1, 3, 2>(g, stream);
     }
     if (g.splits > 1)
         hipLaunchKernelGGL(join_kernel, wide_grid(((int64_t)a.M * (g.blocks * 32) / 4 + kThreads - 1) / kThreads),
