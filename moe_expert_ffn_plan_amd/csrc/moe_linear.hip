@@ -36,6 +36,12 @@ __device__ __forceinline__ void dma16(uint32_t voff, const uint8_t* base, uint32
 __device__ __forceinline__ void dma4(uint32_t voff, const uint8_t* base, uint32_t lds) {
     asm volatile("global_load_lds_dword %0, %1" ::"v"(voff), "s"(base), "{m0}"(lds) : "memory");
 }
+// The lane, computed where it is used: what a tile derives from it once is then not kept in registers over its K-steps.
+__device__ __forceinline__ int fresh_lane() {
+    int l;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+    return l;
+}
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
     return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)p);
 }
@@ -59,6 +65,8 @@ struct Args {
     int64_t sf_band;
     int sf_row, sf_step;
     int M, N, KT;
+    bool wide;            // rows of y can be stored 8 outputs at a time
+    bool stream;          // y is larger than the L2s together: its lines would only push out x's and the weights'
     int blocks;           // blocks of 32 weight rows
     int splits, per;      // K-steps of a split
     int mt, nt;           // tiles
@@ -100,7 +108,8 @@ struct Tile {
     static constexpr int CHUNKS = RB / 16;
     static constexpr int MI = BM / WM / 32, NI = BN / WN / 32;
     static constexpr int UNIT = BM * RB, UNITS = AK == 1 ? NS : 2;  // of x; behind them the stages of everything else
-    static constexpr int B = 0, S = B + BN * 64, STAGE = S + (BM + BN) * 4, LDS = UNITS * UNIT + NS * STAGE;
+    static constexpr int B = 0, S = B + BN * 64, STAGE = S + (BM + BN) * 4, RING = UNITS * UNIT + NS * STAGE;
+    static constexpr int OUT = 8 * (BN / WN) * 2, LDS = RING + W * OUT;  // of a wave: 8 rows of its outputs
     static constexpr int A_I = BM * RB / 1024, B_I = BN * 64 / 1024, S_I = (BM + BN) / 64;  // DMA instructions
     static constexpr int A_PW = (A_I + W - 1) / W, B_PW = (B_I + W - 1) / W, S_PW = (S_I + W - 1) / W;
     static constexpr int D = (AK == 1 ? A_PW : 0) + B_PW + S_PW;  // of a stage
@@ -143,57 +152,65 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
     auto stage_of = [&](int t) { return smem + T::UNITS * T::UNIT + t % NS * T::STAGE; };
 
     // every XCD takes a contiguous run of tiles, in columns of 8 tile rows, so that what runs together shares
-    // its rows of x and its weights in the XCD's L2
+    // its rows of x and its weights in the XCD's L2; a workgroup takes every (workgroups of an XCD)-th of its run
     const int per_split = g.mt * g.nt, tiles = per_split * g.splits;
-    const int share = (tiles + kNumXcd - 1) / kNumXcd;
-    const int id = (blockIdx.x % kNumXcd) * share + blockIdx.x / kNumXcd;
-    if ((int)(blockIdx.x / kNumXcd) >= share || id >= tiles) return;
-    const int z = id / per_split, in = id % per_split;
-    const int band = in / (8 * g.nt), rows = min(8, g.mt - band * 8), at = in - band * 8 * g.nt;
-    const int m0 = (band * 8 + at % rows) * BM, n0 = at / rows * BN;
-    const int k0 = z * g.per, n = min(g.per, g.KT - k0);
+    const int share = (tiles + kNumXcd - 1) / kNumXcd, xcd = blockIdx.x % kNumXcd;
+    const int last = min((xcd + 1) * share, tiles), stride = gridDim.x / kNumXcd;
+    int id = xcd * share + blockIdx.x / kNumXcd;
+    if (id >= last) return;
 
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-    // ---- DMA sources
-    const uint8_t* x = uniform_ptr(g.x + (int64_t)m0 * g.x_row);
+    // ---- DMA sources of a tile
+    int m0, n0, z, k0, n;  // its first row, output, split, K-step, and its K-steps
+    const uint8_t* x;
     // the rows of a wave's instructions lie W * 64 / CHUNKS apart, a multiple of the permutation's 16
     const uint32_t chunk = ((lane % T::CHUNKS) ^ T::permuted(w * (64 / T::CHUNKS) + lane / T::CHUNKS)) * 16;
-    uint32_t a_row[T::A_PW];
-#pragma unroll
-    for (int i = 0; i < T::A_PW; ++i) {
-        const int row = (i * T::W + w) % T::A_I * (64 / T::CHUNKS) + lane / T::CHUNKS;
-        a_row[i] = (uint32_t)min(row, g.M - 1 - m0) * (uint32_t)g.x_row;
-    }
-    const int nb0 = n0 / 32;
+    uint32_t a_row[T::A_PW], s_off[T::S_PW], s_step[T::S_PW];
     const uint8_t* b_src[T::B_PW];
-#pragma unroll
-    for (int i = 0; i < T::B_PW; ++i) {
-        const int blk = (i * T::W + w) % T::B_I;
-        b_src[i] = uniform_ptr(g.w + (int64_t)min(nb0 + blk / 2, g.blocks - 1) * g.KT * kBlockCodes + (blk & 1) * 1024);
-    }
-    // a wave's scales of row r of its blocks of 32 lie side by side: word (part * 32 + r) * blocks + i is that of row
-    // part * 32 * blocks + 32 i + r
-    uint32_t s_off[T::S_PW], s_step[T::S_PW];
     const uint8_t* s_src[T::S_PW];
+    auto take = [&](int tile) {
+        const int lane = fresh_lane();
+        z = tile / per_split;
+        const int in = tile % per_split;
+        const int band = in / (8 * g.nt), rows = min(8, g.mt - band * 8), at = in - band * 8 * g.nt;
+        m0 = (band * 8 + at % rows) * BM;
+        n0 = at / rows * BN;
+        k0 = z * g.per;
+        n = min(g.per, g.KT - k0);
+        x = uniform_ptr(g.x + (int64_t)m0 * g.x_row);
 #pragma unroll
-    for (int i = 0; i < T::S_PW; ++i) {
-        const int idx = (i * T::W + w) % T::S_I;
-        if (idx < BM / 64) {  // rows of x
-            const int word = idx * 64 + lane, at = word / T::MI;
-            const int row = at / 32 * (32 * T::MI) + word % T::MI * 32 + at % 32;
-            const int m = min(row, g.M - 1 - m0);
-            s_src[i] = uniform_ptr(g.sf + m0 / 64 * g.sf_band);
-            s_step[i] = g.sf_step;
-            s_off[i] = (uint32_t)(m / 64) * (uint32_t)g.sf_band + (uint32_t)(m % 64) * (uint32_t)g.sf_row;
-        } else {  // weight rows
-            const int word = (idx - BM / 64) * 64 + lane, at = word / T::NI;
-            const int blk = at / 32 * T::NI + word % T::NI;
-            s_src[i] = uniform_ptr(g.w_sf + (int64_t)nb0 * g.KT * kBlockScales);
-            s_step[i] = kBlockScales;
-            s_off[i] = (uint32_t)min(blk, g.blocks - 1 - nb0) * (uint32_t)g.KT * kBlockScales + (uint32_t)(at % 32) * 4;
+        for (int i = 0; i < T::A_PW; ++i) {
+            const int row = (i * T::W + w) % T::A_I * (64 / T::CHUNKS) + lane / T::CHUNKS;
+            a_row[i] = (uint32_t)min(row, g.M - 1 - m0) * (uint32_t)g.x_row;
         }
-    }
+        const int nb0 = n0 / 32;
+#pragma unroll
+        for (int i = 0; i < T::B_PW; ++i) {
+            const int blk = (i * T::W + w) % T::B_I;
+            b_src[i] = uniform_ptr(g.w + (int64_t)min(nb0 + blk / 2, g.blocks - 1) * g.KT * kBlockCodes + (blk & 1) * 1024);
+        }
+        // a wave's scales of row r of its blocks of 32 lie side by side: word (part * 32 + r) * blocks + i is that of row
+        // part * 32 * blocks + 32 i + r
+#pragma unroll
+        for (int i = 0; i < T::S_PW; ++i) {
+            const int idx = (i * T::W + w) % T::S_I;
+            if (idx < BM / 64) {  // rows of x
+                const int word = idx * 64 + lane, at = word / T::MI;
+                const int row = at / 32 * (32 * T::MI) + word % T::MI * 32 + at % 32;
+                const int m = min(row, g.M - 1 - m0);
+                s_src[i] = uniform_ptr(g.sf + m0 / 64 * g.sf_band);
+                s_step[i] = g.sf_step;
+                s_off[i] = (uint32_t)(m / 64) * (uint32_t)g.sf_band + (uint32_t)(m % 64) * (uint32_t)g.sf_row;
+            } else {  // weight rows
+                const int word = (idx - BM / 64) * 64 + lane, at = word / T::NI;
+                const int blk = at / 32 * T::NI + word % T::NI;
+                s_src[i] = uniform_ptr(g.w_sf + (int64_t)nb0 * g.KT * kBlockScales);
+                s_step[i] = kBlockScales;
+                s_off[i] = (uint32_t)min(blk, g.blocks - 1 - nb0) * (uint32_t)g.KT * kBlockScales + (uint32_t)(at % 32) * 4;
+            }
+        }
+    };
     // DMA instruction i of unit u of x: K-steps k0 + AK u and on.  Columns past the last are those of the row's last chunk:
     // the weights there are 0.
     auto issue_a = [&](int i, int u) {
@@ -261,10 +278,6 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
     };
 
     v16f acc[T::MI][T::NI];
-#pragma unroll
-    for (int i = 0; i < T::MI; ++i)
-#pragma unroll
-        for (int j = 0; j < T::NI; ++j) acc[i][j] = v16f{};
     constexpr int FRAGS = T::MI + T::NI, SLOTS = T::MI * T::NI, PER = (FRAGS + SLOTS - 1) / SLOTS;
     Half f0, f1;
     Scales sc, sn;
@@ -313,14 +326,14 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
     };
     constexpr std::true_type yes{};
     constexpr std::false_type no{};
-    int t = 0;
+    // the first stages of a tile
+    auto fill = [&]() {
     if constexpr (AK == 1) {
         // a split of fewer than NS K-steps fills the ring with its last one
 #pragma unroll
         for (int u = 0; u < NS; ++u)
 #pragma unroll
             for (int i = 0; i < (u < NS - 1 ? T::D : D1); ++i) issue1(i, u, min(u, n - 1));
-        wait_and_barrier<(NS - 2) * T::D + D1>();
     } else {  // in the order of the steps that would come before the first: of each stage, and of unit 0 with stage 1
 #pragma unroll
         for (int i = 0; i < T::D; ++i) issue1(i, 0, 0);
@@ -334,8 +347,17 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
         for (int i = 0; i < A1; ++i) issue_a(i, 1);
 #pragma unroll
         for (int i = 0; i < D1; ++i) issue1(i, 3, 3);
-        wait_and_barrier<2 * T::D + A1 + D1>();
     }
+    };
+    take(id);
+    fill();
+    for (;;) {
+    wait_and_barrier<AK == 1 ? (NS - 2) * T::D + D1 : 2 * T::D + A1 + D1>();
+#pragma unroll
+    for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+        for (int j = 0; j < T::NI; ++j) acc[i][j] = v16f{};
+    int t = 0;
 #pragma unroll
     for (int i = 0; i < FRAGS; ++i) read1(i, f0, 0, 0);
     read_scales(sc, 0);
@@ -400,29 +422,76 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
         }
     }
 
-    // nothing is on its way to LDS when the workgroup ends: a split of fewer than NS K-steps filled the ring all the same
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // Nothing is on its way to LDS any more (a split of fewer than NS K-steps filled the ring all the same), and no wave
+    // reads it.  The next tile's first stages are loaded while this one's outputs are stored.
+    wait_and_barrier<0>();
+    const int om = m0 + wm0, on = n0 + wn0;
+    float* part = g.partial + (int64_t)z * g.M * partial_columns(g);
+    id += stride;
+    if (id < last) {
+        take(id);
+        fill();
+    }
 
     // ---- outputs: weight rows are laid so that lane r of blocks 2b and 2b + 1 holds outputs 2r and 2r + 1 of their 64
-    float* part = g.partial + (int64_t)z * g.M * partial_columns(g);
+    const int l = fresh_lane(), c = 2 * (l & 31), p = l >> 5;
+    if (g.splits > 1) {
 #pragma unroll
-    for (int i = 0; i < T::MI; ++i)
+        for (int i = 0; i < T::MI; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int row = m0 + wm0 + i * 32 + 8 * (e / 4) + 4 * q + e % 4;
-            if (row >= g.M) continue;
+            for (int e = 0; e < 16; ++e) {
+                const int row = om + i * 32 + 8 * (e / 4) + 4 * p + e % 4;
 #pragma unroll
-            for (int j = 0; j < T::NI; j += 2) {
-                const int col = n0 + wn0 + j * 32 + 2 * r;
-                if (g.splits > 1) {
-                    if (col < partial_columns(g))
+                for (int j = 0; j < T::NI; j += 2) {
+                    const int col = on + j * 32 + c;
+                    if (row < g.M && col < partial_columns(g))
                         *reinterpret_cast<f32x2*>(part + (int64_t)row * partial_columns(g) + col) =
                             f32x2{acc[i][j][e], acc[i][j + 1][e]};
-                } else {
-                    store2(g, row, col, acc[i][j][e], acc[i][j + 1][e]);
                 }
             }
-        }
+    } else if (g.wide) {
+        auto store = [&](auto stream) {
+        // 8 rows at a time through LDS, where each wave has a place of its own, so that a store is whole lines
+        constexpr int COLS = BN / WN, LANES = COLS / 8;  // lanes of a row
+        uint8_t* place = smem + T::RING + w * T::OUT;
+#pragma unroll
+        for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int j = 0; j < T::NI; j += 2)
+                        *reinterpret_cast<uint32_t*>(place + ((4 * p + k) * COLS + j * 32 + c) * 2) =
+                            pack_bf16(acc[i][j][e + k], acc[i][j + 1][e + k]);
+#pragma unroll
+                for (int h = 0; h < 8 * LANES / 64; ++h) {
+                    const int at = h * 64 + l;
+                    const v4i v = *reinterpret_cast<const v4i*>(place + at * 16);
+                    const int row = om + i * 32 + 2 * e + at / LANES, col = on + at % LANES * 8;
+                    if (row < g.M && col < g.N) {
+                        v4i* to = reinterpret_cast<v4i*>(g.y + (int64_t)row * g.y_stride + col);
+                        if constexpr (decltype(stream)::value) __builtin_nontemporal_store(v, to);
+                        else *to = v;
+                    }
+                }
+            }
+        };
+        if (g.stream) store(yes);
+        else store(no);
+    } else {
+#pragma unroll
+        for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int row = om + i * 32 + 8 * (e / 4) + 4 * p + e % 4;
+#pragma unroll
+                for (int j = 0; j < T::NI; j += 2)
+                    if (row < g.M) store2(g, row, on + j * 32 + c, acc[i][j][e], acc[i][j + 1][e]);
+            }
+    }
+    if (id >= last) break;
+    }
 }
 
 // Few rows of x: what counts is how the weights stream in.  A workgroup takes a block of 32 weight rows over all columns,
@@ -550,23 +619,46 @@ __global__ __launch_bounds__(kThreads) void join_kernel(Args g) {
 }
 
 // Scales of x by K-step, [M/64][KT][64 rows][4 B], zeros behind the last column: what a tile loads of a K-step is then
-// whole lines.
+// whole lines.  A workgroup turns 64 rows of kTurn K-steps in LDS, so that it reads along rows and writes along K-steps.
+constexpr int kTurn = 8;
 __global__ __launch_bounds__(kThreads) void tile_scales_kernel(const uint8_t* sf, int M, int blocks, int KT, uint32_t* out) {
-    const int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
-    const int64_t band = i / (64 * KT);
-    const int kt = (int)(i % (64 * KT) / 64);
-    const int64_t row = band * 64 + i % 64;
-    if (row >= M) return;
-    uint32_t v = 0;
-    for (int b = 0; b < 4; ++b)
-        if (kt * 4 + b < blocks) v |= (uint32_t)sf[row * blocks + kt * 4 + b] << (8 * b);
-    out[i] = v;
+    __shared__ uint32_t words[kTurn][65];
+    const int chunks = (KT + kTurn - 1) / kTurn;
+    const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, band = block / chunks;
+    const int kt0 = (int)(block % chunks) * kTurn;
+    if (band * 64 >= M) return;
+    const int kt = kt0 + threadIdx.x % kTurn;
+#pragma unroll
+    for (int i = 0; i < 64; i += kThreads / kTurn) {
+        const int in = i + threadIdx.x / kTurn;
+        const int64_t row = band * 64 + in;
+        uint32_t v = 0;
+        if (row < M && kt < KT) {
+            const uint8_t* at = sf + row * blocks + kt * 4;
+            if (blocks % 4 == 0) {
+                v = *reinterpret_cast<const uint32_t*>(at);
+            } else {
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    if (kt * 4 + b < blocks) v |= (uint32_t)at[b] << (8 * b);
+            }
+        }
+        words[threadIdx.x % kTurn][in] = v;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kTurn; i += kThreads / 64) {
+        const int step = i + threadIdx.x / 64;
+        if (kt0 + step < KT) out[(band * KT + kt0 + step) * 64 + threadIdx.x % 64] = words[step][threadIdx.x % 64];
+    }
 }
 
 template <int FMT, int BM, int BN, int WM, int WN, int AK, int NS, int OCC>
 void go(const Args& g, hipStream_t stream) {
     const int tiles = g.mt * g.nt * g.splits, share = (tiles + kNumXcd - 1) / kNumXcd;
-    hipLaunchKernelGGL((tile_kernel<FMT, BM, BN, WM, WN, AK, NS, OCC>), dim3((unsigned)(share * kNumXcd)), dim3(64 * WM * WN), 0,
+    constexpr int PER_CU = 160 * 1024 / Tile<FMT, BM, BN, WM, WN, AK, NS>::LDS;
+    const int per_xcd = std::min(share, std::max(1, cu_count() / kNumXcd * PER_CU));
+    hipLaunchKernelGGL((tile_kernel<FMT, BM, BN, WM, WN, AK, NS, OCC>), dim3((unsigned)(per_xcd * kNumXcd)), dim3(64 * WM * WN), 0,
                        stream, g);
 }
 
@@ -578,26 +670,47 @@ void few(const Args& g, hipStream_t stream) {
 
 }  // namespace
 
-constexpr int kFewRows = 128;
-constexpr int kLongSteps = 5;  // K-steps that the ring of two units of x needs
+constexpr int kFewRows = 64, kSomeRows = 128;
+constexpr int kLongSteps = 5;    // K-steps that the ring of two units of x needs
 constexpr int kFillTiles = 256;  // a workgroup for every compute unit
+constexpr int kMostSplits = 16, kLeastSteps = 4;
 
+// The kernel with the least estimated time, in microseconds (measured at 2048 .. 16384 rows, 2016 .. 7168 columns and 512
+// .. 7168 outputs, most within 15%): a K-step of a 256 x 256 tile takes 0.8 (E2M1) or 1.3 (E4M3), one of a 128 x 128 tile
+// 0.27 or 0.4, or 0.36 or 0.42 for each of two that share a compute unit; to lay out the scales takes 4, to join splits 4 and their
+// partial sums' way to memory and back.
 MxLinearChoice choose_mx_linear(int M, int N, int K, int format) {
     MxLinearChoice c{};
     const int KT = mx_steps(K);
-    if (M <= kFewRows) {
+    const bool four = format == MOE_E2M1;
+    c.splits = 1;
+    const int64_t groups = ((int64_t)M + 63) / 64, blocks = mx_column_blocks(N);
+    // up to 64 rows (64 x 7168 x 4096: 8.7 us, 12.3 in tiles), or 128 where all workgroups run at once (128 rows: 8.9, 14.8)
+    if (M <= kFewRows || (M <= kSomeRows && groups * blocks <= kFillTiles)) {
         c.kernel = 2;
         c.tokens = M <= 32 ? 32 : 64;
         c.columns = 32;
-        c.splits = 1;
         return c;
     }
     const int64_t big = (((int64_t)M + 255) / 256) * (((int64_t)N + 255) / 256);
-    c.kernel = big >= kFillTiles ? 0 : 1;
-    c.tokens = c.columns = c.kernel == 0 ? 256 : 128;
-    const int64_t tiles = (((int64_t)M + c.tokens - 1) / c.tokens) * (((int64_t)N + c.columns - 1) / c.columns);
-    c.splits = 1;
-    while (tiles * c.splits < kFillTiles && KT / (c.splits * 2) >= 4 && c.splits < 16) c.splits *= 2;
+    const int64_t small = (((int64_t)M + 127) / 128) * (((int64_t)N + 127) / 128);
+    const double lay_out = K % kStep != 0 ? 4.0 : 0.0;
+    double best = (double)((big + kFillTiles - 1) / kFillTiles) * (KT * (four ? 0.8 : 1.3) + 5.0) + 9.0;
+    c.tokens = c.columns = 256;
+    for (int splits = 1; splits <= kMostSplits; splits *= 2) {
+        const int64_t tiles = small * splits;
+        if (splits > 1 && (KT / splits < kLeastSteps || small >= kFillTiles || tiles > 2 * kFillTiles)) break;
+        const double at_once = tiles <= kFillTiles ? 1.0 : 2.0 * (double)((tiles + 2 * kFillTiles - 1) / (2 * kFillTiles));
+        const double step = at_once > 1.0 ? (four ? 0.36 : 0.42) : (four ? 0.27 : 0.4);
+        double us = at_once * ((KT + splits - 1) / splits) * step + 4.0 + lay_out;
+        if (splits > 1) us += 4.0 + (double)splits * M * N * 8.0 / 6e6;
+        if (us >= best) continue;
+        best = us;
+        c.kernel = 1;
+        c.tokens = c.columns = 128;
+        c.splits = splits;
+    }
+    // A K-step's word of a row is a line of its own, so large tiles want them laid out; and words start at multiples of 4.
     c.tile_scales = K % kStep != 0 || c.kernel == 0;
     c.scale_bytes = c.tile_scales ? ((size_t)M + 63) / 64 * KT * 256 : 0;
     c.partial_bytes = c.splits > 1 ? (size_t)c.splits * M * mx_column_blocks(N) * 32 * 4 : 0;
@@ -605,10 +718,10 @@ MxLinearChoice choose_mx_linear(int M, int N, int K, int format) {
 }
 
 size_t most_mx_linear_workspace(int M, int N, int K, int format) {
-    // More tokens in as many tiles need more, and from kFillTiles tile rows on nothing is split: the most is that of M,
-    // or of the last number of tokens of some smaller number of tile rows.
+    // What scales take grows with the tokens.  Partial sums are had by fewer than kFillTiles tile rows alone, and there
+    // more tokens may need less: all of them are asked.
     size_t most = M > 0 ? choose_mx_linear(M, N, K, format).workspace_bytes() : 0;
-    for (int m = std::min(M / 16, kFillTiles * 8) * 16; m > 0; m -= 16)
+    for (int m = std::min(M, kFillTiles * 128); m > 0; --m)
         most = std::max(most, choose_mx_linear(m, N, K, format).workspace_bytes());
     return most;
 }
@@ -636,13 +749,15 @@ hipError_t launch_mx_linear(const MxLinearArgs& a, const MxLinearChoice& c, hipS
         g.sf_band = (int64_t)g.KT * 256;
         g.sf_row = 4;
         g.sf_step = 256;
-        const int64_t words = ((int64_t)a.M + 63) / 64 * 64 * g.KT;
-        hipLaunchKernelGGL(tile_scales_kernel, wide_grid((words + kThreads - 1) / kThreads), dim3(kThreads), 0, stream, a.x_sf,
-                           a.M, a.K / 32, g.KT, reinterpret_cast<uint32_t*>(a.ws));
+        const int64_t turns = ((int64_t)a.M + 63) / 64 * ((g.KT + kTurn - 1) / kTurn);
+        hipLaunchKernelGGL(tile_scales_kernel, wide_grid(turns), dim3(kThreads), 0, stream, a.x_sf, a.M, a.K / 32, g.KT,
+                           reinterpret_cast<uint32_t*>(a.ws));
     }
     g.splits = c.splits;
     g.per = (g.KT + c.splits - 1) / c.splits;
     g.splits = (g.KT + g.per - 1) / g.per;  // none without a K-step
+    g.wide = a.N % 8 == 0 && a.y_stride % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
+    g.stream = (int64_t)a.M * a.N * 2 > 32ll << 20;
     g.mt = (a.M + c.tokens - 1) / c.tokens;
     g.nt = (a.N + c.columns - 1) / c.columns;
     if (c.kernel == 2) {
