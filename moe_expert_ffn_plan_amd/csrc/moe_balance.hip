@@ -200,20 +200,28 @@ __device__ __forceinline__ int sequence_of(const int64_t* off, int row, int S, i
     return lo - 1;
 }
 
-// The same of one row for a whole wave, which compares 64 offsets at a time.
-__device__ __forceinline__ int sequence_of_wave(const int64_t* off, int row, int S, int T) {
-    if (!off) return 0;
+// The same of one row for a whole wave, which compares 64 offsets at a time, and the sequence's rows: in front of the first
+// sequence those up to it, behind the last those from its end on.
+struct Span {
+    int s, begin, end;
+};
+__device__ __forceinline__ Span span_of_wave(const int64_t* off, int row, int S, int T) {
+    if (!off) return {0, 0, T};
     const int lane = threadIdx.x % 64;
     int lo = 0, n = S + 1;  // the offsets in question
+    Span r{-1, 0, T};
     while (n > 0) {
         const int step = (n + 63) / 64, at = lane * step;
-        const bool before = at < n && offset_at(off, lo + at, T) <= row;
-        const int c = __popcll(__ballot(before));
+        const int o = at < n ? offset_at(off, lo + at, T) : T;
+        const int c = __popcll(__ballot(at < n && o <= row));
+        if (c > 0) r.begin = __builtin_amdgcn_readlane(o, c - 1);
+        if (c < 64 && c * step < n) r.end = __builtin_amdgcn_readlane(o, c);
         if (c == 0) break;
         lo += (c - 1) * step + 1;
         n = min(step - 1, n - (c - 1) * step - 1);
     }
-    return lo - 1;
+    r.s = lo - 1;
+    return r;
 }
 // The sequence of a row at or behind sequence s's first: often s or the next one.
 __device__ __forceinline__ int sequence_from(const int64_t* off, int s, int row, int S, int T) {
@@ -340,16 +348,18 @@ __global__ __launch_bounds__(kWaves<V> * 64) void balance_parts_kernel(BalanceAr
         for (int s = tid; s < a.S; s += THREADS) tickets[s] = 0;
     int row = (int)min((int64_t)b * tile, (int64_t)a.T);
     const int last = min(row + tile, a.T);
-    int s = sequence_of_wave(a.seq_offsets, row, a.S, a.T);
+    const Span span = span_of_wave(a.seq_offsets, row, a.S, a.T);
+    int s = span.s, next = span.end;
     while (row < last && s < a.S) {
         if (s < 0) {  // rows in front of the first sequence
-            row = max(row, offset_at(a.seq_offsets, 0, a.T));
+            row = max(row, next);
             s = 0;
+            next = offset_at(a.seq_offsets, 1, a.T);
             continue;
         }
-        const int end = min(last, offset_at(a.seq_offsets, s + 1, a.T));
+        const int end = min(last, next);
         if (end <= row) {
-            ++s;
+            if (++s < a.S) next = offset_at(a.seq_offsets, s + 1, a.T);
             continue;
         }
         sum_rows<TYPE, SCORE, L, V, VEC>(a, row, end, sums);
@@ -367,7 +377,7 @@ __global__ __launch_bounds__(kWaves<V> * 64) void balance_parts_kernel(BalanceAr
         }
         __syncthreads();
         row = end;
-        ++s;
+        if (++s < a.S) next = offset_at(a.seq_offsets, s + 1, a.T);
     }
 }
 
@@ -416,7 +426,7 @@ __global__ __launch_bounds__(kWaves<V> * 64) void balance_whole_kernel(BalanceAr
 }
 
 // One workgroup per sequence and kColumns experts; the last of a sequence to arrive adds up the loss.
-constexpr int kColumns = 32, kJoinThreads = 1024;
+constexpr int kColumns = 16, kJoinThreads = 1024;
 static_assert(kMaxGateExperts / kColumns <= 64, "a lane for each of a sequence's workgroups");
 __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs a, int tile, const float* parts,
                                                                     uint32_t* tickets, float* sums) {
@@ -454,7 +464,7 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs 
     }
     __syncthreads();
     if (threadIdx.x >= 64) return;
-    // one wave: its halves add the even and the odd parts of the columns
+    // one wave, whose lanes of a column take its parts in turn
     rows = (int)threadIdx.x < LANES ? rows_part[threadIdx.x] : 0;
     z = (int)threadIdx.x < LANES ? z_part[threadIdx.x] : 0.0f;
     rows = sum_over_lanes<64>(rows);
@@ -462,12 +472,15 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs 
     share = 0.0f;
     count = 0;
 #pragma unroll 4
-    for (int q = part; q < LANES; q += 2) {
+    for (int q = part; q < LANES; q += 64 / kColumns) {
         share += share_part[q][col];
         count += count_part[q][col];
     }
-    share += __shfl_xor(share, kColumns);
-    count += __shfl_xor(count, kColumns);
+#pragma unroll
+    for (int d = kColumns; d < 64; d *= 2) {
+        share += __shfl_xor(share, d);
+        count += __shfl_xor(count, d);
+    }
     share = rows > 0 ? share / (float)rows : 0.0f;
     const bool mine = threadIdx.x < kColumns && e < a.E;
     if (mine) {
@@ -551,9 +564,9 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
     const char* in = static_cast<const char*>(a.logits) + t * a.stride * SIZE;
     char* out = static_cast<char*>(a.d_logits) + t * a.E * SIZE;
     int64_t at_k = t * a.k + lane;
-    // the sequence of the last row, and its rows; before the first row none is known
-    int s = sequence_of_wave(a.seq_offsets, (int)min(first + threadIdx.x / 64 * (64 / L), (int64_t)a.T), a.S, a.T);
-    int begin = 0, end = 0;
+    // the sequence of the last row, and its rows; `known`: what of it the rows need is loaded
+    int s = 0, begin = 0, end = 0;
+    bool known = false;
     float pull[V], zpull = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) pull[i] = 0.0f;
@@ -575,17 +588,28 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
                 }
             }
         }
+        if (step == 0) {  // of the wave's first row
+            const Span span =
+                span_of_wave(a.seq_offsets, (int)min(first + threadIdx.x / 64 * (64 / L), (int64_t)a.T), a.S, a.T);
+            s = span.s;
+            begin = span.begin;
+            end = span.end;
+        }
         if (t < begin || t >= end) {
+            known = false;
             s = sequence_from(a.seq_offsets, max(s, 0), (int)t, a.S, a.T);
             begin = offset_at(a.seq_offsets, min(s, a.S), a.T);
             if (s == 0 && t < begin) {  // in front of the first sequence
                 s = -1;
                 end = begin;
                 begin = 0;
-                continue;
+            } else {
+                end = s < a.S ? offset_at(a.seq_offsets, s + 1, a.T) : a.T;
             }
-            end = s < a.S ? offset_at(a.seq_offsets, s + 1, a.T) : a.T;
-            if (s < 0 || s >= a.S) continue;
+        }
+        if (s < 0 || s >= a.S) continue;
+        if (!known) {
+            known = true;
             const float n = a.rows ? (float)a.rows[s] : 0.0f;
             if (a.d_loss) {
                 int c[V], low = 0, high = 0;  // halves of the sum, which may pass 32 bits
@@ -603,7 +627,6 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
             }
             zpull = a.d_z && n > 0.0f ? 2.0f * a.d_z[s] / n : 0.0f;
         }
-        if (s < 0 || s >= a.S) continue;
 
         float less[V];  // of sigmoid scores
         const RowSum r = shares<SCORE, L, V, SCORE == MOE_SCORE_SIGMOID>(l, p, less);
@@ -791,7 +814,7 @@ hipError_t launch_balance(const BalanceArgs& a, void* ws, hipStream_t stream) {
     if (a.T <= kWholeRows) return hipSuccess;
     const int chunks = (a.E + kColumns - 1) / kColumns;
     // lanes for the parts that a sequence has if all are as long
-    const int threads = l.tiles / a.S >= 16 ? kJoinThreads : kThreads;
+    const int threads = l.tiles / a.S >= 64 ? kJoinThreads : kThreads;
     hipLaunchKernelGGL(balance_join_kernel, wide_grid((int64_t)chunks * a.S), dim3((unsigned)threads), 0, stream, a, l.tile,
                        reinterpret_cast<const float*>(base + l.parts), reinterpret_cast<uint32_t*>(base + l.tickets),
                        reinterpret_cast<float*>(base + l.sums));
