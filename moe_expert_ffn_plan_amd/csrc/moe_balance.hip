@@ -425,19 +425,20 @@ __global__ __launch_bounds__(kWaves<V> * 64) void balance_whole_kernel(BalanceAr
     }
 }
 
-// One workgroup per sequence and kColumns experts; the last of a sequence to arrive adds up the loss.
-constexpr int kColumns = 16, kJoinThreads = 1024;
-static_assert(kMaxGateExperts / kColumns <= 64, "a lane for each of a sequence's workgroups");
+// One workgroup per sequence and COLUMNS experts; the last of a sequence to arrive adds up the loss.
+constexpr int kFewColumns = 16, kJoinThreads = 1024;
+static_assert(kMaxGateExperts / kFewColumns <= 64, "a lane for each of a sequence's workgroups");
+template <int COLUMNS>
 __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs a, int tile, const float* parts,
                                                                     uint32_t* tickets, float* sums) {
-    __shared__ float share_part[kJoinThreads / kColumns][kColumns], z_part[kJoinThreads / kColumns];
-    __shared__ int count_part[kJoinThreads / kColumns][kColumns], rows_part[kJoinThreads / kColumns];
-    const int LANES = blockDim.x / kColumns;
-    const int chunks = (a.E + kColumns - 1) / kColumns;
+    __shared__ float share_part[kJoinThreads / COLUMNS][COLUMNS], z_part[kJoinThreads / COLUMNS];
+    __shared__ int count_part[kJoinThreads / COLUMNS][COLUMNS], rows_part[kJoinThreads / COLUMNS];
+    const int LANES = blockDim.x / COLUMNS;
+    const int chunks = (a.E + COLUMNS - 1) / COLUMNS;
     const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     if (block >= (int64_t)chunks * a.S) return;
     const int s = (int)(block / chunks), chunk = (int)(block % chunks);
-    const int col = threadIdx.x % kColumns, part = threadIdx.x / kColumns, e = chunk * kColumns + col;
+    const int col = threadIdx.x % COLUMNS, part = threadIdx.x / COLUMNS, e = chunk * COLUMNS + col;
     const int from = offset_at(a.seq_offsets, s, a.T), to = offset_at(a.seq_offsets, s + 1, a.T);
     const int64_t words = Slot::words(a.E);
     float share = 0.0f, z = 0.0f;
@@ -472,17 +473,17 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs 
     share = 0.0f;
     count = 0;
 #pragma unroll 4
-    for (int q = part; q < LANES; q += 64 / kColumns) {
+    for (int q = part; q < LANES; q += 64 / COLUMNS) {
         share += share_part[q][col];
         count += count_part[q][col];
     }
 #pragma unroll
-    for (int d = kColumns; d < 64; d *= 2) {
+    for (int d = COLUMNS; d < 64; d *= 2) {
         share += __shfl_xor(share, d);
         count += __shfl_xor(count, d);
     }
     share = rows > 0 ? share / (float)rows : 0.0f;
-    const bool mine = threadIdx.x < kColumns && e < a.E;
+    const bool mine = threadIdx.x < COLUMNS && e < a.E;
     if (mine) {
         if (a.counts) a.counts[(int64_t)s * a.E + e] = count;
         if (a.share) a.share[(int64_t)s * a.E + e] = share;
@@ -532,7 +533,7 @@ BalanceLayout balance_layout(int T, int E, int S) {
     auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, kAlign); return at; };
     l.parts = take((size_t)((int64_t)l.tiles + S) * Slot::words(E) * 4);
     l.tickets = take((size_t)S * 4);
-    l.sums = take((size_t)S * ((E + kColumns - 1) / kColumns) * 8);
+    l.sums = take((size_t)S * ((E + kFewColumns - 1) / kFewColumns) * 8);
     l.total = o;
     return l;
 }
@@ -812,12 +813,21 @@ hipError_t launch_balance(const BalanceArgs& a, void* ws, hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (a.T <= kWholeRows) return hipSuccess;
-    const int chunks = (a.E + kColumns - 1) / kColumns;
-    // lanes for the parts that a sequence has if all are as long
-    const int threads = l.tiles / a.S >= 64 ? kJoinThreads : kThreads;
-    hipLaunchKernelGGL(balance_join_kernel, wide_grid((int64_t)chunks * a.S), dim3((unsigned)threads), 0, stream, a, l.tile,
-                       reinterpret_cast<const float*>(base + l.parts), reinterpret_cast<uint32_t*>(base + l.tickets),
-                       reinterpret_cast<float*>(base + l.sums));
+    // Long sequences: 16 experts a workgroup, 64 lanes to add up each one's parts (65536 x 384 in one sequence, 256
+    // parts: 6.0 us to 7.2 with 32 and 32).  Shorter ones: 32, half as many to wait for (16384 x 256 in 13, 20 parts:
+    // 5.4 us to 7.6).  The shortest: a quarter of the lanes, so that sequences share a compute unit.
+    const int64_t each = l.tiles / a.S;
+    auto join = [&](auto columns, int threads) {
+        constexpr int COLUMNS = decltype(columns)::value;
+        const int64_t chunks = (a.E + COLUMNS - 1) / COLUMNS;
+        hipLaunchKernelGGL(balance_join_kernel<COLUMNS>, wide_grid(chunks * a.S), dim3((unsigned)threads), 0, stream, a, l.tile,
+                           reinterpret_cast<const float*>(base + l.parts), reinterpret_cast<uint32_t*>(base + l.tickets),
+                           reinterpret_cast<float*>(base + l.sums));
+    };
+    if (each >= 64)
+        join(std::integral_constant<int, kFewColumns>{}, kJoinThreads);
+    else
+        join(std::integral_constant<int, 2 * kFewColumns>{}, each >= 16 ? kJoinThreads : kThreads);
     return hipGetLastError();
 }
 
