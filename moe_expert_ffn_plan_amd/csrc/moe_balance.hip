@@ -234,16 +234,19 @@ __device__ __forceinline__ int sequence_from(const int64_t* off, int s, int row,
 
 // ---- forward: sums of a tile's rows, then sums of the tiles
 //
-// Tiles of `tile` rows, whatever the sequences.  The part of sequence s in tile b goes to slot b + s: from one part to
-// the next b or s grows, so no two parts share a slot, and there are at most tiles + S of them.  The second kernel adds
-// a sequence's parts in the order of their tiles; nothing depends on the order of workgroups or of atomics (those on
-// counts are whole numbers).
+// The rows are cut into tiles, whatever the sequences.  A sequence within one tile is summed and written by a workgroup
+// of its own.  What a tile has of longer ones, the tail of one that began before it and the head of one that goes on
+// behind it, goes to slots, and a second kernel adds a sequence's parts in the order of their tiles.  So a workgroup has
+// two parts to sum at most, however many sequences there are, and nothing depends on the order of workgroups or of
+// atomics (those on counts are whole numbers).
+// The part of sequence s in tile b has slot b + s (from one part to the next b or s grows, so no two share one) or, with
+// more sequences than tiles, 2 b and, where the sequence begins in the tile, 2 b + 1.
+__device__ __forceinline__ int64_t slot_of(int b, int s, bool head, bool many) {
+    return many ? 2 * (int64_t)b + head : (int64_t)b + s;
+}
 struct Slot {  // floats and ints of one part: shares [E], counts [E], then rows and z
     static __host__ __device__ __forceinline__ int64_t words(int E) { return 2 * (int64_t)E + 2; }
 };
-
-//
-// Few rows are one launch: a workgroup takes a sequence whole and writes its results.
 
 // Waves of a workgroup of the first kernel; their sums, one per expert, stand side by side in LDS.
 template <int V>
@@ -338,61 +341,52 @@ __device__ __forceinline__ void sum_rows(const BalanceArgs& a, int row, int end,
 }
 
 template <int TYPE, int SCORE, int L, int V, bool VEC>
-__global__ __launch_bounds__(kWaves<V> * 64) void balance_parts_kernel(BalanceArgs a, int tile, float* parts,
-                                                                       uint32_t* tickets) {
-    extern __shared__ float smem[];
-    const RowSums<V> sums(smem, a.E);
-    constexpr int THREADS = kWaves<V> * 64;
-    const int tid = threadIdx.x, b = blockIdx.x;
-    if (b == 0)
-        for (int s = tid; s < a.S; s += THREADS) tickets[s] = 0;
-    int row = (int)min((int64_t)b * tile, (int64_t)a.T);
-    const int last = min(row + tile, a.T);
-    const Span span = span_of_wave(a.seq_offsets, row, a.S, a.T);
-    int s = span.s, next = span.end;
-    while (row < last && s < a.S) {
-        if (s < 0) {  // rows in front of the first sequence
-            row = max(row, next);
-            s = 0;
-            next = offset_at(a.seq_offsets, 1, a.T);
-            continue;
-        }
-        const int end = min(last, next);
-        if (end <= row) {
-            if (++s < a.S) next = offset_at(a.seq_offsets, s + 1, a.T);
-            continue;
-        }
-        sum_rows<TYPE, SCORE, L, V, VEC>(a, row, end, sums);
-        float* out = parts + (int64_t)(b + s) * Slot::words(a.E);
-        for (int e = tid; e < a.E; e += THREADS) {
-            out[e] = sums.share_of(e, a.E);
-            reinterpret_cast<int*>(out)[a.E + e] = sums.count[e];
-        }
-        if (tid == 0) {
-            int n;
-            float z;
-            sums.row_totals(n, z);
-            reinterpret_cast<int*>(out)[2 * a.E] = n;
-            out[2 * a.E + 1] = z;
-        }
-        __syncthreads();
-        row = end;
-        if (++s < a.S) next = offset_at(a.seq_offsets, s + 1, a.T);
-    }
-}
-
-// A sequence whole.
-template <int TYPE, int SCORE, int L, int V, bool VEC>
-__global__ __launch_bounds__(kWaves<V> * 64) void balance_whole_kernel(BalanceArgs a) {
+__global__ __launch_bounds__(kWaves<V> * 64) void balance_rows_kernel(BalanceArgs a, int tile, int tiles, float* parts,
+                                                                      uint32_t* tickets) {
     extern __shared__ float smem[];
     __shared__ float cross_part[kWaves<V>];
     __shared__ int count_part[kWaves<V>];
     const RowSums<V> sums(smem, a.E);
     constexpr int THREADS = kWaves<V> * 64;
     const int tid = threadIdx.x;
-    const int64_t s = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (block < tiles) {  // none where all rows are of one tile
+        const int b = (int)block, row = b * tile, last = min(row + tile, a.T);
+        if (tid == 0 && b < a.S) tickets[b] = 0;
+        Span span = span_of_wave(a.seq_offsets, row, a.S, a.T);
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+            int from = row, to = min(span.end, last);
+            bool has = span.begin < row;
+            if (part == 1) {
+                if (last == a.T) break;
+                if (span.end <= last) span = span_of_wave(a.seq_offsets, last - 1, a.S, a.T);
+                from = span.begin;
+                to = last;
+                has = span.begin >= row && span.end > last;
+            }
+            if (!has || span.s < 0 || span.s >= a.S) continue;
+            sum_rows<TYPE, SCORE, L, V, VEC>(a, from, to, sums);
+            float* out = parts + slot_of(b, span.s, part == 1, a.S > tiles) * Slot::words(a.E);
+            for (int e = tid; e < a.E; e += THREADS) {
+                out[e] = sums.share_of(e, a.E);
+                reinterpret_cast<int*>(out)[a.E + e] = sums.count[e];
+            }
+            if (tid == 0) {
+                int n;
+                float z;
+                sums.row_totals(n, z);
+                reinterpret_cast<int*>(out)[2 * a.E] = n;
+                out[2 * a.E + 1] = z;
+            }
+            __syncthreads();
+        }
+        return;
+    }
+    const int64_t s = block - tiles;
     if (s >= a.S) return;
     const int from = offset_at(a.seq_offsets, (int)s, a.T), to = max(from, offset_at(a.seq_offsets, (int)s + 1, a.T));
+    if (tiles > 0 && to > from && from / tile != (to - 1) / tile) return;  // the tiles'
     sum_rows<TYPE, SCORE, L, V, VEC>(a, from, to, sums);
     int n;
     float z;
@@ -425,36 +419,48 @@ __global__ __launch_bounds__(kWaves<V> * 64) void balance_whole_kernel(BalanceAr
     }
 }
 
-// One workgroup per sequence and COLUMNS experts; the last of a sequence to arrive adds up the loss.
+// One workgroup per sequence and COLUMNS experts (or, where there are more sequences than tiles, per border of two tiles,
+// for the sequence that crosses it first there); the last of a sequence to arrive adds up the loss.
 constexpr int kFewColumns = 16, kJoinThreads = 1024;
 static_assert(kMaxGateExperts / kFewColumns <= 64, "a lane for each of a sequence's workgroups");
 template <int COLUMNS>
-__global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs a, int tile, const float* parts,
-                                                                    uint32_t* tickets, float* sums) {
+__global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs a, int tile, int borders,
+                                                                    const float* parts, uint32_t* tickets, float* sums) {
     __shared__ float share_part[kJoinThreads / COLUMNS][COLUMNS], z_part[kJoinThreads / COLUMNS];
     __shared__ int count_part[kJoinThreads / COLUMNS][COLUMNS], rows_part[kJoinThreads / COLUMNS];
     const int LANES = blockDim.x / COLUMNS;
     const int chunks = (a.E + COLUMNS - 1) / COLUMNS;
     const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-    if (block >= (int64_t)chunks * a.S) return;
-    const int s = (int)(block / chunks), chunk = (int)(block % chunks);
+    int s = (int)(block / chunks), from, to;
+    const int chunk = (int)(block % chunks);
+    if (borders == 0) {
+        if (s >= a.S) return;
+        from = offset_at(a.seq_offsets, s, a.T);
+        to = offset_at(a.seq_offsets, s + 1, a.T);
+    } else {
+        if (s >= borders) return;
+        const int border = (s + 1) * tile;
+        const Span span = span_of_wave(a.seq_offsets, border, a.S, a.T);
+        s = span.s;
+        from = span.begin;
+        to = span.end;
+        if (s < 0 || s >= a.S || from >= border || from / tile != border / tile - 1) return;
+    }
+    const int first = from / tile, end = (to - 1) / tile + 1, index = borders ? first : s;
+    if (to <= from || end == first + 1) return;  // written already
     const int col = threadIdx.x % COLUMNS, part = threadIdx.x / COLUMNS, e = chunk * COLUMNS + col;
-    const int from = offset_at(a.seq_offsets, s, a.T), to = offset_at(a.seq_offsets, s + 1, a.T);
     const int64_t words = Slot::words(a.E);
     float share = 0.0f, z = 0.0f;
     int count = 0, rows = 0;
-    if (to > from) {
-        const int first = from / tile, end = (to - 1) / tile + 1;
-        const int at = min(e, a.E - 1);
+    const int at = min(e, a.E - 1);
 #pragma unroll 8
-        for (int b = first + part; b < end; b += LANES) {
-            const float* in = parts + (int64_t)(b + s) * words;
-            share += in[at];
-            count += reinterpret_cast<const int*>(in)[a.E + at];
-            if (col == 0) {
-                rows += reinterpret_cast<const int*>(in)[2 * a.E];
-                z += in[2 * a.E + 1];
-            }
+    for (int b = first + part; b < end; b += LANES) {
+        const float* in = parts + slot_of(b, s, b == first, borders > 0) * words;
+        share += in[at];
+        count += reinterpret_cast<const int*>(in)[a.E + at];
+        if (col == 0) {
+            rows += reinterpret_cast<const int*>(in)[2 * a.E];
+            z += in[2 * a.E + 1];
         }
     }
     share_part[part][col] = share;
@@ -495,15 +501,15 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs 
     if (!a.loss) return;
     const float cross = over_lanes<Sum, 64>(mine && count > 0 ? (float)count * share : 0.0f);
     const int total = sum_over_lanes<64>(mine ? count : 0);
-    float* out = sums + ((int64_t)s * chunks + chunk) * 2;
+    float* out = sums + ((int64_t)index * chunks + chunk) * 2;
     uint32_t before = 0;
     if (threadIdx.x == 0) {
         __hip_atomic_store(out, cross, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         __hip_atomic_store(out + 1, __int_as_float(total), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        before = __hip_atomic_fetch_add(&tickets[s], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        before = __hip_atomic_fetch_add(&tickets[index], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
     }
     if (__builtin_amdgcn_readfirstlane(before) != (uint32_t)chunks - 1) return;
-    const float* all = sums + ((int64_t)s * chunks + min((int)threadIdx.x, chunks - 1)) * 2;
+    const float* all = sums + ((int64_t)index * chunks + min((int)threadIdx.x, chunks - 1)) * 2;
     const float part_cross = __hip_atomic_load(all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     const int part_total = __float_as_int(__hip_atomic_load(all + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
     const bool has = (int)threadIdx.x < chunks;
@@ -512,14 +518,17 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs 
     if (threadIdx.x == 0) a.loss[s] = n > 0 ? (float)a.E * v / (float)n : 0.0f;
 }
 
-// Rows of a tile: a tile for every compute unit, and no more parts than the second kernel can add quickly.
-int tile_rows(int T) {
+// Rows of a tile.  Where one tile has all rows there is one launch: the shortest inputs, and sequences of some 128 rows
+// up to 1024 (us for one tile / several; E = 256: 300 rows in 5 sequences 4.9 / 10.0, 1000 in 7 7.0 / 10.7; but 300 in
+// one 10.2 / 8.2, 1000 in one 26 / 8.8).  Else a tile for every compute unit, and no more parts than the second kernel can
+// add quickly (65536 x 384: 28.4 us for tiles of 256 rows, 41.8 for 512, 27.9 for 128; 16384 x 256: 12.1, 11.7, 16.8
+// for 64, 128, 32).
+int tile_rows(int T, int S) {
     int tile = 16;
+    if (T <= 256 || (T <= 1024 && T / 128 <= S)) return 1024;
     while (tile < 1024 && (int64_t)tile * 256 < T) tile *= 2;
     return tile;
 }
-// Few enough rows for one launch: no sequence has more.
-constexpr int kWholeRows = 512;
 
 struct BalanceLayout {
     int tile, tiles;
@@ -527,13 +536,14 @@ struct BalanceLayout {
 };
 BalanceLayout balance_layout(int T, int E, int S) {
     BalanceLayout l;
-    l.tile = tile_rows(T);
-    l.tiles = (T + l.tile - 1) / l.tile;
+    l.tile = tile_rows(T, S);
+    l.tiles = (int)(((int64_t)T + l.tile - 1) / l.tile);
     size_t o = 0;
     auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, kAlign); return at; };
-    l.parts = take((size_t)((int64_t)l.tiles + S) * Slot::words(E) * 4);
-    l.tickets = take((size_t)S * 4);
-    l.sums = take((size_t)S * ((E + kFewColumns - 1) / kFewColumns) * 8);
+    const size_t longer = std::max(1, std::min(l.tiles, S));  // sequences of more than one tile, at most
+    l.parts = take((l.tiles + longer) * Slot::words(E) * 4);
+    l.tickets = take(longer * 4);
+    l.sums = take(longer * ((E + kFewColumns - 1) / kFewColumns) * 8);
     l.total = o;
     return l;
 }
@@ -753,12 +763,10 @@ bool vector_rows(const void* base, int64_t stride, int E, int type) {
 template <int TYPE, int SCORE, int L, int V, bool VEC>
 void parts_go(const BalanceArgs& a, const BalanceLayout& l, char* ws, hipStream_t stream) {
     const size_t lds = RowSums<V>::bytes(a.E);
-    if (a.T <= kWholeRows)
-        hipLaunchKernelGGL((balance_whole_kernel<TYPE, SCORE, L, V, VEC>), wide_grid(a.S), dim3(kWaves<V> * 64), lds, stream, a);
-    else
-        hipLaunchKernelGGL((balance_parts_kernel<TYPE, SCORE, L, V, VEC>), dim3((unsigned)l.tiles), dim3(kWaves<V> * 64), lds,
-                           stream, a, l.tile, reinterpret_cast<float*>(ws + l.parts),
-                           reinterpret_cast<uint32_t*>(ws + l.tickets));
+    const int tiles = l.tiles > 1 ? l.tiles : 0;
+    hipLaunchKernelGGL((balance_rows_kernel<TYPE, SCORE, L, V, VEC>), wide_grid((int64_t)tiles + a.S), dim3(kWaves<V> * 64),
+                       lds, stream, a, l.tile, tiles, reinterpret_cast<float*>(ws + l.parts),
+                       reinterpret_cast<uint32_t*>(ws + l.tickets));
 }
 template <int TYPE, int SCORE, int L, int V, bool VEC, int KV>
 void grad_go(const GateGradArgs& a, hipStream_t stream) {
@@ -812,15 +820,17 @@ hipError_t launch_balance(const BalanceArgs& a, void* ws, hipStream_t stream) {
              });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (a.T <= kWholeRows) return hipSuccess;
+    if (l.tiles <= 1) return hipSuccess;
     // Long sequences: 16 experts a workgroup, 64 lanes to add up each one's parts (65536 x 384 in one sequence, 256
     // parts: 6.0 us to 7.2 with 32 and 32).  Shorter ones: 32, half as many to wait for (16384 x 256 in 13, 20 parts:
     // 5.4 us to 7.6).  The shortest: a quarter of the lanes, so that sequences share a compute unit.
     const int64_t each = l.tiles / a.S;
+    const int borders = a.S > l.tiles ? l.tiles - 1 : 0;
     auto join = [&](auto columns, int threads) {
         constexpr int COLUMNS = decltype(columns)::value;
         const int64_t chunks = (a.E + COLUMNS - 1) / COLUMNS;
-        hipLaunchKernelGGL(balance_join_kernel<COLUMNS>, wide_grid(chunks * a.S), dim3((unsigned)threads), 0, stream, a, l.tile,
+        hipLaunchKernelGGL(balance_join_kernel<COLUMNS>, wide_grid(chunks * (borders ? borders : a.S)), dim3((unsigned)threads), 0,
+                           stream, a, l.tile, borders,
                            reinterpret_cast<const float*>(base + l.parts), reinterpret_cast<uint32_t*>(base + l.tickets),
                            reinterpret_cast<float*>(base + l.sums));
     };

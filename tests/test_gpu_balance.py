@@ -103,6 +103,28 @@ def test_forward_many_short_sequences(gpu):
     check_forward(l, ids, torch.arange(1401).div(2, rounding_mode="floor"), gpu, S=1400)
 
 
+# sequences within tiles of 16 rows (64 of 20000), over their borders, at them, and fewer, as many or more than there are tiles
+TILED = {"borders": [0, 16, 32, 48, 64, 128, 256, 599, 600], "around borders": [0, 15, 17, 31, 32, 33, 47, 65, 300, 303, 600],
+         "long ones between short": [0, 1, 2, 100, 101, 102, 103, 400, 401, 400 + 16, 580], "gaps": [20, 21, 90, 580, 581],
+         "more than tiles": sorted([*range(0, 600, 7), *([300] * 10)]), "as many": [*range(0, 590, 16)] + [600],
+         "one of all between empty ones": [0] * 30 + [600] * 30, "rows behind": [*range(0, 100)], "none": [600] * 50}
+
+
+@pytest.mark.parametrize("name", list(TILED))
+def test_forward_tiles(gpu, name):
+    print(name, flush=True)
+    l, ids, _ = inputs(600, 36, 3, 4, F32, 0.1)
+    check_forward(l, ids, torch.tensor(TILED[name]), gpu, S=len(TILED[name]) - 1)
+
+
+@pytest.mark.parametrize("T,E,S", [(256, 40, 1), (256, 40, 400), (257, 40, 1), (257, 40, 2), (1024, 33, 7), (1024, 33, 8), (1025, 33, 64),
+                                   (1025, 33, 65), (1025, 33, 66), (1500, 48, 1300), (20000, 16, 312), (20000, 16, 313), (20000, 16, 4000)])
+def test_forward_sequences_by_tiles(gpu, T, E, S):
+    print(T, E, S, flush=True)
+    l, ids, off = inputs(T, E, 2, T + S, F32, 0.1, S)
+    check_forward(l, ids, off, gpu, S=S)
+
+
 def test_forward_falling_offsets_stay_in_bounds(gpu):
     """Their result is not specified; the call ends, and leaves what it was not given alone."""
     l, ids, _ = inputs(300, 20, 3, 4)
