@@ -252,33 +252,47 @@ struct Slot {  // floats and ints of one part: shares [E], counts [E], then rows
 template <int V>
 constexpr int kWaves = V > 8 ? 8 : 16;
 
-template <int V>
+constexpr int kShortWaves = 4;
+
 struct RowSums {  // in LDS
-    float* share;  // [kWaves][E]
+    int waves, E;
+    float* share;  // [waves][E]
     int* count;    // [E]
-    int* rows;     // [kWaves]
-    float* z;      // [kWaves]
-    __device__ __forceinline__ RowSums(float* smem, int E)
-        : share(smem), count(reinterpret_cast<int*>(smem + kWaves<V> * E)), rows(count + E),
-          z(reinterpret_cast<float*>(rows + kWaves<V>)) {}
-    static size_t bytes(int E) { return ((size_t)(kWaves<V> + 1) * E + 2 * kWaves<V>) * 4; }
-    __device__ __forceinline__ float share_of(int e, int E) const {
+    int* rows;     // [waves]
+    float* z;      // [waves]
+    __device__ __forceinline__ RowSums(float* smem, int waves, int E)
+        : waves(waves), E(E), share(smem), count(reinterpret_cast<int*>(smem + waves * E)), rows(count + E),
+          z(reinterpret_cast<float*>(rows + waves)) {}
+    static size_t bytes(int waves, int E) { return ((size_t)(waves + 1) * E + 2 * waves) * 4; }
+    template <int W>
+    __device__ __forceinline__ float share_over(int e) const {
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves<V>; ++w) v += share[w * E + e];
+        for (int w = 0; w < W; ++w) v += share[w * E + e];
         return v;
     }
-    __device__ __forceinline__ void row_totals(int& n, float& zz) const {
+    template <int V>
+    __device__ __forceinline__ float share_of(int e) const {
+        return waves == kWaves<V> ? share_over<kWaves<V>>(e) : share_over<kShortWaves>(e);
+    }
+    template <int W>
+    __device__ __forceinline__ void row_sums(int& n, float& zz) const {
         n = 0;
         zz = 0.0f;
-        for (int w = 0; w < kWaves<V>; ++w) n += rows[w], zz += z[w];
+#pragma unroll
+        for (int w = 0; w < W; ++w) n += rows[w], zz += z[w];
+    }
+    template <int V>
+    __device__ __forceinline__ void row_totals(int& n, float& zz) const {
+        if (waves == kWaves<V>) row_sums<kWaves<V>>(n, zz);
+        else row_sums<kShortWaves>(n, zz);
     }
 };
 
 // Sums of rows [row, end), of the whole workgroup; the caller's next barrier is behind the last read of them.
 template <int TYPE, int SCORE, int L, int V, bool VEC>
-__device__ __forceinline__ void sum_rows(const BalanceArgs& a, int row, int end, const RowSums<V>& out) {
-    constexpr int THREADS = kWaves<V> * 64, GROUPS = THREADS / L;
+__device__ __forceinline__ void sum_rows(const BalanceArgs& a, int row, int end, const RowSums& out) {
+    const int THREADS = blockDim.x, GROUPS = THREADS / L;
     constexpr int U = V > 8 ? 1 : 2;  // rows of a group that are loaded together
     const int tid = threadIdx.x, lane = tid % L, group = tid / L, wave = tid / 64;
     for (int e = tid; e < a.E; e += THREADS) out.count[e] = 0;
@@ -346,13 +360,13 @@ __global__ __launch_bounds__(kWaves<V> * 64) void balance_rows_kernel(BalanceArg
     extern __shared__ float smem[];
     __shared__ float cross_part[kWaves<V>];
     __shared__ int count_part[kWaves<V>];
-    const RowSums<V> sums(smem, a.E);
-    constexpr int THREADS = kWaves<V> * 64;
+    const int THREADS = blockDim.x, waves = THREADS / 64;
+    const RowSums sums(smem, waves, a.E);
     const int tid = threadIdx.x;
     const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     if (block < tiles) {  // none where all rows are of one tile
         const int b = (int)block, row = b * tile, last = min(row + tile, a.T);
-        if (tid == 0 && b < a.S) tickets[b] = 0;
+        if (tid == 0 && tickets && b < a.S) tickets[b] = 0;
         Span span = span_of_wave(a.seq_offsets, row, a.S, a.T);
 #pragma unroll 1
         for (int part = 0; part < 2; ++part) {
@@ -369,13 +383,13 @@ __global__ __launch_bounds__(kWaves<V> * 64) void balance_rows_kernel(BalanceArg
             sum_rows<TYPE, SCORE, L, V, VEC>(a, from, to, sums);
             float* out = parts + slot_of(b, span.s, part == 1, a.S > tiles) * Slot::words(a.E);
             for (int e = tid; e < a.E; e += THREADS) {
-                out[e] = sums.share_of(e, a.E);
+                out[e] = sums.template share_of<V>(e);
                 reinterpret_cast<int*>(out)[a.E + e] = sums.count[e];
             }
             if (tid == 0) {
                 int n;
                 float z;
-                sums.row_totals(n, z);
+                sums.template row_totals<V>(n, z);
                 reinterpret_cast<int*>(out)[2 * a.E] = n;
                 out[2 * a.E + 1] = z;
             }
@@ -390,12 +404,12 @@ __global__ __launch_bounds__(kWaves<V> * 64) void balance_rows_kernel(BalanceArg
     sum_rows<TYPE, SCORE, L, V, VEC>(a, from, to, sums);
     int n;
     float z;
-    sums.row_totals(n, z);
+    sums.template row_totals<V>(n, z);
     float cross = 0.0f;
     int total = 0;
     for (int e = tid; e < a.E; e += THREADS) {
         const int count = sums.count[e];
-        const float share = n > 0 ? sums.share_of(e, a.E) / (float)n : 0.0f;
+        const float share = n > 0 ? sums.template share_of<V>(e) / (float)n : 0.0f;
         if (a.counts) a.counts[s * a.E + e] = count;
         if (a.share) a.share[s * a.E + e] = share;
         if (count > 0) cross += (float)count * share;
@@ -414,48 +428,60 @@ __global__ __launch_bounds__(kWaves<V> * 64) void balance_rows_kernel(BalanceArg
     }
     __syncthreads();
     if (tid == 0) {
-        for (int w = 1; w < kWaves<V>; ++w) cross += cross_part[w], total += count_part[w];
+        for (int w = 1; w < waves; ++w) cross += cross_part[w], total += count_part[w];
         a.loss[s] = total > 0 ? (float)a.E * cross / (float)total : 0.0f;
     }
 }
 
-// One workgroup per sequence and COLUMNS experts (or, where there are more sequences than tiles, per border of two tiles,
-// for the sequence that crosses it first there); the last of a sequence to arrive adds up the loss.
-constexpr int kFewColumns = 16, kJoinThreads = 1024;
-static_assert(kMaxGateExperts / kFewColumns <= 64, "a lane for each of a sequence's workgroups");
-template <int COLUMNS>
-__global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs a, int tile, int borders,
-                                                                    const float* parts, uint32_t* tickets, float* sums) {
-    __shared__ float share_part[kJoinThreads / COLUMNS][COLUMNS], z_part[kJoinThreads / COLUMNS];
-    __shared__ int count_part[kJoinThreads / COLUMNS][COLUMNS], rows_part[kJoinThreads / COLUMNS];
-    const int LANES = blockDim.x / COLUMNS;
-    const int chunks = (a.E + COLUMNS - 1) / COLUMNS;
-    const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-    int s = (int)(block / chunks), from, to;
-    const int chunk = (int)(block % chunks);
+// The sequence that a workgroup of the second kernel joins, s < 0 for none: the `index`th or, where there are more
+// sequences than tiles, the one that crosses its first border of two tiles there; its tiles are [first, end).
+struct Longer {
+    int s, first, end;
+};
+__device__ __forceinline__ Longer longer_of(const BalanceArgs& a, int64_t index, int tile, int borders) {
+    const Longer none{-1, 0, 0};
+    int s = (int)index, from, to;
     if (borders == 0) {
-        if (s >= a.S) return;
+        if (index >= a.S) return none;
         from = offset_at(a.seq_offsets, s, a.T);
         to = offset_at(a.seq_offsets, s + 1, a.T);
     } else {
-        if (s >= borders) return;
+        if (index >= borders) return none;
         const int border = (s + 1) * tile;
         const Span span = span_of_wave(a.seq_offsets, border, a.S, a.T);
         s = span.s;
         from = span.begin;
         to = span.end;
-        if (s < 0 || s >= a.S || from >= border || from / tile != border / tile - 1) return;
+        if (s < 0 || s >= a.S || from >= border || from / tile != border / tile - 1) return none;
     }
-    const int first = from / tile, end = (to - 1) / tile + 1, index = borders ? first : s;
-    if (to <= from || end == first + 1) return;  // written already
-    const int col = threadIdx.x % COLUMNS, part = threadIdx.x / COLUMNS, e = chunk * COLUMNS + col;
+    const int first = from / tile, end = (to - 1) / tile + 1;
+    if (to <= from || end == first + 1) return none;  // written already
+    return {s, first, end};
+}
+
+// One workgroup per sequence and kColumns experts; the last of a sequence to arrive adds up the loss.
+constexpr int kColumns = 16, kJoinThreads = 1024;
+static_assert(kMaxGateExperts / kColumns <= 64, "a lane for each of a sequence's workgroups");
+static_assert(kMaxGateExperts <= kJoinThreads, "a lane for each expert");
+__global__ __launch_bounds__(kJoinThreads) void balance_long_join_kernel(BalanceArgs a, int tile, const float* parts,
+                                                                         uint32_t* tickets, float* sums) {
+    __shared__ float share_part[kJoinThreads / kColumns][kColumns], z_part[kJoinThreads / kColumns];
+    __shared__ int count_part[kJoinThreads / kColumns][kColumns], rows_part[kJoinThreads / kColumns];
+    constexpr int LANES = kJoinThreads / kColumns;
+    const int chunks = (a.E + kColumns - 1) / kColumns;
+    const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    const int chunk = (int)(block % chunks);
+    const Longer q = longer_of(a, block / chunks, tile, 0);
+    if (q.s < 0) return;
+    const int s = q.s, first = q.first, end = q.end;
+    const int col = threadIdx.x % kColumns, part = threadIdx.x / kColumns, e = chunk * kColumns + col;
     const int64_t words = Slot::words(a.E);
     float share = 0.0f, z = 0.0f;
     int count = 0, rows = 0;
     const int at = min(e, a.E - 1);
 #pragma unroll 8
     for (int b = first + part; b < end; b += LANES) {
-        const float* in = parts + slot_of(b, s, b == first, borders > 0) * words;
+        const float* in = parts + slot_of(b, s, b == first, false) * words;
         share += in[at];
         count += reinterpret_cast<const int*>(in)[a.E + at];
         if (col == 0) {
@@ -479,17 +505,17 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs 
     share = 0.0f;
     count = 0;
 #pragma unroll 4
-    for (int q = part; q < LANES; q += 64 / COLUMNS) {
+    for (int q = part; q < LANES; q += 64 / kColumns) {
         share += share_part[q][col];
         count += count_part[q][col];
     }
 #pragma unroll
-    for (int d = COLUMNS; d < 64; d *= 2) {
+    for (int d = kColumns; d < 64; d *= 2) {
         share += __shfl_xor(share, d);
         count += __shfl_xor(count, d);
     }
     share = rows > 0 ? share / (float)rows : 0.0f;
-    const bool mine = threadIdx.x < COLUMNS && e < a.E;
+    const bool mine = threadIdx.x < kColumns && e < a.E;
     if (mine) {
         if (a.counts) a.counts[(int64_t)s * a.E + e] = count;
         if (a.share) a.share[(int64_t)s * a.E + e] = share;
@@ -501,15 +527,15 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs 
     if (!a.loss) return;
     const float cross = over_lanes<Sum, 64>(mine && count > 0 ? (float)count * share : 0.0f);
     const int total = sum_over_lanes<64>(mine ? count : 0);
-    float* out = sums + ((int64_t)index * chunks + chunk) * 2;
+    float* out = sums + ((int64_t)s * chunks + chunk) * 2;
     uint32_t before = 0;
     if (threadIdx.x == 0) {
         __hip_atomic_store(out, cross, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         __hip_atomic_store(out + 1, __int_as_float(total), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        before = __hip_atomic_fetch_add(&tickets[index], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        before = __hip_atomic_fetch_add(&tickets[s], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
     }
     if (__builtin_amdgcn_readfirstlane(before) != (uint32_t)chunks - 1) return;
-    const float* all = sums + ((int64_t)index * chunks + min((int)threadIdx.x, chunks - 1)) * 2;
+    const float* all = sums + ((int64_t)s * chunks + min((int)threadIdx.x, chunks - 1)) * 2;
     const float part_cross = __hip_atomic_load(all, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     const int part_total = __float_as_int(__hip_atomic_load(all + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
     const bool has = (int)threadIdx.x < chunks;
@@ -518,20 +544,85 @@ __global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(BalanceArgs 
     if (threadIdx.x == 0) a.loss[s] = n > 0 ? (float)a.E * v / (float)n : 0.0f;
 }
 
-// Rows of a tile.  Where one tile has all rows there is one launch: the shortest inputs, and sequences of some 128 rows
-// up to 1024 (us for one tile / several; E = 256: 300 rows in 5 sequences 4.9 / 10.0, 1000 in 7 7.0 / 10.7; but 300 in
-// one 10.2 / 8.2, 1000 in one 26 / 8.8).  Else a tile for every compute unit, and no more parts than the second kernel can
-// add quickly (65536 x 384: 28.4 us for tiles of 256 rows, 41.8 for 512, 27.9 for 128; 16384 x 256: 12.1, 11.7, 16.8
-// for 64, 128, 32).
+// One workgroup per sequence, or per border where there are more sequences than tiles: a lane for every expert and, of few
+// experts, several lanes for its parts in turn.
+__global__ __launch_bounds__(kJoinThreads) void balance_short_join_kernel(BalanceArgs a, int tile, int borders,
+                                                                          const float* parts) {
+    __shared__ float share_part[kJoinThreads], cross_part[kJoinThreads / 64];
+    __shared__ int count_part[kJoinThreads], total_part[kJoinThreads / 64];
+    const Longer q = longer_of(a, (int64_t)blockIdx.y * gridDim.x + blockIdx.x, tile, borders);
+    if (q.s < 0) return;
+    const int width = (a.E + 63) / 64 * 64, lanes = blockDim.x / width;
+    const int e = threadIdx.x % width, part = threadIdx.x / width;
+    const int64_t words = Slot::words(a.E);
+    const int at = min(e, a.E - 1);
+    float share = 0.0f, z = 0.0f;
+    int count = 0, rows = 0;
+#pragma unroll 8
+    for (int b = q.first + part; b < q.end; b += lanes) {
+        const float* in = parts + slot_of(b, q.s, b == q.first, borders > 0) * words;
+        share += in[at];
+        count += reinterpret_cast<const int*>(in)[a.E + at];
+    }
+    for (int b = q.first + (int)threadIdx.x % 64; b < q.end; b += 64) {  // each wave for itself
+        const float* in = parts + slot_of(b, q.s, b == q.first, borders > 0) * words;
+        rows += reinterpret_cast<const int*>(in)[2 * a.E];
+        z += in[2 * a.E + 1];
+    }
+    rows = sum_over_lanes<64>(rows);
+    z = over_lanes<Sum, 64>(z);
+    share_part[threadIdx.x] = share;
+    count_part[threadIdx.x] = count;
+    __syncthreads();
+    float cross = 0.0f;
+    int total = 0;
+    if (part == 0 && e < a.E) {
+        for (int l = 1; l < lanes; ++l) {
+            share += share_part[l * width + e];
+            count += count_part[l * width + e];
+        }
+        share = rows > 0 ? share / (float)rows : 0.0f;
+        if (a.counts) a.counts[(int64_t)q.s * a.E + e] = count;
+        if (a.share) a.share[(int64_t)q.s * a.E + e] = share;
+        if (count > 0) cross = (float)count * share;
+        total = count;
+    }
+    if (threadIdx.x == 0) {
+        if (a.rows) a.rows[q.s] = rows;
+        if (a.z) a.z[q.s] = rows > 0 ? z / (float)rows : 0.0f;
+    }
+    if (!a.loss) return;
+    cross = over_lanes<Sum, 64>(cross);
+    total = sum_over_lanes<64>(total);
+    if (threadIdx.x % 64 == 0) {
+        cross_part[threadIdx.x / 64] = cross;
+        total_part[threadIdx.x / 64] = total;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < width / 64; ++w) cross += cross_part[w], total += total_part[w];
+        a.loss[q.s] = total > 0 ? (float)a.E * cross / (float)total : 0.0f;
+    }
+}
+
+// Rows of a tile.  One tile, and one launch, where sequences have some 192 rows and all together 1024 at most (us for one
+// tile / several, E = 256: 300 rows in 5 sequences 4.9 / 10.0, 1000 in 7 7.4 / 10.7; in one sequence 190 rows 7.9 / 8.0,
+// 256 9.5 / 8.6, 1000 26 / 8.8).  Else a tile for every compute unit, and no more parts than the second kernel adds quickly
+// (65536 x 384: 28.4 us for tiles of 256 rows, 41.8 for 512, 27.9 for 128; 16384 x 256: 12.1, 11.7, 16.8 for 64, 128, 32).
 int tile_rows(int T, int S) {
     int tile = 16;
-    if (T <= 256 || (T <= 1024 && T / 128 <= S)) return 1024;
+    if (T <= 1024 && T <= 192 * (int64_t)S) return 1024;
     while (tile < 1024 && (int64_t)tile * 256 < T) tile *= 2;
     return tile;
 }
 
+// Sequences of so many tiles or more, if all are as long, are joined by 16 experts a workgroup, shorter ones by one each:
+// a workgroup that takes a ticket costs the others' time (its release writes back the cache), so that 13 sequences of 20
+// tiles take 14.7 us to 17.4, 50 of 5 13.4 to 27.4; one of 256, which leaves a single workgroup, is the other way about.
+constexpr int kLong = 64;
 struct BalanceLayout {
     int tile, tiles;
+    bool long_join;
     size_t parts = 0, tickets = 0, sums = 0, total = 0;
 };
 BalanceLayout balance_layout(int T, int E, int S) {
@@ -540,10 +631,10 @@ BalanceLayout balance_layout(int T, int E, int S) {
     l.tiles = (int)(((int64_t)T + l.tile - 1) / l.tile);
     size_t o = 0;
     auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, kAlign); return at; };
-    const size_t longer = std::max(1, std::min(l.tiles, S));  // sequences of more than one tile, at most
-    l.parts = take((l.tiles + longer) * Slot::words(E) * 4);
-    l.tickets = take(longer * 4);
-    l.sums = take(longer * ((E + kFewColumns - 1) / kFewColumns) * 8);
+    l.long_join = l.tiles >= kLong * (int64_t)S;
+    l.parts = take(((size_t)l.tiles + std::max(1, std::min(l.tiles, S))) * Slot::words(E) * 4);
+    l.tickets = take((size_t)(l.long_join ? S : 0) * 4);
+    l.sums = take((size_t)(l.long_join ? S : 0) * ((E + kColumns - 1) / kColumns) * 8);
     l.total = o;
     return l;
 }
@@ -762,11 +853,14 @@ bool vector_rows(const void* base, int64_t stride, int E, int type) {
 
 template <int TYPE, int SCORE, int L, int V, bool VEC>
 void parts_go(const BalanceArgs& a, const BalanceLayout& l, char* ws, hipStream_t stream) {
-    const size_t lds = RowSums<V>::bytes(a.E);
+    // Four waves for short sequences, of which most of a larger workgroup would have no rows (300 sequences of 55 rows
+    // 14.5 us to 18.9, 4000 of 4 19 to 53).
+    const int rows = a.T / a.S, waves = a.S > 1 && rows <= 64 ? kShortWaves : kWaves<V>;
+    const size_t lds = RowSums::bytes(waves, a.E);
     const int tiles = l.tiles > 1 ? l.tiles : 0;
-    hipLaunchKernelGGL((balance_rows_kernel<TYPE, SCORE, L, V, VEC>), wide_grid((int64_t)tiles + a.S), dim3(kWaves<V> * 64),
+    hipLaunchKernelGGL((balance_rows_kernel<TYPE, SCORE, L, V, VEC>), wide_grid((int64_t)tiles + a.S), dim3(waves * 64),
                        lds, stream, a, l.tile, tiles, reinterpret_cast<float*>(ws + l.parts),
-                       reinterpret_cast<uint32_t*>(ws + l.tickets));
+                       l.long_join ? reinterpret_cast<uint32_t*>(ws + l.tickets) : nullptr);
 }
 template <int TYPE, int SCORE, int L, int V, bool VEC, int KV>
 void grad_go(const GateGradArgs& a, hipStream_t stream) {
@@ -821,23 +915,19 @@ hipError_t launch_balance(const BalanceArgs& a, void* ws, hipStream_t stream) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (l.tiles <= 1) return hipSuccess;
-    // Long sequences: 16 experts a workgroup, 64 lanes to add up each one's parts (65536 x 384 in one sequence, 256
-    // parts: 6.0 us to 7.2 with 32 and 32).  Shorter ones: 32, half as many to wait for (16384 x 256 in 13, 20 parts:
-    // 5.4 us to 7.6).  The shortest: a quarter of the lanes, so that sequences share a compute unit.
-    const int64_t each = l.tiles / a.S;
-    const int borders = a.S > l.tiles ? l.tiles - 1 : 0;
-    auto join = [&](auto columns, int threads) {
-        constexpr int COLUMNS = decltype(columns)::value;
-        const int64_t chunks = (a.E + COLUMNS - 1) / COLUMNS;
-        hipLaunchKernelGGL(balance_join_kernel<COLUMNS>, wide_grid(chunks * (borders ? borders : a.S)), dim3((unsigned)threads), 0,
-                           stream, a, l.tile, borders,
-                           reinterpret_cast<const float*>(base + l.parts), reinterpret_cast<uint32_t*>(base + l.tickets),
-                           reinterpret_cast<float*>(base + l.sums));
-    };
-    if (each >= 64)
-        join(std::integral_constant<int, kFewColumns>{}, kJoinThreads);
-    else
-        join(std::integral_constant<int, 2 * kFewColumns>{}, each >= 16 ? kJoinThreads : kThreads);
+    const float* parts = reinterpret_cast<const float*>(base + l.parts);
+    if (l.long_join) {
+        const int64_t chunks = (a.E + kColumns - 1) / kColumns;
+        hipLaunchKernelGGL(balance_long_join_kernel, wide_grid(chunks * a.S), dim3(kJoinThreads), 0, stream, a, l.tile, parts,
+                           reinterpret_cast<uint32_t*>(base + l.tickets), reinterpret_cast<float*>(base + l.sums));
+    } else {
+        const int borders = a.S > l.tiles ? l.tiles - 1 : 0;
+        const int width = (a.E + 63) / 64 * 64, lanes = kJoinThreads / width;
+        // no more lanes for an expert than its sequence has parts, if all are as long
+        const int threads = width * std::max(1, std::min(lanes, l.tiles / a.S));
+        hipLaunchKernelGGL(balance_short_join_kernel, wide_grid(borders ? borders : a.S), dim3((unsigned)threads), 0, stream,
+                           a, l.tile, borders, parts);
+    }
     return hipGetLastError();
 }
 
