@@ -640,9 +640,10 @@ MOE_API int moe_mx_linear(const moe_mx_linear_shape* shape, const uint8_t* x, co
  * of that loss and of the gate's weights goes back to the logits.
  * Rows belong to sequences: with seq_offsets (int64 [S + 1], not falling)
  * sequence s is the rows seq_offsets[s] .. seq_offsets[s + 1] - 1; offsets
- * below 0 count as 0, those above T as T, and where one lies below the one
- * before it the sequence is empty.  Rows in no sequence take no part; without
- * seq_offsets S is 1 and all rows are its.  Of sequence s:
+ * below 0 count as 0, those above T as T (where they fall, results are not
+ * specified; nothing outside the arrays is read or written).  Rows in no
+ * sequence take no part; without seq_offsets S is 1 and all rows are its.  Of
+ * sequence s:
  *   p[t, e]      row t's scores over their sum: softmax(l), or sigmoid(l) /
  *                sum of sigmoid(l); 0 for a row whose logits are all
  *                -infinity (padding)
@@ -658,7 +659,8 @@ MOE_API int moe_mx_linear(const moe_mx_linear_shape* shape, const uint8_t* x, co
  * constants; counts may be summed over ranks first.  Sums hold in FP32 in an
  * order that depends on the shape alone: the same inputs give the same bits.
  * A NaN or +infinity among a row's logits makes the p of that row NaN (with
- * sigmoid scores an infinity stands for 1).
+ * sigmoid scores an infinity stands for 1).  Exponentials below 2^-126 of a
+ * row's largest may count as 0; a z beyond FP32's range is infinite.
  * Limits: num_tokens 0 .. 2^28 - 1, T * topk < 2^30; num_experts 1 .. 1024;
  * topk 1 .. min(64, num_experts); num_seqs 1 .. 2^20, 1 without seq_offsets,
  * S * E < 2^30; scale finite; logits_stride >= num_experts. */
