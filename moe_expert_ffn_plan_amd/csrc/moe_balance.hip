@@ -239,6 +239,9 @@ __device__ __forceinline__ int sequence_from(const int64_t* off, int s, int row,
 // behind it, goes to slots, and a second kernel adds a sequence's parts in the order of their tiles.  So a workgroup has
 // two parts to sum at most, however many sequences there are, and nothing depends on the order of workgroups or of
 // atomics (those on counts are whole numbers).
+// Bound by memory where rows are many (65536 x 384 FP32: 22.5 us, 4.6 TB/s, and 6 to join) and by the chain of a
+// workgroup where they are few (128 x 256: 6.0 us): loads, two instructions an exponential, sums over lanes and waves.
+// Two rows of a group are loaded together; more in flight gained nothing.
 // The part of sequence s in tile b has slot b + s (from one part to the next b or s grows, so no two share one) or, with
 // more sequences than tiles, 2 b and, where the sequence begins in the tile, 2 b + 1.
 __device__ __forceinline__ int64_t slot_of(int b, int s, bool head, bool many) {
@@ -254,45 +257,33 @@ constexpr int kWaves = V > 8 ? 8 : 16;
 
 constexpr int kShortWaves = 4;
 
+template <int W>
 struct RowSums {  // in LDS
-    int waves, E;
-    float* share;  // [waves][E]
+    int E;
+    float* share;  // [W][E]
     int* count;    // [E]
-    int* rows;     // [waves]
-    float* z;      // [waves]
-    __device__ __forceinline__ RowSums(float* smem, int waves, int E)
-        : waves(waves), E(E), share(smem), count(reinterpret_cast<int*>(smem + waves * E)), rows(count + E),
-          z(reinterpret_cast<float*>(rows + waves)) {}
-    static size_t bytes(int waves, int E) { return ((size_t)(waves + 1) * E + 2 * waves) * 4; }
-    template <int W>
-    __device__ __forceinline__ float share_over(int e) const {
+    int* rows;     // [W]
+    float* z;      // [W]
+    __device__ __forceinline__ RowSums(float* smem, int E)
+        : E(E), share(smem), count(reinterpret_cast<int*>(smem + W * E)), rows(count + E), z(reinterpret_cast<float*>(rows + W)) {}
+    static size_t bytes(int E) { return ((size_t)(W + 1) * E + 2 * W) * 4; }
+    __device__ __forceinline__ float share_of(int e) const {
         float v = 0.0f;
 #pragma unroll
         for (int w = 0; w < W; ++w) v += share[w * E + e];
         return v;
     }
-    template <int V>
-    __device__ __forceinline__ float share_of(int e) const {
-        return waves == kWaves<V> ? share_over<kWaves<V>>(e) : share_over<kShortWaves>(e);
-    }
-    template <int W>
-    __device__ __forceinline__ void row_sums(int& n, float& zz) const {
+    __device__ __forceinline__ void row_totals(int& n, float& zz) const {
         n = 0;
         zz = 0.0f;
-#pragma unroll
         for (int w = 0; w < W; ++w) n += rows[w], zz += z[w];
-    }
-    template <int V>
-    __device__ __forceinline__ void row_totals(int& n, float& zz) const {
-        if (waves == kWaves<V>) row_sums<kWaves<V>>(n, zz);
-        else row_sums<kShortWaves>(n, zz);
     }
 };
 
 // Sums of rows [row, end), of the whole workgroup; the caller's next barrier is behind the last read of them.
-template <int TYPE, int SCORE, int L, int V, bool VEC>
-__device__ __forceinline__ void sum_rows(const BalanceArgs& a, int row, int end, const RowSums& out) {
-    const int THREADS = blockDim.x, GROUPS = THREADS / L;
+template <int TYPE, int SCORE, int L, int V, bool VEC, int W>
+__device__ __forceinline__ void sum_rows(const BalanceArgs& a, int row, int end, const RowSums<W>& out) {
+    constexpr int THREADS = W * 64, GROUPS = THREADS / L;
     constexpr int U = V > 8 ? 1 : 2;  // rows of a group that are loaded together
     const int tid = threadIdx.x, lane = tid % L, group = tid / L, wave = tid / 64;
     for (int e = tid; e < a.E; e += THREADS) out.count[e] = 0;
@@ -354,14 +345,14 @@ __device__ __forceinline__ void sum_rows(const BalanceArgs& a, int row, int end,
     __syncthreads();
 }
 
-template <int TYPE, int SCORE, int L, int V, bool VEC>
-__global__ __launch_bounds__(kWaves<V> * 64) void balance_rows_kernel(BalanceArgs a, int tile, int tiles, float* parts,
+template <int TYPE, int SCORE, int L, int V, bool VEC, int W>
+__global__ __launch_bounds__(W * 64) void balance_rows_kernel(BalanceArgs a, int tile, int tiles, float* parts,
                                                                       uint32_t* tickets) {
     extern __shared__ float smem[];
-    __shared__ float cross_part[kWaves<V>];
-    __shared__ int count_part[kWaves<V>];
-    const int THREADS = blockDim.x, waves = THREADS / 64;
-    const RowSums sums(smem, waves, a.E);
+    __shared__ float cross_part[W];
+    __shared__ int count_part[W];
+    constexpr int THREADS = W * 64;
+    const RowSums<W> sums(smem, a.E);
     const int tid = threadIdx.x;
     const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     if (block < tiles) {  // none where all rows are of one tile
@@ -380,16 +371,16 @@ __global__ __launch_bounds__(kWaves<V> * 64) void balance_rows_kernel(BalanceArg
                 has = span.begin >= row && span.end > last;
             }
             if (!has || span.s < 0 || span.s >= a.S) continue;
-            sum_rows<TYPE, SCORE, L, V, VEC>(a, from, to, sums);
+            sum_rows<TYPE, SCORE, L, V, VEC, W>(a, from, to, sums);
             float* out = parts + slot_of(b, span.s, part == 1, a.S > tiles) * Slot::words(a.E);
             for (int e = tid; e < a.E; e += THREADS) {
-                out[e] = sums.template share_of<V>(e);
+                out[e] = sums.share_of(e);
                 reinterpret_cast<int*>(out)[a.E + e] = sums.count[e];
             }
             if (tid == 0) {
                 int n;
                 float z;
-                sums.template row_totals<V>(n, z);
+                sums.row_totals(n, z);
                 reinterpret_cast<int*>(out)[2 * a.E] = n;
                 out[2 * a.E + 1] = z;
             }
@@ -401,15 +392,15 @@ __global__ __launch_bounds__(kWaves<V> * 64) void balance_rows_kernel(BalanceArg
     if (s >= a.S) return;
     const int from = offset_at(a.seq_offsets, (int)s, a.T), to = max(from, offset_at(a.seq_offsets, (int)s + 1, a.T));
     if (tiles > 0 && to > from && from / tile != (to - 1) / tile) return;  // the tiles'
-    sum_rows<TYPE, SCORE, L, V, VEC>(a, from, to, sums);
+    sum_rows<TYPE, SCORE, L, V, VEC, W>(a, from, to, sums);
     int n;
     float z;
-    sums.template row_totals<V>(n, z);
+    sums.row_totals(n, z);
     float cross = 0.0f;
     int total = 0;
     for (int e = tid; e < a.E; e += THREADS) {
         const int count = sums.count[e];
-        const float share = n > 0 ? sums.template share_of<V>(e) / (float)n : 0.0f;
+        const float share = n > 0 ? sums.share_of(e) / (float)n : 0.0f;
         if (a.counts) a.counts[s * a.E + e] = count;
         if (a.share) a.share[s * a.E + e] = share;
         if (count > 0) cross += (float)count * share;
@@ -428,7 +419,7 @@ __global__ __launch_bounds__(kWaves<V> * 64) void balance_rows_kernel(BalanceArg
     }
     __syncthreads();
     if (tid == 0) {
-        for (int w = 1; w < waves; ++w) cross += cross_part[w], total += count_part[w];
+        for (int w = 1; w < W; ++w) cross += cross_part[w], total += count_part[w];
         a.loss[s] = total > 0 ? (float)a.E * cross / (float)total : 0.0f;
     }
 }
@@ -648,6 +639,11 @@ BalanceLayout balance_layout(int T, int E, int S) {
 // z adds p * 2 lse d_z / rows.  The weights w = scale * r, r = s over the sum of the chosen (or s), add at the chosen
 //   renormalised:  softmax  scale r (d - m),  sigmoid  scale r (1 - s) (d - m),  m = sum of r d
 //   else:          softmax  scale p d, and -p * (sum of scale p d) at every expert;  sigmoid  scale s (1 - s) d
+//
+// A row is read and written once; what its sequence needs stays in registers while a group's rows are of it.  65536 x 384
+// FP32 takes 48 us (207 MB, 4.3 TB/s), 16384 x 256 BF16 in 13 sequences 11.2, bound by vector instructions.  Scores of the
+// chosen are gathered and their gradients scattered in LDS, not by comparing every id with every expert (with that and
+// exponentials of more instructions 75).
 template <int TYPE, int SCORE, int L, int V, bool VEC, int KV>
 __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int rows_per_group) {
     constexpr int GROUPS = kThreads / L, SIZE = TYPE == MOE_F32 ? 4 : 2;
@@ -853,14 +849,17 @@ bool vector_rows(const void* base, int64_t stride, int E, int type) {
 
 template <int TYPE, int SCORE, int L, int V, bool VEC>
 void parts_go(const BalanceArgs& a, const BalanceLayout& l, char* ws, hipStream_t stream) {
-    // Four waves for short sequences, of which most of a larger workgroup would have no rows (300 sequences of 55 rows
-    // 14.5 us to 18.9, 4000 of 4 19 to 53).
-    const int rows = a.T / a.S, waves = a.S > 1 && rows <= 64 ? kShortWaves : kWaves<V>;
-    const size_t lds = RowSums::bytes(waves, a.E);
+    // Four waves for short sequences, of which most of a larger workgroup would have no rows (16384 rows in 4000 18 us to
+    // 53), longer ones where there are many (300 of 55 rows 14.0 to 18.9; but 5 of 60 5.9 to 4.9).
     const int tiles = l.tiles > 1 ? l.tiles : 0;
-    hipLaunchKernelGGL((balance_rows_kernel<TYPE, SCORE, L, V, VEC>), wide_grid((int64_t)tiles + a.S), dim3(waves * 64),
-                       lds, stream, a, l.tile, tiles, reinterpret_cast<float*>(ws + l.parts),
-                       l.long_join ? reinterpret_cast<uint32_t*>(ws + l.tickets) : nullptr);
+    auto launch = [&](auto waves) {
+        constexpr int W = decltype(waves)::value;
+        hipLaunchKernelGGL((balance_rows_kernel<TYPE, SCORE, L, V, VEC, W>), wide_grid((int64_t)tiles + a.S), dim3(W * 64),
+                           RowSums<W>::bytes(a.E), stream, a, l.tile, tiles, reinterpret_cast<float*>(ws + l.parts),
+                           l.long_join ? reinterpret_cast<uint32_t*>(ws + l.tickets) : nullptr);
+    };
+    if (a.S > 1 && a.T / a.S <= (a.S >= 64 ? 64 : 32)) launch(std::integral_constant<int, kShortWaves>{});
+    else launch(std::integral_constant<int, kWaves<V>>{});
 }
 template <int TYPE, int SCORE, int L, int V, bool VEC, int KV>
 void grad_go(const GateGradArgs& a, hipStream_t stream) {

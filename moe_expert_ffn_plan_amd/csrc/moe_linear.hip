@@ -99,7 +99,14 @@ __device__ __forceinline__ void store2(const Args& a, int row, int col, float v0
 // hands over a stage's buffer stands between the two.
 //
 // AK = 2: the rows of x come two K-steps at a time, into a ring of their own of two units.  Rows of 64 bytes are half a
-// line each, and a request for half a line takes as long as one for a line.
+// line each, and a request for half a line takes as long as one for a line (16384 x 7168 x 4096 E2M1: 237 us, 243 by one).
+//
+// Workgroups stay: each takes a run of tiles, whose outputs go through LDS to whole lines while the next tile's first stages
+// load (237 us to 214).  Bound: 16384 x 7168 x 4096 E2M1 takes 205-216 us, 4500-4700 TFLOP/s of the 6960 that the
+// instructions reach from registers, with the matrix cores busy 69% of the time at the clock that the load leaves; without
+// DMA 190-200, without products 170-200.  E4M3 takes 312-334 (2900-3100 of 4310).  256 x 256 tiles, 64 x 128 to a wave,
+// read least LDS for a product; 128 x 256 tiles, two to a CU, take 258, four waves 273.  128 x 128 tiles, two to a CU, fill
+// the card where rows are fewer (2047 x 4064 x 1537 E4M3: 22 us to 32).
 template <int FMT, int BM, int BN, int WM, int WN, int AK, int NS_>
 struct Tile {
     static constexpr int W = WM * WN, THREADS = 64 * W, NS = NS_;
@@ -499,6 +506,8 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
 // waves read the same ones, so LDS would only be a detour).  x goes through LDS, where each wave has a place of its own and
 // needs no barrier: lanes that load neighbouring chunks of few rows touch few lines, lanes that load what they multiply
 // touch one each.  The waves' sums are added through LDS, in the waves' order.
+// Bound by the launch and by the weights' latency: 1 x 7168 x 4096 E4M3 takes 4.9 us, 32 rows 6.3 to 7.3, 64 8.7, 128 (two
+// groups, E2M1) 8.9; the same in tiles 11.8 to 14.8.
 template <int FMT, int ROWS, int W, int U>
 struct Few {
     static constexpr int RB = FMT == MOE_E2M1 ? 64 : 128, BYTES = U * RB, CHUNKS = BYTES / 16;  // of a row in a turn
@@ -622,7 +631,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(Args g) {
 // whole lines.  A workgroup turns 64 rows of kTurn K-steps in LDS, so that it reads along rows and writes along K-steps.
 constexpr int kTurn = 8;
 __global__ __launch_bounds__(kThreads) void tile_scales_kernel(const uint8_t* sf, int M, int blocks, int KT, uint32_t* out) {
-    __shared__ uint32_t words[kTurn][65];
+    __shared__ uint32_t words[kTurn][72];  // the 8 K-steps of 8 rows, which are written together, to 64 banks
     const int chunks = (KT + kTurn - 1) / kTurn;
     const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, band = block / chunks;
     const int kt0 = (int)(block % chunks) * kTurn;
@@ -671,7 +680,7 @@ void few(const Args& g, hipStream_t stream) {
 }  // namespace
 
 constexpr int kFewRows = 64, kSomeRows = 128;
-constexpr int kLongSteps = 5;    // K-steps that the ring of two units of x needs
+constexpr int kLongSteps = 5;    // K-steps that the ring of two units of x needs; shorter tiles load it by one
 constexpr int kFillTiles = 256;  // a workgroup for every compute unit
 constexpr int kMostSplits = 16, kLeastSteps = 4;
 
