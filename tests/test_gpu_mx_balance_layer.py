@@ -263,3 +263,72 @@ def test_tensors_elsewhere_are_refused(gpu):
         B.mx_linear(B.make_mx_linear(300, 1056, 130, "e4m3"), u8(gpu, 300, 1056), u8(gpu, 300, 33),
                     u8(gpu, B.mx_linear_weight_bytes(B.make_mx_linear(300, 1056, 130))), torch.empty(300, 130, dtype=BF16, device=gpu))
     torch.cuda.synchronize()
+
+
+def test_rows_behind_four_gibibytes(gpu):
+    """Rows whose offsets pass 32 bits have the results of the same rows at the start."""
+    block = 4096
+
+    def far(n, row, dtype, seed, make):
+        """[n, row] whose blocks of rows are all the same."""
+        t = torch.empty(n, row, dtype=dtype, device=gpu)
+        t.view(-1, block, row)[:] = make(torch.Generator(gpu).manual_seed(seed), (block, row)).to(dtype)
+        return t
+
+    def alike(*ts):
+        for t in ts:
+            assert torch.equal(t[:block], t[-block:])
+
+    normal = lambda g, s: torch.randn(s, generator=g, device=gpu)  # noqa: E731
+    # 270336 x 16384: 8.9 GB of x, 4.4 GB of codes and 2.2
+    n, K, N = 66 * block, 16384, 96
+    print("quant", flush=True)
+    x = far(n, K, BF16, 1, normal)
+    for fmt, width in (("e4m3", K), ("e2m1", K // 2)):
+        q, sf = torch.empty(n, width, dtype=torch.uint8, device=gpu), torch.empty(n, K // 32, dtype=torch.uint8, device=gpu)
+        B.mx_quant(B.make_mx_quant(n, K, fmt), x, q, sf)
+        alike(q, sf)
+        print("product", fmt, flush=True)
+        s = B.make_mx_linear(n, K, N, fmt)
+        w = B.mx_linear_prepare(s, *quantised(gpu, N, K))
+        y, ws = torch.empty(n, N, dtype=BF16, device=gpu), u8(gpu, B.mx_linear_workspace_bytes(s))
+        B.mx_linear(s, q, sf, w, y, ws)
+        alike(y)
+        few = B.make_mx_linear(block, K, N, fmt)
+        z = torch.empty(block, N, dtype=BF16, device=gpu)
+        B.mx_linear(few, q[-block:], sf[-block:], w, z, u8(gpu, B.mx_linear_workspace_bytes(few)))
+        assert (z.float() - y[:block].float()).abs().max() <= 2.0 ** -7 * y[:block].float().abs().max()  # other sums: a step or two
+        del q, sf, y, ws
+    print("product with wide rows of y", flush=True)
+    s = B.make_mx_linear(n, 64, N, "e2m1", y_stride=9000)
+    q, sf = far(n, 32, torch.uint8, 2, lambda g, sh: torch.randint(0, 256, sh, generator=g, device=gpu)), \
+        torch.full((n, 2), 127, dtype=torch.uint8, device=gpu)
+    y = torch.empty(n, 9000, dtype=BF16, device=gpu)
+    B.mx_linear(s, q, sf, B.mx_linear_prepare(s, *quantised(gpu, N, 64)), y[:, :N], u8(gpu, B.mx_linear_workspace_bytes(s)))
+    alike(y[:, :N])
+    del x, y
+    print("balance and gradient", flush=True)
+    n, E, k = 1056 * block, 257, 3
+    logits = far(n, E, F32, 3, normal)
+    ids = torch.topk(logits[:block], k)[1].repeat(n // block, 1)
+    s = B.make_balance(n, E, k, num_seqs=3)
+    off = torch.tensor([0, block, n - block, n], device=gpu)
+    out = {"counts": torch.empty(3, E, dtype=torch.int32, device=gpu), "rows": torch.empty(3, dtype=torch.int32, device=gpu),
+           "share": torch.empty(3, E, device=gpu), "loss": torch.empty(3, device=gpu)}
+    B.balance(s, logits, ids, u8(gpu, B.balance_workspace_bytes(s)), seq_offsets=off, **out)
+    assert torch.equal(out["counts"][0], out["counts"][2]) and torch.equal(out["counts"][1], out["counts"][0] * (n // block - 2))
+    assert out["rows"].tolist() == [block, n - 2 * block, block]
+    for t in (out["share"], out["loss"]):  # sums of 2^22 values by lanes, waves and tiles
+        assert (t - t[:1]).abs().max() <= 2.0 ** -14 * t.abs().max()
+    d = torch.empty(n, E, device=gpu)
+    one = torch.ones(3, device=gpu)
+    B.gate_grad(s, logits, ids, d, seq_offsets=off, counts=out["counts"], rows=out["rows"], d_loss=one,
+                d_topk_w=torch.ones(n, k, device=gpu))
+    alike(d)
+    torch.cuda.synchronize()
+
+
+def quantised(dev, N, K):
+    q, sf = torch.empty(N, K // 2, dtype=torch.uint8, device=dev), torch.empty(N, K // 32, dtype=torch.uint8, device=dev)
+    B.mx_quant(B.make_mx_quant(N, K, "e2m1", F32), torch.randn(N, K, generator=torch.Generator(dev).manual_seed(N), device=dev), q, sf)
+    return q, sf
