@@ -201,7 +201,7 @@ __device__ __forceinline__ int sequence_of(const int64_t* off, int row, int S, i
 }
 
 // The same of one row for a whole wave, which compares 64 offsets at a time, and the sequence's rows: in front of the first
-// sequence those up to it, behind the last those from its end on.
+// sequence those up to it, behind the last those from its end on.  All lanes of the wave have to be on.
 struct Span {
     int s, begin, end;
 };
@@ -662,8 +662,10 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
     const char* in = static_cast<const char*>(a.logits) + t * a.stride * SIZE;
     char* out = static_cast<char*>(a.d_logits) + t * a.E * SIZE;
     int64_t at_k = t * a.k + lane;
-    // the sequence of the last row, and its rows; `known`: what of it the rows need is loaded
-    int s = 0, begin = 0, end = 0;
+    // the sequence of the last row, here of the wave's first one, and its rows; `known`: what of it the rows need is loaded.
+    // Looked up in front of the loop, where lanes of groups without a row are on too: the search has all 64 take part.
+    const Span span = span_of_wave(a.seq_offsets, (int)min(first + threadIdx.x / 64 * (64 / L), (int64_t)a.T), a.S, a.T);
+    int s = span.s, begin = span.begin, end = span.end;
     bool known = false;
     float pull[V], zpull = 0.0f;
 #pragma unroll
@@ -685,13 +687,6 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
                     dw[q] = a.scale * a.d_topk_w[at_k + q * L];
                 }
             }
-        }
-        if (step == 0) {  // of the wave's first row
-            const Span span =
-                span_of_wave(a.seq_offsets, (int)min(first + threadIdx.x / 64 * (64 / L), (int64_t)a.T), a.S, a.T);
-            s = span.s;
-            begin = span.begin;
-            end = span.end;
         }
         if (t < begin || t >= end) {
             known = false;
