@@ -684,6 +684,8 @@ constexpr int kLongSteps = 5;    // K-steps that the ring of two units of x need
 constexpr int kFillTiles = 256;  // a workgroup for every compute unit
 constexpr int kMostSplits = 16, kLeastSteps = 4;
 
+static size_t laid_out_bytes(int M, int KT) { return ((size_t)M + 63) / 64 * KT * 256; }  // of x's scales by K-step
+
 // The kernel with the least estimated time, in microseconds (measured at 2048 .. 16384 rows, 2016 .. 7168 columns and 512
 // .. 7168 outputs, most within 15%): a K-step of a 256 x 256 tile takes 0.8 (E2M1) or 1.3 (E4M3), one of a 128 x 128 tile
 // 0.27 or 0.4, or 0.36 or 0.42 for each of two that share a compute unit; to lay out the scales takes 4, to join splits 4 and their
@@ -721,17 +723,17 @@ MxLinearChoice choose_mx_linear(int M, int N, int K, int format) {
     }
     // A K-step's word of a row is a line of its own, so large tiles want them laid out; and words start at multiples of 4.
     c.tile_scales = K % kStep != 0 || c.kernel == 0;
-    c.scale_bytes = c.tile_scales ? ((size_t)M + 63) / 64 * KT * 256 : 0;
+    c.scale_bytes = c.tile_scales ? laid_out_bytes(M, KT) : 0;
     c.partial_bytes = c.splits > 1 ? (size_t)c.splits * M * mx_column_blocks(N) * 32 * 4 : 0;
     return c;
 }
 
 size_t most_mx_linear_workspace(int M, int N, int K, int format) {
-    // What scales take grows with the tokens.  Partial sums are had by fewer than kFillTiles tile rows alone, and there
-    // more tokens may need less: all of them are asked.
-    size_t most = M > 0 ? choose_mx_linear(M, N, K, format).workspace_bytes() : 0;
-    for (int m = std::min(M, kFillTiles * 128); m > 0; --m)
-        most = std::max(most, choose_mx_linear(m, N, K, format).workspace_bytes());
+    // Partial sums are had by fewer than kFillTiles tile rows alone: those batches are asked one by one.  Larger ones take
+    // laid out scales or nothing, now this and now that as the tokens grow, and no more than the scales of M tokens.
+    const int asked = std::min(M, kFillTiles * 128);
+    size_t most = M > asked ? laid_out_bytes(M, mx_steps(K)) : 0;
+    for (int m = asked; m > 0; --m) most = std::max(most, choose_mx_linear(m, N, K, format).workspace_bytes());
     return most;
 }
 
