@@ -677,9 +677,9 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
         load_row<TYPE, L, V, VEC>(l, in, a.E, lane);
         if (a.d_topk_w) {
 #pragma unroll
+            for (int q = 0; q < KV; ++q) id[q] = -1, dw[q] = 0.0f;
+#pragma unroll
             for (int q = 0; q < KV; ++q) {
-                id[q] = -1;
-                dw[q] = 0.0f;
                 if (q > 0 && q * L >= a.k) break;
                 if (lane + q * L < a.k) {
                     const int64_t e = a.topk_idx[at_k + q * L];
@@ -736,9 +736,9 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
             float w[KV], rest[KV];  // the chosen's scores and, of sigmoid ones, what they lack to 1
             float sum = 0.0f, m = 0.0f;
 #pragma unroll
+            for (int q = 0; q < KV; ++q) w[q] = 0.0f, rest[q] = 1.0f;
+#pragma unroll
             for (int q = 0; q < KV; ++q) {
-                w[q] = 0.0f;
-                rest[q] = 1.0f;
                 if (q > 0 && q * L >= a.k) break;
                 if (id[q] >= 0) {
                     const float v = values[id[q]];
