@@ -659,8 +659,9 @@ MOE_API int moe_mx_linear(const moe_mx_linear_shape* shape, const uint8_t* x, co
  * constants; counts may be summed over ranks first.  Sums hold in FP32 in an
  * order that depends on the shape alone: the same inputs give the same bits.
  * A NaN or +infinity among a row's logits makes the p of that row NaN (with
- * sigmoid scores an infinity stands for 1).  Exponentials below 2^-126 of a
- * row's largest may count as 0; a z beyond FP32's range is infinite.
+ * sigmoid scores an infinity stands for 1), and with them its sequence's
+ * share, loss and z (z infinite with an infinity).  Exponentials below 2^-125
+ * of a row's largest may count as 0; a z beyond FP32's range is infinite.
  * Limits: num_tokens 0 .. 2^28 - 1, T * topk < 2^30; num_experts 1 .. 1024;
  * topk 1 .. min(64, num_experts); num_seqs 1 .. 2^20, 1 without seq_offsets,
  * S * E < 2^30; scale finite; logits_stride >= num_experts. */

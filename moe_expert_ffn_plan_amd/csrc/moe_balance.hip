@@ -116,9 +116,13 @@ __device__ __forceinline__ void load_row(float (&l)[V], const char* row, int E, 
 // Scores of a row as shares of their sum.  `top` is the largest logit, NaN aside; a padding row has none and shares of 0.
 //   softmax: exp(l - top) as 2^(l log2 e - top log2 e), the difference rounded once: off by 2^-24 |l - top| (1 + 0.2),
 //            for the rounding and for log2 e's; what the rounding of top log2 e does is the same for the whole row
+//            and, below kFar, a factor of 2^(+-1/16) at most.  From 2^31 on that factor alone would pass FP32's range, so from
+//            kFar on it is 2^((l - top) log2 e): off by 2^-24 |l - top| (2 + 0.2), and logits there lie 1/8 apart or are equal
 //   sigmoid: 1 / (1 + 2^(-l log2 e)); where all logits are below -60, exp(l - top) / (1 + exp(l)), which keeps the bits
 //            of the shares of tiny scores
-// A NaN or, with softmax, an infinity makes the sum NaN.  Exponentials below 2^-126 of the largest may be 0.
+// A NaN or, with softmax, an infinity makes the sum NaN, and the log-sum-exp NaN or infinite.  Exponentials below 2^-125 of
+// the largest may be 0.
+constexpr float kFar = 0x1p20f;
 struct RowSum {
     float top, by, sum, inv;  // by: top log2 e, or 0; inv: 1 over the sum
     bool alive;
@@ -149,12 +153,18 @@ __device__ __forceinline__ RowSum shares(const float (&l)[V], float (&p)[V], flo
     }
     r.by = r.alive ? r.top * kLog2e : 0.0f;
     if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
-        if (fabsf(r.top) < 0x1p100f || !r.alive) {
+        if (fabsf(r.top) < kFar || !r.alive) {
 #pragma unroll
             for (int i = 0; i < V; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(l[i], kLog2e, -r.by));
-        } else {  // top log2 e may be beyond FP32
+        } else {
+            float nan = 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) p[i] = exp_over(l[i], r.top);
+            for (int i = 0; i < V; ++i) {
+                p[i] = exp_over(l[i], r.top);
+                nan += p[i];
+            }
+            nan = over_lanes<Sum, L>(nan);
+            if (nan != nan && r.top < INFINITY) r.top = nan;  // for lse
         }
     } else {
         if (r.top > -60.0f || !r.alive) {

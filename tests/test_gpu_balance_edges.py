@@ -1,9 +1,11 @@
 """moe_balance and moe_gate_grad where they can go wrong.  Tolerances as derived in test_gpu_balance.py."""
+import itertools
+
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_balance import check_gradient, inputs
+from test_gpu_balance import INF, NAN, check_forward, check_gradient, forward, inputs, on
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +41,48 @@ def test_gradient_of_chosen_far_below_the_others(gpu, E, k, dtype, score):
     ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(33)])
     low = -128.0 - torch.randint(0, 4, (33, k), generator=g).to(dtype)
     check_gradient(l.scatter(1, ids, low), ids, None, gpu, score, True, 1.0, 1, ("w",))
+
+
+# ---- logits of any size
+
+def far_rows(seed, E=24):
+    """Rows around tops of any power of two, both signs: neighbours within two steps of FP32 (and of 1), whose distance is
+    exact and either at most 16 or above 127, where exponentials count as 0."""
+    g = np.random.default_rng(seed)
+    rows = []
+    for e in [0, 10, 16, 19, 20, 21, 24, 26, *range(31, 64, 2), 75, 90, 98, 99, 100, 101, 120, 126]:
+        for sign in (1, -1):
+            top = np.float32(sign * g.uniform(1, 2) * 2.0 ** e)
+            step = max(np.spacing(np.abs(top)), np.float32(1.0))
+            rows.append(np.float32(np.round(top / step) * step) - step * g.integers(0, 3, E).astype(np.float32))
+    return torch.from_numpy(np.stack(rows).astype(np.float32))
+
+
+def test_forward_logits_of_any_size(gpu):
+    l = far_rows(1)
+    ids = torch.randint(0, 24, (len(l), 3), generator=torch.Generator().manual_seed(1))
+    for score in ("softmax", "sigmoid"):
+        check_forward(l, ids, torch.arange(len(l) + 1), gpu, score, len(l))
+
+
+@pytest.mark.parametrize("score,renorm", itertools.product(["softmax", "sigmoid"], [True, False]))
+def test_gradient_logits_of_any_size(gpu, score, renorm):
+    l = far_rows(2)
+    g = torch.Generator().manual_seed(2)
+    ids = torch.stack([torch.randperm(24, generator=g)[:3] for _ in range(len(l))])
+    check_gradient(l, ids, None, gpu, score, renorm, 1.0, 1, ("loss", "w"))
+    if score == "softmax":
+        keep = l.abs().amax(1) < 2.0 ** 63  # d_z and the logarithm stay finite
+        check_gradient(l[keep], ids[keep], None, gpu, score, renorm, 1.0, 1, ("z",))
+
+
+def test_z_of_rows_without_a_logarithm(gpu):
+    """A NaN makes z NaN, whatever stands beside it, and +infinity makes it infinite."""
+    l = torch.zeros(6, 16)
+    l[0, 3], l[1], l[1, 5], l[2], l[2, 6], l[3], l[3, 0] = NAN, -INF, NAN, 2.0 ** 110, NAN, -(2.0 ** 40), NAN
+    l[4, 2] = INF
+    ids = torch.zeros(6, 2, dtype=torch.int64)
+    out = forward(*on(gpu, l, ids, torch.arange(7)), gpu, S=6)
+    z = out["z"].cpu()
+    assert torch.isnan(z[:4]).all() and torch.isinf(z[4]) and abs(z[5].item() - np.log(16) ** 2) < 1e-5
+    assert torch.isnan(out["share"][:5]).all()
