@@ -118,8 +118,8 @@ __device__ __forceinline__ void load_row(float (&l)[V], const char* row, int E, 
 //            for the rounding and for log2 e's; what the rounding of top log2 e does is the same for the whole row
 //            and, below kFar, a factor of 2^(+-1/16) at most.  From 2^31 on that factor alone would pass FP32's range, so from
 //            kFar on it is 2^((l - top) log2 e): off by 2^-24 |l - top| (2 + 0.2), and logits there lie 1/8 apart or are equal
-//   sigmoid: 1 / (1 + 2^(-l log2 e)); where all logits are below -60, exp(l - top) / (1 + exp(l)), which keeps the bits
-//            of the shares of tiny scores
+//   sigmoid: 1 / (1 + 2^(-l log2 e)), which is 0 below 2^-126; where all logits are below 0, exp(l - top) / (1 + exp(l)),
+//            which keeps the shares of scores that are tiny beside 1, but not beside the largest
 // A NaN or, with softmax, an infinity makes the sum NaN, and the log-sum-exp NaN or infinite.  Exponentials below 2^-125 of
 // the largest may be 0.
 constexpr float kFar = 0x1p20f;
@@ -167,7 +167,7 @@ __device__ __forceinline__ RowSum shares(const float (&l)[V], float (&p)[V], flo
             if (nan != nan && r.top < INFINITY) r.top = nan;  // for lse
         }
     } else {
-        if (r.top > -60.0f || !r.alive) {
+        if (r.top >= 0.0f || !r.alive) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float e = __builtin_amdgcn_exp2f(-kLog2e * l[i]);
@@ -765,7 +765,8 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
             sum = over_lanes<Sum, L>(sum);
             m = over_lanes<Sum, L>(m);
             if (a.renorm) {
-                if (sum < 0x1p-80f) {  // far below the row's largest, or all tiny: formed over the largest of them
+                // far below the row's largest, or sigmoid scores of which smaller ones may be lost: formed over the largest of them
+                if (sum < (SCORE == MOE_SCORE_SOFTMAX ? 0x1p-80f : 0.5f)) {
                     float top = -INFINITY, lk[KV];
 #pragma unroll
                     for (int i = 0; i < V; ++i) values[expert_of<L, V, VEC>(lane, i)] = l[i];

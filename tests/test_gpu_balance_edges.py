@@ -86,3 +86,26 @@ def test_z_of_rows_without_a_logarithm(gpu):
     z = out["z"].cpu()
     assert torch.isnan(z[:4]).all() and torch.isinf(z[4]) and abs(z[5].item() - np.log(16) ** 2) < 1e-5
     assert torch.isnan(out["share"][:5]).all()
+
+
+# ---- sigmoid scores far below the row's largest
+
+def low_rows(E=24):
+    """Whole numbers, so that distances are exact: tops from 2 to -200 and scores down to exp(-60) of them."""
+    g = np.random.default_rng(3)
+    tops = [2, 0, -1, -5, -20, -30, -40, -50, -59, -60, -61, -90, -150, -200]
+    l = np.stack([t - g.integers(0, 61, E) for t in tops]).astype(np.float32)
+    l[:, 0], l[:, 1] = tops, np.array(tops) - 60
+    return torch.from_numpy(l)
+
+
+def test_forward_low_sigmoid_scores(gpu):
+    l = low_rows()
+    check_forward(l, torch.zeros(len(l), 2, dtype=torch.int64), torch.arange(len(l) + 1), gpu, "sigmoid", len(l))
+
+
+@pytest.mark.parametrize("ids", [[0, 1, 2], [1, 2, 3], [1, 5, 6]])
+def test_gradient_low_sigmoid_scores(gpu, ids):
+    l = low_rows()
+    check_gradient(l, torch.tensor([ids] * len(l)), None, gpu, "sigmoid", True, 1.0, 1, ("loss", "w"))
+    check_gradient(l, torch.tensor([ids] * len(l)), None, gpu, "sigmoid", True, 1.0, 1, ("w",))
