@@ -700,7 +700,9 @@ MOE_API int moe_balance(const moe_balance_shape* shape, const void* logits, cons
  *   + sum over t, j of d_topk_w[t, j] * topk_w[t, j]
  * with topk_w as moe_gate forms it (scores of topk_idx, over their sum where
  * renormalize is set, times scale; an entry whose id is outside 0 .. E - 1 has
- * weight 0; an id that occurs twice in a row counts twice).  0 where a logit
+ * weight 0, as one whose logit is -infinity, and the d_topk_w of an entry of
+ * weight 0 is not used, whatever it is; an id that occurs twice in a row counts
+ * twice).  0 where a logit
  * is -infinity.  Rows in no sequence are left as they were.
  *   logits, topk_idx, seq_offsets   as for moe_balance
  *   counts, rows   int32 [S, E] and [S], from moe_balance; counts with d_loss,

@@ -743,7 +743,9 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
         if (a.d_topk_w) {
 #pragma unroll
             for (int i = 0; i < V; ++i) values[expert_of<L, V, VEC>(lane, i)] = SCORE == MOE_SCORE_SOFTMAX ? p[i] : l[i];
-            float w[KV], rest[KV];  // the chosen's scores and, of sigmoid ones, what they lack to 1
+            // the chosen's scores and, of sigmoid ones, what they lack to 1; where there is no score, as of an id that is none or
+            // a masked logit's, d_topk_w may be anything
+            float w[KV], rest[KV];
             float sum = 0.0f, m = 0.0f;
 #pragma unroll
             for (int q = 0; q < KV; ++q) w[q] = 0.0f, rest[q] = 1.0f;
@@ -760,7 +762,7 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
                     }
                 }
                 sum += w[q];
-                m = fmaf(w[q], dw[q], m);
+                if (w[q] != 0.0f) m = fmaf(w[q], dw[q], m);
             }
             sum = over_lanes<Sum, L>(sum);
             m = over_lanes<Sum, L>(m);
@@ -782,7 +784,7 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
                         w[q] = lk[q] > -INFINITY ? exp_over(lk[q], top) : 0.0f;
                         if constexpr (SCORE == MOE_SCORE_SIGMOID) w[q] *= rest[q];  // 1 / (1 + exp(l))
                         sum += w[q];
-                        m = fmaf(w[q], dw[q], m);
+                        if (w[q] != 0.0f) m = fmaf(w[q], dw[q], m);
                     }
                     sum = over_lanes<Sum, L>(sum);
                     m = over_lanes<Sum, L>(m);
@@ -802,7 +804,7 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
 #pragma unroll
             for (int q = 0; q < KV; ++q) {
                 if (q > 0 && q * L >= a.k) break;
-                if (id[q] >= 0) atomicAdd(&own[id[q]], w[q] * (dw[q] - m) * rest[q]);
+                if (id[q] >= 0 && w[q] != 0.0f) atomicAdd(&own[id[q]], w[q] * (dw[q] - m) * rest[q]);
             }
         }
         float g[V];

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_balance import INF, NAN, check_forward, check_gradient, forward, inputs, on
+from test_gpu_balance import INF, NAN, check_forward, check_gradient, forward, gradient, inputs, on
 
 pytestmark = pytest.mark.gpu
 
@@ -109,3 +109,40 @@ def test_gradient_low_sigmoid_scores(gpu, ids):
     l = low_rows()
     check_gradient(l, torch.tensor([ids] * len(l)), None, gpu, "sigmoid", True, 1.0, 1, ("loss", "w"))
     check_gradient(l, torch.tensor([ids] * len(l)), None, gpu, "sigmoid", True, 1.0, 1, ("w",))
+
+
+# ---- entries that take no part
+
+@pytest.mark.parametrize("E", [24, 33, 300])
+@pytest.mark.parametrize("score,renorm", itertools.product(["softmax", "sigmoid"], [True, False]))
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+def test_gradient_of_entries_without_a_weight(gpu, score, renorm, value, E):
+    """What stands at ids that are none, or whose logit is masked, is not read into the row."""
+    l, ids, _ = inputs(40, E, 5, 5)
+    ids[3, 1], ids[4, 0], ids[5, 2], ids[6] = -1, E, 1 << 40, -1
+    l[7, ids[7, 2]] = -INF
+    l[8, ids[8]] = -INF
+    l[9] = -INF
+    l[10] -= 300.0  # sums of the chosen that are formed again
+    ids[10, 4] = -1
+    l[11, ids[11, 1:]] = -INF
+    d = torch.randn(40, 5, generator=torch.Generator().manual_seed(6))
+    none = (ids < 0) | (ids >= E) | (l.gather(1, ids.clamp(0, E - 1)) == -INF)
+    assert none.sum() > 20
+    want = gradient(*on(gpu, l, ids, None), gpu, score=score, renormalize=renorm, d_topk_w=d.masked_fill(none, 0.0).to(gpu))
+    got = gradient(*on(gpu, l, ids, None), gpu, score=score, renormalize=renorm, d_topk_w=d.masked_fill(none, value).to(gpu))
+    assert torch.isfinite(want).all() and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("score,renorm", itertools.product(["softmax", "sigmoid"], [True, False]))
+def test_gradient_of_rows_with_a_nan_and_unused_entries(gpu, score, renorm):
+    """Neither reaches another row, wherever it lies in the workgroup."""
+    for E in (8, 33, 64, 200):
+        l, ids, _ = inputs(50, E, 4, 7)
+        ids[::3, 1], ids[::3, 3] = -1, E
+        d = torch.randn(50, 4, generator=torch.Generator().manual_seed(8)).to(gpu)
+        want = gradient(*on(gpu, l, ids, None), gpu, score=score, renormalize=renorm, d_topk_w=d)
+        l[::3, 2] = NAN
+        got = gradient(*on(gpu, l, ids, None), gpu, score=score, renormalize=renorm, d_topk_w=d)
+        bad = torch.arange(50, device=gpu) % 3 == 0
+        assert torch.equal(got[~bad], want[~bad]) and torch.isfinite(want).all() and torch.isnan(got[bad]).any(1).all()
