@@ -659,13 +659,14 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
     constexpr int GROUPS = kThreads / L, SIZE = TYPE == MOE_F32 ? 4 : 2;
     // What a group's row adds at the experts it chose, by expert (zeros between rows), and the row's scores (softmax) or
     // logits for its chosen experts to be read from.  A group's lanes are of one wave, whose LDS instructions are done in
-    // their order, and an instruction's additions to one place in the lanes' order.
+    // their order (wave_exchange has the compiler keep it), and an instruction's additions to one place in the lanes' order.
     __shared__ __attribute__((aligned(16))) float sums_of_rows[GROUPS][L * V], row_of_group[GROUPS][L * V];
     const int lane = threadIdx.x % L, group = threadIdx.x / L;
     float* own = sums_of_rows[group];
     float* values = row_of_group[group];
 #pragma unroll
     for (int i = 0; i < V; ++i) own[lane + L * i] = 0.0f;
+    wave_exchange();
     const int64_t first = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * GROUPS * rows_per_group;
     if (first >= a.T) return;
     int64_t t = first + group;
@@ -743,6 +744,7 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
         if (a.d_topk_w) {
 #pragma unroll
             for (int i = 0; i < V; ++i) values[expert_of<L, V, VEC>(lane, i)] = SCORE == MOE_SCORE_SOFTMAX ? p[i] : l[i];
+            wave_exchange();
             // the chosen's scores and, of sigmoid ones, what they lack to 1; where there is no score, as of an id that is none or
             // a masked logit's, d_topk_w may be anything
             float w[KV], rest[KV];
@@ -770,8 +772,10 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
                 // far below the row's largest, or sigmoid scores of which smaller ones may be lost: formed over the largest of them
                 if (sum < (SCORE == MOE_SCORE_SOFTMAX ? 0x1p-80f : 0.5f)) {
                     float top = -INFINITY, lk[KV];
+                    wave_exchange();
 #pragma unroll
                     for (int i = 0; i < V; ++i) values[expert_of<L, V, VEC>(lane, i)] = l[i];
+                    wave_exchange();
 #pragma unroll
                     for (int q = 0; q < KV; ++q) {
                         lk[q] = id[q] >= 0 ? values[id[q]] : -INFINITY;
@@ -814,8 +818,10 @@ __global__ __launch_bounds__(kThreads) void gate_grad_kernel(GateGradArgs a, int
             if constexpr (SCORE == MOE_SCORE_SIGMOID) g[i] *= less[i];
         }
         if (a.d_topk_w) {
+            wave_exchange();
 #pragma unroll
             for (int i = 0; i < V; ++i) g[i] += own[expert_of<L, V, VEC>(lane, i)];
+            wave_exchange();
 #pragma unroll
             for (int q = 0; q < KV; ++q) {
                 if (q > 0 && q * L >= a.k) break;

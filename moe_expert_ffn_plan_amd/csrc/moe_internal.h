@@ -206,6 +206,15 @@ inline dim3 wide_grid(int64_t n) {
     return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
 }
 
+// Between LDS accesses of a wave through which its lanes hand each other values.  The hardware does a wave's LDS
+// instructions in their order; this keeps the compiler, which looks at one lane, from reordering or forwarding them.
+// No instruction of its own.
+__device__ __forceinline__ void wave_exchange() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Strides in elements, 0 already replaced by the row length.
 struct NormArgs {
     const void* x;

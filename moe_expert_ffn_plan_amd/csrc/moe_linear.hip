@@ -471,6 +471,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
                     for (int j = 0; j < T::NI; j += 2)
                         *reinterpret_cast<uint32_t*>(place + ((4 * p + k) * COLS + j * 32 + c) * 2) =
                             pack_bf16(acc[i][j][e + k], acc[i][j + 1][e + k]);
+                wave_exchange();
 #pragma unroll
                 for (int h = 0; h < 8 * LANES / 64; ++h) {
                     const int at = h * 64 + l;
@@ -482,6 +483,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
                         else *to = v;
                     }
                 }
+                wave_exchange();
             }
         };
         if (g.stream) store(yes);

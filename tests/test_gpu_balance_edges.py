@@ -146,3 +146,23 @@ def test_gradient_of_rows_with_a_nan_and_unused_entries(gpu, score, renorm):
         got = gradient(*on(gpu, l, ids, None), gpu, score=score, renormalize=renorm, d_topk_w=d)
         bad = torch.arange(50, device=gpu) % 3 == 0
         assert torch.equal(got[~bad], want[~bad]) and torch.isfinite(want).all() and torch.isnan(got[bad]).any(1).all()
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(20, 3), (33, 8), (64, 20), (257, 6), (1000, 9)])
+def test_gradient_of_rows_one_after_another(gpu, E, k, score, renorm):
+    """Rows that a group of lanes takes in turn, through the same LDS, have the bits that they have alone; ids twice, and
+    the same ones in rows that follow each other."""
+    T = 70001 if E <= 64 else 20011
+    g = torch.Generator(gpu).manual_seed(E)
+    l = torch.randn(T, E, generator=g, device=gpu)
+    ids = torch.randint(-1, E, (T, k), generator=g, device=gpu)
+    ids[T // 2:] = ids[0]
+    l[::3] = l[::3].scatter(1, ids[::3].clamp_min(0), -130.0)  # weights that are formed again
+    d = torch.randn(T, k, generator=g, device=gpu)
+    whole = gradient(l, ids, None, gpu, score=score, renormalize=renorm, d_topk_w=d)
+    for at in range(0, T, 4000):
+        part = slice(at, min(at + 4000, T))
+        alone = gradient(l[part], ids[part], None, gpu, score=score, renormalize=renorm, d_topk_w=d[part])
+        assert torch.equal(whole[part], alone), at
