@@ -297,6 +297,7 @@ struct MxLinearChoice {
     bool tile_scales;                     // x_sf is laid out by K-step first
     size_t scale_bytes, partial_bytes;    // of the workspace, in this order
     size_t workspace_bytes() const { return scale_bytes + partial_bytes; }
+    int split_steps(int KT) const { return (KT + splits - 1) / splits; }  // K-steps of a split, the last may have fewer
 };
 MxLinearChoice choose_mx_linear(int M, int N, int K, int format);
 size_t most_mx_linear_workspace(int M, int N, int K, int format);  // at least that of any choice for 0 .. M tokens

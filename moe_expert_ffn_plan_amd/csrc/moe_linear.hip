@@ -723,6 +723,7 @@ MxLinearChoice choose_mx_linear(int M, int N, int K, int format) {
         c.tokens = c.columns = 128;
         c.splits = splits;
     }
+    c.splits = (KT + c.split_steps(KT) - 1) / c.split_steps(KT);  // none without a K-step
     // A K-step's word of a row is a line of its own, so large tiles want them laid out; and words start at multiples of 4.
     c.tile_scales = K % kStep != 0 || c.kernel == 0;
     c.scale_bytes = c.tile_scales ? laid_out_bytes(M, KT) : 0;
@@ -767,8 +768,7 @@ hipError_t launch_mx_linear(const MxLinearArgs& a, const MxLinearChoice& c, hipS
                            reinterpret_cast<uint32_t*>(a.ws));
     }
     g.splits = c.splits;
-    g.per = (g.KT + c.splits - 1) / c.splits;
-    g.splits = (g.KT + g.per - 1) / g.per;  // none without a K-step
+    g.per = c.split_steps(g.KT);
     g.wide = a.N % 8 == 0 && a.y_stride % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
     g.stream = (int64_t)a.M * a.N * 2 > 32ll << 20;
     g.mt = (a.M + c.tokens - 1) / c.tokens;

@@ -22,3 +22,20 @@ def test_largest_workspace_of_small_batches_is_that_of_one():
         for most in (0, 64, 130, 2000):
             need = max(B.mx_linear_workspace_bytes(B.make_mx_linear(T, K, N)) for T in range(most + 1))
             assert B.mx_linear_max_workspace_bytes(B.make_mx_linear(most, K, N)) == need
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+def test_splits_are_those_that_run(fmt):
+    """Every split has K-steps: ceil(steps / ceil(steps / splits)) of them is the number itself, and the workspace holds
+    that many partial sums."""
+    split = set()
+    for steps in range(1, 80):
+        for T, N in ((129, 64), (200, 512), (500, 1024), (1000, 1500)):
+            s = B.make_mx_linear(T, 128 * steps, N, fmt)
+            splits = B.mx_linear_tile(s)[2]
+            per = -(-steps // splits)
+            assert -(-steps // per) == splits, (steps, T, N)
+            if splits > 1:
+                assert B.mx_linear_workspace_bytes(s) == splits * T * -(-N // 64) * 64 * 4
+                split.add(splits)
+    assert len(split) > 3
