@@ -564,6 +564,10 @@ enum moe_mx_format {
  *   x_q    = x / 2^s rounded to the format's nearest value, ties to the even
  *          code; two E2M1 codes to a byte, the even column low
  *   x_dq   = x_q * 2^s rounded to BF16
+ * This is moe_norm_quant's scale: no value saturates.  What the OCP
+ * microscaling formats recommend, 2^(floor(log2 max|x|) - 2) or - 8, is half
+ * of it where max|x| is above 1.5 (E2M1) or 1.75 (E4M3) times a power of two,
+ * and clips such values.
  * A block that holds a NaN or an infinity has x_sf 255, which stands for NaN,
  * codes 0 and x_dq NaN throughout.  Where the rounding of x_dq passes BF16's
  * range (|x| of almost 2^128) it is infinite.
@@ -603,7 +607,7 @@ typedef struct moe_mx_linear_shape {
 } moe_mx_linear_shape;
 
 /* One-time re-layout of the weights (num_tokens, x_format and y_stride are
- * ignored): w uint8 [N, K / 2] E2M1, w_sf uint8 [N, K / 32], 16-byte aligned
+ * checked like the rest, but change nothing): w uint8 [N, K / 2] E2M1, w_sf uint8 [N, K / 32], 16-byte aligned
  * (w_sf any), into w_tiled of moe_mx_linear_weight_bytes, 16-byte aligned:
  *   codes   [B][KT][128 slots of 16 B], B = 2 * ceil(N / 64), KT =
  *           ceil(K / 128); slot p of (b, kt) holds the 32 columns from
@@ -657,7 +661,8 @@ MOE_API int moe_mx_linear(const moe_mx_linear_shape* shape, const uint8_t* x, co
  *                rows[s]; softmax alone
  * each 0 where its divisor is 0.  The gradient takes counts and rows as
  * constants; counts may be summed over ranks first.  Sums hold in FP32 in an
- * order that depends on the shape alone: the same inputs give the same bits.
+ * order that depends on the shape and the offsets alone: the same inputs give
+ * the same bits.
  * A NaN or +infinity among a row's logits makes the p of that row NaN (with
  * sigmoid scores an infinity stands for 1), and with them its sequence's
  * share, loss and z (z infinite with an infinity).  Exponentials below 2^-125

@@ -610,6 +610,7 @@ __global__ __launch_bounds__(kJoinThreads) void balance_short_join_kernel(Balanc
 // tile / several, E = 256: 300 rows in 5 sequences 4.9 / 10.0, 1000 in 7 7.4 / 10.7; in one sequence 190 rows 7.9 / 8.0,
 // 256 9.5 / 8.6, 1000 26 / 8.8).  Else a tile for every compute unit, and no more parts than the second kernel adds quickly
 // (65536 x 384: 28.4 us for tiles of 256 rows, 41.8 for 512, 27.9 for 128; 16384 x 256: 12.1, 11.7, 16.8 for 64, 128, 32).
+// Measured at 256 and 384 experts, and taken for any number.
 int tile_rows(int T, int S) {
     int tile = 16;
     if (T <= 1024 && T <= 192 * (int64_t)S) return 1024;
@@ -651,7 +652,7 @@ BalanceLayout balance_layout(int T, int E, int S) {
 //   else:          softmax  scale p d, and -p * (sum of scale p d) at every expert;  sigmoid  scale s (1 - s) d
 //
 // A row is read and written once; what its sequence needs stays in registers while a group's rows are of it.  65536 x 384
-// FP32 takes 48 us (207 MB, 4.3 TB/s), 16384 x 256 BF16 in 13 sequences 11.2, bound by vector instructions.  Scores of the
+// FP32 takes 48 us (207 MB, 4.3 TB/s), 16384 x 256 BF16 in 13 sequences 12.0, bound by vector instructions.  Scores of the
 // chosen are gathered and their gradients scattered in LDS, not by comparing every id with every expert (with that and
 // exponentials of more instructions 75).
 template <int TYPE, int SCORE, int L, int V, bool VEC, int KV>

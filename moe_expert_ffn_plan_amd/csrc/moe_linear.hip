@@ -102,9 +102,9 @@ __device__ __forceinline__ void store2(const Args& a, int row, int col, float v0
 // line each, and a request for half a line takes as long as one for a line (16384 x 7168 x 4096 E2M1: 237 us, 243 by one).
 //
 // Workgroups stay: each takes a run of tiles, whose outputs go through LDS to whole lines while the next tile's first stages
-// load (237 us to 214).  Bound: 16384 x 7168 x 4096 E2M1 takes 205-216 us, 4500-4700 TFLOP/s of the 6960 that the
-// instructions reach from registers, with the matrix cores busy 69% of the time at the clock that the load leaves; without
-// DMA 190-200, without products 170-200.  E4M3 takes 312-334 (2900-3100 of 4310).  256 x 256 tiles, 64 x 128 to a wave,
+// load (237 us to 214).  Bound: 16384 x 7168 x 4096 E2M1 takes 205-224 us, 4300-4700 TFLOP/s of the 6960 that the
+// instructions reach from registers, with the matrix cores busy 70% of the time at the clock that the load leaves; without
+// DMA 190-200, without products 170-200.  E4M3 takes 312-346 (2800-3100 of 4310).  256 x 256 tiles, 64 x 128 to a wave,
 // read least LDS for a product; 128 x 256 tiles, two to a CU, take 258, four waves 273.  128 x 128 tiles, two to a CU, fill
 // the card where rows are fewer (2047 x 4064 x 1537 E4M3: 22 us to 32).
 template <int FMT, int BM, int BN, int WM, int WN, int AK, int NS_>
@@ -508,8 +508,8 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void tile_kernel(Args g) {
 // waves read the same ones, so LDS would only be a detour).  x goes through LDS, where each wave has a place of its own and
 // needs no barrier: lanes that load neighbouring chunks of few rows touch few lines, lanes that load what they multiply
 // touch one each.  The waves' sums are added through LDS, in the waves' order.
-// Bound by the launch and by the weights' latency: 1 x 7168 x 4096 E4M3 takes 4.9 us, 32 rows 6.3 to 7.3, 64 8.7, 128 (two
-// groups, E2M1) 8.9; the same in tiles 11.8 to 14.8.
+// Bound by the launch and by the weights' latency: 1 x 7168 x 4096 E4M3 takes 4.9 us, 32 rows 6.3 to 7.3, 64 8.7 to 9.2, 128 (two
+// groups, E2M1) 8.9 to 9.7; the same in tiles 11.8 to 14.8.
 template <int FMT, int ROWS, int W, int U>
 struct Few {
     static constexpr int RB = FMT == MOE_E2M1 ? 64 : 128, BYTES = U * RB, CHUNKS = BYTES / 16;  // of a row in a turn
@@ -689,7 +689,7 @@ constexpr int kMostSplits = 16, kLeastSteps = 4;
 static size_t laid_out_bytes(int M, int KT) { return ((size_t)M + 63) / 64 * KT * 256; }  // of x's scales by K-step
 
 // The kernel with the least estimated time, in microseconds (measured at 2048 .. 16384 rows, 2016 .. 7168 columns and 512
-// .. 7168 outputs, most within 15%): a K-step of a 256 x 256 tile takes 0.8 (E2M1) or 1.3 (E4M3), one of a 128 x 128 tile
+// .. 7168 outputs, most within 15%, and taken from 65 rows up for any size): a K-step of a 256 x 256 tile takes 0.8 (E2M1) or 1.3 (E4M3), one of a 128 x 128 tile
 // 0.27 or 0.4, or 0.36 or 0.42 for each of two that share a compute unit; to lay out the scales takes 4, to join splits 4 and their
 // partial sums' way to memory and back.
 MxLinearChoice choose_mx_linear(int M, int N, int K, int format) {
